@@ -94,9 +94,17 @@ typedef enum qw_wfmt {
 typedef enum qw_afmt {
   QW_A_BF16 = 0,           /* BF16 [rows][K]                                          */
   QW_A_MXFP8_G32 = 1,      /* E4M3 codes [rows][K] + E8M0 scales [rows][K/32]          */
-  QW_A_NVFP4_G16 = 2       /* E2M1 codes [rows][K/2] (even k in the low nibble) +
+  QW_A_NVFP4_G16 = 2,      /* E2M1 codes [rows][K/2] (even k in the low nibble) +
                               unsigned E4M3 scales [rows][K/16]                            */
+  QW_A_INT8_TOKEN = 3      /* INT8 codes [rows][lda] + one FP32 scale per row (qgemm_int8) */
 } qw_afmt;
+
+/* Element types of the calls that take more than one. */
+typedef enum qw_dtype {
+  QW_T_BF16 = 0,
+  QW_T_F32 = 1,
+  QW_T_F16 = 2
+} qw_dtype;
 
 /* Description of one repacked weight set (E experts; E = 1 for a dense layer).
  * Filled by qw_repack_query; treat as read-only. */
@@ -391,6 +399,75 @@ qw_status qgemm_moe_grouped_indexed(const qw_packed_desc* desc, const void* w_pa
                                     int64_t total_rows, const void* bias, void* C,
                                     void* workspace, uint64_t ws_bytes, int32_t* d_err,
                                     void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * INT8 products: codes of 8 bits on both sides, an FP32 scale per token (activation row) and
+ * per output channel (weight row).  Weights are taken as checkpoints hold them: INT8 codes
+ * [N][K], contiguous, any value -128 .. 127, and FP32 scales [N]; nothing is repacked.
+ *
+ * qw_quantize_int8 - BF16 rows -> INT8 codes and a scale per row:
+ *   A_scale[r] = amax_r / 127,  A_q[r][k] = rint(A[r][k] * min(127 / amax_r, FLT_MAX))
+ *   with amax_r the row's largest magnitude; FP32 arithmetic, ties to even (a row of zeros
+ *   has scale 0).  A: BF16, row pitch lda >= K elements; A_q: INT8 [rows][K]; A_scale: FP32
+ *   [rows].  1 <= K, K % 16 == 0 (else QW_ERR_UNSUPPORTED); A and A_q 16-byte aligned, lda a
+ *   multiple of 8.  A row with a non-finite value sets QW_ERR_VALUE in d_err, gets the scale
+ *   NaN and codes 0 (a product with it is NaN, not a plausible number).
+ */
+qw_status qw_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, void* A_q,
+                           float* A_scale, int32_t* d_err, void* stream);
+
+/* qgemm_int8 - C[m][n] = a_scale[m] * w_scale[n] * sum_k A_q[m][k] * W[n][k] + bias[n].
+ *   afmt QW_A_INT8_TOKEN: A holds the codes (INT8, row pitch lda >= K) and a_scale their FP32
+ *        scales [M].
+ *   afmt QW_A_BF16: A is BF16 (row pitch lda >= K elements), quantised per token inside the
+ *        call exactly as qw_quantize_int8 does; a_scale must be NULL.
+ *   bias: BF16 [N] or NULL.  c_type QW_T_BF16 or QW_T_F32 (logits); C: row pitch ldc >= N
+ *   elements.  Sums of products are exact below 2^24 and rounded to FP32 above.
+ * K % 16 == 0 and K <= 131056 (else QW_ERR_UNSUPPORTED); M >= 0 (0 is a no-op), M < 2^31.
+ * Alignment: A and W 16 bytes, the pitch of A a multiple of 16 bytes, scales 4, bias 2, C its
+ * element size, workspace 256.  Workspace: qgemm_int8_workspace_size bytes for up to max_rows
+ * rows (any content; the quantised activations live there during the call; calls that share
+ * one must not overlap).  Values of a row whose scale is NaN are NaN.
+ */
+qw_status qgemm_int8_workspace_size(int32_t afmt, int64_t max_rows, int32_t N, int32_t K,
+                                    uint64_t* bytes);
+qw_status qgemm_int8(int32_t afmt, const void* A, int64_t lda, const float* a_scale,
+                     const void* W, const float* w_scale, const void* bias, int32_t c_type,
+                     void* C, int64_t ldc, int64_t M, int32_t N, int32_t K, void* workspace,
+                     uint64_t ws_bytes, int32_t* d_err, void* stream);
+
+/* qgemm_int8_gated - the gate and up projections of a gated feed-forward block with the
+ *   activation and the product, in one kernel:
+ *     g = product with rows 0 .. I-1 of W, u = product with rows I .. 2I-1 (bias included),
+ *     Y[m][i] = bf16( g / (1 + e^-g) * u ), FP32 until that rounding.
+ *   W: INT8 [2I][K], w_scale FP32 [2I], bias BF16 [2I] or NULL; Y: BF16, row pitch ldy >= I;
+ *   the rest as qgemm_int8 (workspace: qgemm_int8_workspace_size with N = 2I).  I < 2^30.
+ */
+qw_status qgemm_int8_gated(int32_t afmt, const void* A, int64_t lda, const float* a_scale,
+                           const void* W, const float* w_scale, const void* bias, void* Y,
+                           int64_t ldy, int64_t M, int32_t I, int32_t K, void* workspace,
+                           uint64_t ws_bytes, int32_t* d_err, void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * qw_logprobs - what is answered with once the LM head has made logits [T][V] (row pitch
+ * ld >= V elements; l_type QW_T_BF16, QW_T_F16 or QW_T_F32), of p = softmax(row):
+ *   token_logprobs [T] = log p[tokens[t]]; token_ranks [T] (int32) = 1 + the number of ids
+ *     before it in the order of the alternatives (larger logit first, equal logits by the
+ *     lower id); tokens int32 [T];
+ *   entropy [T] = -sum p log p (natural logarithm);
+ *   top_ids (int32) and top_logprobs [T][topk]: the first topk ids in that order.
+ * Outputs are FP32 unless stated; any of them may be NULL (topk = 0 for no alternatives;
+ * tokens may be NULL when token_logprobs and token_ranks are).  0 <= topk <= 32, topk <= V;
+ * T <= 2^26.  A logit of -inf is a masked id: probability 0, log probability -inf, nothing in the entropy.
+ * A row whose every logit is -inf has log probabilities -inf and entropy 0.  A NaN or +inf
+ * logit sets QW_ERR_VALUE in d_err and makes its row's FP32 outputs NaN; a token outside
+ * [0, V) sets QW_ERR_INVALID_ARG and gets NaN and rank 0.  logits aligned to their element
+ * size, the others to 4 bytes.  No workspace; T * ld may pass 2^31 elements.
+ */
+qw_status qw_logprobs(int32_t l_type, const void* logits, int64_t ld, int64_t T, int32_t V,
+                      const int32_t* tokens, int32_t topk, float* token_logprobs,
+                      int32_t* token_ranks, float* entropy, int32_t* top_ids,
+                      float* top_logprobs, int32_t* d_err, void* stream);
 
 /* --------------------------------------------------------------------------------------
  * qw_read_error - synchronise `stream`, copy *d_err to the host (`host_code`, host

@@ -429,6 +429,114 @@ qw_status qgemm_moe_grouped_indexed(const qw_packed_desc* desc, const void* w_pa
                           ws_bytes, d_err, static_cast<cudaStream_t>(stream));
 }
 
+qw_status qw_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, void* A_q,
+                           float* A_scale, int32_t* d_err, void* stream) {
+  if (rows < 0 || K < 1 || lda < K) return QW_ERR_INVALID_ARG;
+  if (K % 16 || rows > 0x7FFFFFFFLL) return QW_ERR_UNSUPPORTED;
+  if (rows == 0) return QW_OK;
+  if (!A || !A_q || !A_scale) return QW_ERR_INVALID_ARG;
+  if (!aligned(A, 16) || lda % 8 || !aligned(A_q, 16) || !aligned(A_scale, 4))
+    return QW_ERR_ALIGNMENT;
+  return launch_quantize_int8(A, lda, rows, K, A_q, A_scale, d_err,
+                              static_cast<cudaStream_t>(stream));
+}
+
+// The workspace of an INT8 product: codes of the quantised activations, then their scales.
+static uint64_t int8_code_bytes(int64_t M, int32_t K) {
+  return (uint64_t)round_up(M * (int64_t)K, 256);
+}
+
+qw_status qgemm_int8_workspace_size(int32_t afmt, int64_t max_rows, int32_t N, int32_t K,
+                                    uint64_t* bytes) {
+  if (!bytes || max_rows < 0 || max_rows > 0x7FFFFFFFLL || N < 1 || K < 1)
+    return QW_ERR_INVALID_ARG;
+  if (afmt != QW_A_BF16 && afmt != QW_A_INT8_TOKEN) return QW_ERR_UNSUPPORTED;
+  if (K % 16 || K > kInt8MaxK) return QW_ERR_UNSUPPORTED;
+  *bytes = afmt == QW_A_BF16 ? int8_code_bytes(max_rows, K) + (uint64_t)max_rows * 4 : 0;
+  return QW_OK;
+}
+
+static qw_status int8_product(int32_t afmt, const void* A, int64_t lda, const float* a_scale,
+                              const void* W, const float* w_scale, const void* bias, int32_t c_type,
+                              void* C, int64_t ldc, int64_t M, int32_t N, int32_t K, bool gated,
+                              void* workspace, uint64_t ws_bytes, int32_t* d_err, void* stream) {
+  uint64_t need = 0;
+  qw_status s = qgemm_int8_workspace_size(afmt, M, N, K, &need);
+  if (s != QW_OK) return s;
+  if (c_type != QW_T_BF16 && c_type != QW_T_F32) return QW_ERR_UNSUPPORTED;
+  const bool quantise = afmt == QW_A_BF16;
+  if (lda < K || ldc < (gated ? N / 2 : N)) return QW_ERR_INVALID_ARG;
+  if (quantise != (a_scale == nullptr) && M > 0) return QW_ERR_INVALID_ARG;
+  if (M == 0) return QW_OK;
+  if (!A || !W || !w_scale || !C) return QW_ERR_INVALID_ARG;
+  if (!aligned(A, 16) || lda % (quantise ? 8 : 16) || !aligned(W, 16) || !aligned(w_scale, 4) ||
+      !aligned(a_scale, 4) || (bias && !aligned(bias, 2)) ||
+      !aligned(C, c_type == QW_T_F32 ? 4 : 2))
+    return QW_ERR_ALIGNMENT;
+  if (need > 0 && (!workspace || ws_bytes < need)) return QW_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 256)) return QW_ERR_ALIGNMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Int8Problem p{};
+  p.A = static_cast<const int8_t*>(A);
+  p.lda = lda;
+  p.a_scale = a_scale;
+  p.W = static_cast<const int8_t*>(W);
+  p.w_scale = w_scale;
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.C = C;
+  p.ldc = ldc;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.c_f32 = c_type == QW_T_F32;
+  if (quantise) {
+    int8_t* codes = static_cast<int8_t*>(workspace);
+    float* scales = reinterpret_cast<float*>(codes + int8_code_bytes(M, K));
+    s = launch_quantize_int8(A, lda, M, K, codes, scales, d_err, st);
+    if (s != QW_OK) return s;
+    p.A = codes;
+    p.lda = K;
+    p.a_scale = scales;
+  }
+  return launch_gemm_int8(p, gated, d_err, st);
+}
+
+qw_status qgemm_int8(int32_t afmt, const void* A, int64_t lda, const float* a_scale,
+                     const void* W, const float* w_scale, const void* bias, int32_t c_type,
+                     void* C, int64_t ldc, int64_t M, int32_t N, int32_t K, void* workspace,
+                     uint64_t ws_bytes, int32_t* d_err, void* stream) {
+  return int8_product(afmt, A, lda, a_scale, W, w_scale, bias, c_type, C, ldc, M, N, K, false,
+                      workspace, ws_bytes, d_err, stream);
+}
+
+qw_status qgemm_int8_gated(int32_t afmt, const void* A, int64_t lda, const float* a_scale,
+                           const void* W, const float* w_scale, const void* bias, void* Y,
+                           int64_t ldy, int64_t M, int32_t I, int32_t K, void* workspace,
+                           uint64_t ws_bytes, int32_t* d_err, void* stream) {
+  if (I < 1 || I >= (1 << 30)) return QW_ERR_INVALID_ARG;
+  return int8_product(afmt, A, lda, a_scale, W, w_scale, bias, QW_T_BF16, Y, ldy, M, 2 * I, K,
+                      true, workspace, ws_bytes, d_err, stream);
+}
+
+qw_status qw_logprobs(int32_t l_type, const void* logits, int64_t ld, int64_t T, int32_t V,
+                      const int32_t* tokens, int32_t topk, float* token_logprobs,
+                      int32_t* token_ranks, float* entropy, int32_t* top_ids,
+                      float* top_logprobs, int32_t* d_err, void* stream) {
+  if (l_type != QW_T_BF16 && l_type != QW_T_F16 && l_type != QW_T_F32) return QW_ERR_UNSUPPORTED;
+  if (T < 0 || T > kLogprobsMaxRows || V < 1 || ld < V) return QW_ERR_INVALID_ARG;
+  if (topk < 0 || topk > kLogprobsMaxTop || topk > V) return QW_ERR_INVALID_ARG;
+  if (T == 0) return QW_OK;
+  if (!logits || (!tokens && (token_logprobs || token_ranks))) return QW_ERR_INVALID_ARG;
+  if (topk > 0 && (!top_ids || !top_logprobs)) return QW_ERR_INVALID_ARG;
+  if (!aligned(logits, l_type == QW_T_F32 ? 4 : 2) || !aligned(tokens, 4) ||
+      !aligned(token_logprobs, 4) || !aligned(token_ranks, 4) || !aligned(entropy, 4) ||
+      !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+    return QW_ERR_ALIGNMENT;
+  const LogprobsArgs a{logits,  ld,   V,       tokens,       token_logprobs, token_ranks,
+                       entropy, topk, top_ids, top_logprobs, d_err};
+  return launch_logprobs(a, l_type, T, static_cast<cudaStream_t>(stream));
+}
+
 qw_status qw_read_error(const int32_t* d_err, void* stream, int32_t* host_code) {
   if (!d_err || !host_code) return QW_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return QW_ERR_CUDA;

@@ -105,6 +105,44 @@ qw_status launch_gemv_w4a8(const qw_packed_desc& d, const void* w_packed, const 
                            const void* A, const void* A_sf, const void* bias, const float* scale2,
                            void* C, int M, int32_t* err, cudaStream_t st);
 
+// INT8 product and its gated form (int8.cu): INT8 codes and FP32 scales on both sides.
+struct Int8Problem {
+  const int8_t* A;       // [M][lda] codes
+  int64_t lda;
+  const float* a_scale;  // [M]
+  const int8_t* W;       // [N][K] codes (gated: N = 2 I, gate rows first)
+  const float* w_scale;  // [N]
+  const uint16_t* bias;  // BF16 [N] or null
+  void* C;               // BF16 or FP32 [M][ldc]
+  int64_t ldc;
+  int64_t M;
+  int32_t N, K;
+  bool c_f32;
+};
+// largest K whose 32-bit integer sums cannot overflow (128 * 128 * K < 2^31), K % 16 == 0
+constexpr int32_t kInt8MaxK = 131056;
+qw_status launch_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, void* Q,
+                               float* scale, int32_t* err, cudaStream_t st);
+qw_status launch_gemm_int8(const Int8Problem& p, bool gated, int32_t* err, cudaStream_t st);
+
+// Log probabilities (logprobs.cu); null outputs are not computed.
+struct LogprobsArgs {
+  const void* logits;
+  int64_t ld;
+  int32_t V;
+  const int32_t* tokens;
+  float* token_logprob;
+  int32_t* token_rank;
+  float* entropy;
+  int32_t topk;
+  int32_t* top_ids;
+  float* top_logprobs;
+  int32_t* err;
+};
+constexpr int32_t kLogprobsMaxTop = 32;
+constexpr int64_t kLogprobsMaxRows = (int64_t)1 << 26;  // rows of one call (grid size)
+qw_status launch_logprobs(const LogprobsArgs& a, int32_t type, int64_t T, cudaStream_t st);
+
 // MoE scheduling.
 qw_status launch_moe_route(const float* logits, int32_t T, int32_t E, int32_t topk,
                            int32_t* topk_ids, int32_t* sorted_pairs, int32_t* offsets, void* ws,

@@ -38,6 +38,10 @@ QW_W_SCALE2 = 0x100  # flag: second-level FP32 scale per output channel (and exp
 QW_A_BF16 = 0
 QW_A_MXFP8_G32 = 1
 QW_A_NVFP4_G16 = 2
+QW_A_INT8_TOKEN = 3
+QW_T_BF16 = 0
+QW_T_F32 = 1
+QW_T_F16 = 2
 
 EXPORTS = (
     "qw_status_str", "qw_version", "qw_repack_query", "qw_repack", "qw_unpack",
@@ -48,6 +52,8 @@ EXPORTS = (
     "qgemm_moe_route_noalloc", "qw_quantize_mxfp8", "qw_silu_mul",
     "qgemm_moe_combine_workspace_size", "qgemm_moe_combine", "qw_stream_read",
     "qw_mma_rate_probe",
+    "qw_quantize_int8", "qgemm_int8_workspace_size", "qgemm_int8", "qgemm_int8_gated",
+    "qw_logprobs",
 )
 
 
@@ -98,6 +104,13 @@ _SIGS = {
     "qgemm_moe_combine": (_I32, [_P, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _U64, _P, _P]),
     "qw_stream_read": (_I32, [_P, _U64, _P, _I32, _P]),
     "qw_mma_rate_probe": (_I32, [_I32, _I32, _I32, _P, _P, _P]),
+    "qw_quantize_int8": (_I32, [_P, _I64, _I64, _I32, _P, _P, _P, _P]),
+    "qgemm_int8_workspace_size": (_I32, [_I32, _I64, _I32, _I32, ctypes.POINTER(_U64)]),
+    "qgemm_int8": (_I32, [_I32, _P, _I64, _P, _P, _P, _P, _I32, _P, _I64, _I64, _I32, _I32, _P,
+                          _U64, _P, _P]),
+    "qgemm_int8_gated": (_I32, [_I32, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _P,
+                                _U64, _P, _P]),
+    "qw_logprobs": (_I32, [_I32, _P, _I64, _I64, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 
@@ -265,6 +278,46 @@ def qgemm_moe_combine(Y, sorted_pairs, topk_ids, logits, T, E, topk, N, out, wor
     _check("qgemm_moe_combine", LIB.qgemm_moe_combine(
         _ptr(Y), _ptr(sorted_pairs), _ptr(topk_ids), _ptr(logits), T, E, topk, N, _ptr(out),
         _ptr(workspace), ws_bytes, _ptr(d_err), _stream(stream)))
+
+
+def qw_quantize_int8(A, lda, rows, K, A_q, A_scale, d_err=None, stream=None):
+    """BF16 rows (row pitch ``lda`` elements) -> INT8 codes [rows][K] and FP32 scales [rows]."""
+    _check("qw_quantize_int8", LIB.qw_quantize_int8(
+        _ptr(A), lda, rows, K, _ptr(A_q), _ptr(A_scale), _ptr(d_err), _stream(stream)))
+
+
+def qgemm_int8_workspace_size(afmt: int, max_rows: int, N: int, K: int) -> int:
+    n = _U64(0)
+    _check("qgemm_int8_workspace_size",
+           LIB.qgemm_int8_workspace_size(afmt, max_rows, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def qgemm_int8(afmt, A, lda, a_scale, W, w_scale, bias, c_type, C, ldc, M, N, K, workspace=None,
+               ws_bytes=0, d_err=None, stream=None):
+    """C = a_scale * w_scale * (A_q W^T) + bias: INT8 codes W [N][K] with a scale per channel,
+    activations as INT8 codes with a scale per token or BF16 (quantised in the call)."""
+    _check("qgemm_int8", LIB.qgemm_int8(
+        afmt, _ptr(A), lda, _ptr(a_scale), _ptr(W), _ptr(w_scale), _ptr(bias), c_type, _ptr(C),
+        ldc, M, N, K, _ptr(workspace), ws_bytes, _ptr(d_err), _stream(stream)))
+
+
+def qgemm_int8_gated(afmt, A, lda, a_scale, W, w_scale, bias, Y, ldy, M, I, K, workspace=None,
+                     ws_bytes=0, d_err=None, stream=None):
+    """Y = silu(gate) * up of a gated feed-forward block; W [2I][K], gate rows first."""
+    _check("qgemm_int8_gated", LIB.qgemm_int8_gated(
+        afmt, _ptr(A), lda, _ptr(a_scale), _ptr(W), _ptr(w_scale), _ptr(bias), _ptr(Y), ldy, M, I,
+        K, _ptr(workspace), ws_bytes, _ptr(d_err), _stream(stream)))
+
+
+def qw_logprobs(l_type, logits, ld, T, V, tokens, topk, token_logprobs, token_ranks, entropy,
+                top_ids, top_logprobs, d_err=None, stream=None):
+    """Log probability and rank of each row's token, entropy and top alternatives; any output
+    may be None."""
+    _check("qw_logprobs", LIB.qw_logprobs(
+        l_type, _ptr(logits), ld, T, V, _ptr(tokens), topk, _ptr(token_logprobs),
+        _ptr(token_ranks), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), _ptr(d_err),
+        _stream(stream)))
 
 
 def qw_read_error(d_err, stream=None) -> int:
