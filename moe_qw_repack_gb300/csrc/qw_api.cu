@@ -437,13 +437,14 @@ qw_status qw_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, 
   if (!A || !A_q || !A_scale) return QW_ERR_INVALID_ARG;
   if (!aligned(A, 16) || lda % 8 || !aligned(A_q, 16) || !aligned(A_scale, 4))
     return QW_ERR_ALIGNMENT;
-  return launch_quantize_int8(A, lda, rows, K, A_q, A_scale, d_err,
+  return launch_quantize_int8(A, lda, rows, K, A_q, A_scale, false, d_err,
                               static_cast<cudaStream_t>(stream));
 }
 
-// The workspace of an INT8 product: codes of the quantised activations, then their scales.
+// The workspace of an INT8 product: the activations' codes as its kernel takes them (INT8 for
+// the GEMV, FP16 for the tensor cores), then the scales of rows quantised in the call.
 static uint64_t int8_code_bytes(int64_t M, int32_t K) {
-  return (uint64_t)round_up(M * (int64_t)K, 256);
+  return (uint64_t)round_up(M * (int64_t)K * (M > kInt8GemvRows ? 2 : 1), 256);
 }
 
 qw_status qgemm_int8_workspace_size(int32_t afmt, int64_t max_rows, int32_t N, int32_t K,
@@ -452,7 +453,10 @@ qw_status qgemm_int8_workspace_size(int32_t afmt, int64_t max_rows, int32_t N, i
     return QW_ERR_INVALID_ARG;
   if (afmt != QW_A_BF16 && afmt != QW_A_INT8_TOKEN) return QW_ERR_UNSUPPORTED;
   if (K % 16 || K > kInt8MaxK) return QW_ERR_UNSUPPORTED;
-  *bytes = afmt == QW_A_BF16 ? int8_code_bytes(max_rows, K) + (uint64_t)max_rows * 4 : 0;
+  if (afmt == QW_A_BF16)
+    *bytes = int8_code_bytes(max_rows, K) + (uint64_t)max_rows * 4;
+  else
+    *bytes = max_rows > kInt8GemvRows ? int8_code_bytes(max_rows, K) : 0;
   return QW_OK;
 }
 
@@ -489,16 +493,19 @@ static qw_status int8_product(int32_t afmt, const void* A, int64_t lda, const fl
   p.N = N;
   p.K = K;
   p.c_f32 = c_type == QW_T_F32;
+  const bool tensor = M > kInt8GemvRows;
   if (quantise) {
-    int8_t* codes = static_cast<int8_t*>(workspace);
-    float* scales = reinterpret_cast<float*>(codes + int8_code_bytes(M, K));
-    s = launch_quantize_int8(A, lda, M, K, codes, scales, d_err, st);
-    if (s != QW_OK) return s;
-    p.A = codes;
+    float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + int8_code_bytes(M, K));
+    s = launch_quantize_int8(A, lda, M, K, workspace, scales, tensor, d_err, st);
+    p.A = static_cast<const int8_t*>(workspace);
     p.lda = K;
     p.a_scale = scales;
+  } else if (tensor) {
+    s = launch_widen_int8(A, lda, M, K, workspace, st);
   }
-  return launch_gemm_int8(p, gated, d_err, st);
+  if (s != QW_OK) return s;
+  return tensor ? launch_gemm_int8_tc(p, workspace, gated, d_err, st)
+                : launch_gemv_int8(p, gated, d_err, st);
 }
 
 qw_status qgemm_int8(int32_t afmt, const void* A, int64_t lda, const float* a_scale,

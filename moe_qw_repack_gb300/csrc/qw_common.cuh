@@ -8,6 +8,7 @@
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cstdint>
 
 #include "../../include/qw.h"
@@ -329,6 +330,21 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
   const float hi = __half2float(__ushort_as_half((unsigned short)(h >> 16)));
   __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&b);
+}
+
+// Four INT8 codes -> two FP16 pairs, exactly: byte b of code + 128 dropped into the mantissa of
+// 1024 is the FP16 number 1024 + b.
+__device__ __forceinline__ void int8x4_to_f16x2(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  x ^= 0x80808080u;  // code + 128, unsigned
+  const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140);  // 1024 + byte
+  const uint32_t b = __byte_perm(x, 0x64646464u, 0x4342);
+  const uint32_t off = 0x64806480u;  // 1024 + 128
+  const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&a),
+                             *reinterpret_cast<const __half2*>(&off));
+  const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&b),
+                             *reinterpret_cast<const __half2*>(&off));
+  lo = *reinterpret_cast<const uint32_t*>(&ra);
+  hi = *reinterpret_cast<const uint32_t*>(&rb);
 }
 
 // INT1 sign codes: bits p and 16 + p of `w` (bit b = weight 2b - 1) -> the pair (+-1, +-1)
