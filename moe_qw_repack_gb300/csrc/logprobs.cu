@@ -1,5 +1,24 @@
 // logprobs.cu - what a server answers with once it has logits: the log probability and rank of
-// a given token, the entropy and the top alternatives of each row.
+// a given token, the entropy and the top alternatives of each row, in one pass over the row.
+//
+// Mathematics.  In base 2, with y = x log2(e) - r for a running reference r (the largest x so far
+// times log2(e), rounded): s = sum 2^y and t = sum 2^y y.  A new reference r' rescales
+// t <- 2^(r-r') (t + s (r - r')), s <- 2^(r-r') s, which also merges the partial sums of threads,
+// warps and CTAs.  Then log p(x) = ln2 (x log2(e) - r - log2 s) and the entropy is
+// ln2 (log2 s - t / s): r's own rounding cancels, so rows of large logits lose nothing.
+//
+// Alternatives: ids are ordered by a 64-bit key (the value's bits as an ordered integer above the
+// complement of the id), so ties need no second pass.  Each CTA keeps a lower bound `thr` of its
+// topk-th key; a vector whose maximum is below it costs one comparison, what passes goes to a
+// shared buffer, and when that fills up it is cut back to the topk largest and thr rises to the
+// last of them.  The first bound is the smallest of 32 group maxima of the first block (32
+// different elements are at least that).  If one block overflows the buffer (ascending rows),
+// the bound still rises by what the buffer holds, and the block is offered again from registers.
+//
+// Bound: the row is read once (HBM); the work per logit is one exponential and about seven
+// instructions.  A CTA of 256 threads takes a row, each thread four 16-byte vectors at a time
+// with the next four in flight; few long rows are split over the CTAs of a cluster, whose
+// rank 0 merges the partial results through distributed shared memory in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -9,103 +28,588 @@
 namespace qw {
 namespace {
 
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int RV = 4;               // vectors of a thread per block
+constexpr int CAP = 512;            // candidate buffer
+constexpr int CUT = 128;            // candidates from which the buffer is cut back
+constexpr int MAX_CLUSTER = 8;
+constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
+
+// Per element type: values per 16-byte vector; `LOW`: sums skip vectors whose maximum is not
+// above it (next to anything larger they are zero; rows that have nothing larger are summed
+// by slow_row); `FLOOR`: what -inf is replaced with inside a vector, far enough below LOW to
+// stay zero and finite, so that 0 * y never is 0 * inf.
 template <int TYPE>
-__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-  if constexpr (TYPE == QW_T_F32) return static_cast<const float*>(p)[i];
-  if constexpr (TYPE == QW_T_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+struct El;
+template <>
+struct El<QW_T_F32> {
+  static constexpr int VE = 4;
+  static constexpr float LOW = -1e30f;
+  static __device__ __forceinline__ float load(const void* p, int64_t i) {
+    return __ldg(static_cast<const float*>(p) + i);
+  }
+  static __device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ void unpack_floored(const uint4& v, float (&x)[4]) {
+    unpack(v, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = fmaxf(x[i], LOW);
+  }
+  // how many of the vector's values are above t (or equal, with `equal`)
+  static __device__ __forceinline__ int above(const uint4& v, float t, bool equal) {
+    float x[4];
+    unpack(v, x);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += equal ? x[i] >= t : x[i] > t;
+    return n;
+  }
+};
+
+__device__ __forceinline__ uint32_t as_u32(const __nv_bfloat162& h) {
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t as_u32(const __half2& h) {
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// the two 16-bit types: H2 their packed pair
+template <class H2>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat162> {
+  static __device__ __forceinline__ __nv_bfloat162 splat(float x) { return __float2bfloat162_rn(x); }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+};
+template <>
+struct Pair<__half2> {
+  static __device__ __forceinline__ __half2 splat(float x) { return __float2half2_rn(x); }
+  static __device__ __forceinline__ float lo(uint32_t w) {
+    return __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
+  }
+  static __device__ __forceinline__ float hi(uint32_t w) {
+    return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+  }
+};
+
+template <class H2>
+struct El16 {
+  static constexpr int VE = 8;
+  static __device__ __forceinline__ H2 pair(uint32_t w) { return *reinterpret_cast<const H2*>(&w); }
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    const uint32_t m = as_u32(__hmax2_nan(__hmax2_nan(pair(v.x), pair(v.y)),
+                                          __hmax2_nan(pair(v.z), pair(v.w))));
+    return El<QW_T_F32>::max_nan(Pair<H2>::lo(m), Pair<H2>::hi(m));
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = Pair<H2>::lo(w[i]);
+      x[2 * i + 1] = Pair<H2>::hi(w[i]);
+    }
+  }
+  static __device__ __forceinline__ void unpack_floored(const uint4& v, float floor, float (&x)[8]) {
+    const H2 f = Pair<H2>::splat(floor);
+    unpack(make_uint4(as_u32(__hmax2(pair(v.x), f)), as_u32(__hmax2(pair(v.y), f)),
+                      as_u32(__hmax2(pair(v.z), f)), as_u32(__hmax2(pair(v.w), f))),
+           x);
+  }
+  static __device__ __forceinline__ int above(const uint4& v, float t, bool equal) {
+    const H2 tt = Pair<H2>::splat(t);  // t is a value of the type: exact
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t ones = 0;  // 1.0 or 0.0 in each half, summed
+    H2 sum = *reinterpret_cast<H2*>(&ones);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = __hadd2(sum, equal ? __hge2(pair(w[i]), tt) : __hgt2(pair(w[i]), tt));
+    const uint32_t s = as_u32(sum);
+    return (int)(Pair<H2>::lo(s) + Pair<H2>::hi(s));
+  }
+};
+template <>
+struct El<QW_T_BF16> : El16<__nv_bfloat162> {
+  static constexpr float LOW = -1e30f;
+  static __device__ __forceinline__ float load(const void* p, int64_t i) {
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  }
+  static __device__ __forceinline__ void unpack_floored(const uint4& v, float (&x)[8]) {
+    El16<__nv_bfloat162>::unpack_floored(v, LOW, x);
+  }
+};
+template <>
+struct El<QW_T_F16> : El16<__half2> {
+  static constexpr float LOW = -60000.f;  // FP16 values next to it are 32 apart
+  static __device__ __forceinline__ float load(const void* p, int64_t i) {
+    return __half2float(static_cast<const __half*>(p)[i]);
+  }
+  static __device__ __forceinline__ void unpack_floored(const uint4& v, float (&x)[8]) {
+    El16<__half2>::unpack_floored(v, -65504.f, x);
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Order of the alternatives as one integer: larger value first, equal values by the lower id.
-__device__ __forceinline__ uint64_t order_key(float x, int32_t id) {
+__device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);  // -0 and 0 are equal
-  const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((uint64_t)o << 32) | (0xFFFFFFFFu - (uint32_t)id);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(float x, int32_t id) {
+  return ((uint64_t)order_of(x) << 32) | (0xFFFFFFFFu - (uint32_t)id);
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+  const uint32_t o = (uint32_t)(key >> 32);
+  return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
 }
 
-template <class T, class F>
-__device__ T block_reduce(T v, F f, T* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = sh[0];
-  for (unsigned i = 1; i < blockDim.x / 32; ++i) v = f(v, sh[i]);
+__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t v, int o) {
+  return __shfl_xor_sync(0xFFFFFFFFu, (unsigned long long)v, o);
+}
+
+// Partial result of some of a row's logits.
+struct Part {
+  float rmax;  // largest logit
+  float r, s, t;
+  int32_t above;
+  int32_t bad;
+  int32_t n;  // entries of the sorted list
+};
+__device__ __forceinline__ void merge(float& r, float& s, float& t, float r2, float s2, float t2) {
+  const float m = fmaxf(r, r2);
+  const float f = ex2(r - m), f2 = ex2(r2 - m);
+  t = f * (t + s * (r - m)) + f2 * (t2 + s2 * (r2 - m));
+  s = f * s + f2 * s2;
+  r = m;
+}
+
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 
+// One block of a CTA's vectors, in shared memory.
+constexpr int BLOCK = THREADS * RV;
+constexpr int STAGES = 3;
+constexpr size_t RING_BYTES = (size_t)STAGES * BLOCK * 16;
+// a reference is kept until a logit passes it by more than this (2^12 x 2^31 terms stay finite,
+// and the entropy, a difference of two numbers of that many bits, loses four of its own)
+constexpr float HEADROOM = 8.f;
+
 template <int TYPE>
-__global__ void __launch_bounds__(512) logprobs_kernel(const LogprobsArgs a) {
-  __shared__ float shf[32];
-  __shared__ unsigned long long shk[32];
-  const int64_t row = blockIdx.x;
+__global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs a, const int csize) {
+  using E = El<TYPE>;
+  constexpr int VE = E::VE;
+  constexpr int ES = 16 / VE;
+  extern __shared__ __align__(128) uint4 ring[];  // [STAGES][BLOCK]
+  __shared__ uint64_t buf[CAP];
+  __shared__ uint64_t sorted[kLogprobsMaxTop];
+  __shared__ int cnt;
+  __shared__ uint64_t group[32];
+  __shared__ Part wpart[WARPS];
+  __shared__ Part part;  // this CTA's result; on rank 0, at the end, the row's
+  __shared__ uint64_t full[STAGES];
+  __shared__ int abort_flag;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    cnt = 0;
+    abort_flag = 0;
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+    fence_barrier_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  const int64_t row = blockIdx.x / csize;
+  const int rank = blockIdx.x % csize;
   const int64_t off = row * a.ld;
-  auto maxf = [](float x, float y) { return fmaxf(x, y); };
-  auto addf = [](float x, float y) { return x + y; };
-  float m = -INFINITY;
-  bool bad = false;
-  for (int32_t i = threadIdx.x; i < a.V; i += blockDim.x) {
-    const float x = load_logit<TYPE>(a.logits, off + i);
-    bad = bad || !(x < INFINITY);
-    m = fmaxf(m, x);
-  }
-  bad = __syncthreads_or(bad);
-  m = block_reduce(m, maxf, shf);
-  const bool none = m == -INFINITY;
-  const int32_t tok = a.tokens ? a.tokens[row] : -1;
+  const uint8_t* base = static_cast<const uint8_t*>(a.logits) + off * ES;
+  const int k = a.topk;
+
+  // 16-byte vectors of the row, and the logits before and after them
+  const int head = min((int)(((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / ES), a.V);
+  const int nv = (a.V - head) / VE;
+  const int tail = a.V - head - nv * VE;
+  const uint4* vec = reinterpret_cast<const uint4*>(base + (int64_t)head * ES);
+  const int per = (nv + csize - 1) / csize;
+  const int vbeg = min(nv, rank * per), vend = min(nv, vbeg + per);
+  const int nblk = (vend - vbeg + BLOCK - 1) / BLOCK;
+
+  auto fetch = [&](int b) {  // thread 0
+    const int v = vbeg + b * BLOCK;
+    const uint32_t bytes = (uint32_t)min(BLOCK, vend - v) * 16;
+    mbar_arrive_expect_tx(&full[b % STAGES], bytes);
+    bulk_load(ring + (b % STAGES) * BLOCK, vec + v, bytes, &full[b % STAGES]);
+  };
+  if (tid == 0)
+    for (int b = 0; b < min(STAGES, nblk); ++b) fetch(b);
+
+  const int32_t tok = a.tokens ? __ldg(a.tokens + row) : -1;
   const bool tok_ok = tok >= 0 && tok < a.V;
-  const float xt = tok_ok ? load_logit<TYPE>(a.logits, off + tok) : 0.f;
-  float s = 0.f, t = 0.f, above = 0.f;
-  for (int32_t i = threadIdx.x; i < a.V; i += blockDim.x) {
-    const float x = load_logit<TYPE>(a.logits, off + i);
-    const float d = fmaxf(x - m, -1e4f);
-    const float e = expf(d);
-    s += e;
-    t += e * d;
-    above += (x > xt || (x == xt && i < tok)) ? 1.f : 0.f;
+  // a value above every logit counts nothing
+  const float xt = tok_ok && a.token_rank ? E::load(base, tok) : INFINITY;
+
+  // M: the logit the reference r was made from (LOW: none yet)
+  float rmax = -INFINITY, M = E::LOW, r = E::LOW * LOG2E;
+  uint64_t s2 = 0, t2 = 0;
+  int above = 0;
+  bool bad = false, over = false;
+  // lower bound of the k-th key, and its value; -inf is never offered (the masked ids that
+  // follow are added at the end)
+  constexpr float kLowest = -3.4028234663852886e38f;
+  uint64_t thr = (uint64_t)order_of(kLowest) << 32;
+  float thr_x = k > 0 ? kLowest : INFINITY;
+  int settled = 0;  // entries at the front of buf that are there before the current block
+
+  auto rise = [&](float m) {  // a new reference
+    const float rn = m * LOG2E, d = r - rn, f = ex2(d);
+    const uint64_t f2 = pack2(f, f);
+    t2 = fma2(f2, fma2(s2, pack2(d, d), t2), 0);
+    s2 = fma2(f2, s2, 0);
+    M = m;
+    r = rn;
+  };
+  auto offer = [&](float x, int32_t id) {
+    if (!(x >= thr_x)) return;
+    const uint64_t key = order_key(x, id);
+    if (key >= thr) {
+      const int pos = atomicAdd(&cnt, 1);
+      if (pos < CAP) buf[pos] = key;
+      over = over || pos >= CUT;
+    }
+  };
+  auto offer_vector = [&](const uint4& v, int vi) {
+    float x[VE];
+    E::unpack(v, x);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) offer(x[i], head + vi * VE + i);
+  };
+
+  // cut the buffer back to the k largest keys and raise thr to the last of them; after an
+  // overflow the entries of the current block are dropped instead (they are offered again)
+  auto cut = [&]() {
+    const int n = min(cnt, CAP);
+    const bool lost = cnt > CAP;
+    for (int i = tid; i < n; i += THREADS) {
+      const uint64_t key = buf[i];
+      int before = 0;
+      for (int j = 0; j < n; ++j) before += buf[j] > key;
+      if (before < k) sorted[before] = key;
+    }
+    __syncthreads();
+    if (n >= k && sorted[k - 1] > thr) {
+      thr = sorted[k - 1];
+      thr_x = value_of(thr);
+    }
+    if (!lost) settled = min(n, k);
+    if (!lost && tid < settled) buf[tid] = sorted[tid];
+    if (tid == 0) cnt = settled;
+    over = false;
+    __syncthreads();
+    return lost;
+  };
+
+  // what a vector needs besides its sums when its maximum is not below `gate`
+  auto special = [&](const uint4& x4, float vm, int v) {
+    bad = bad || !(vm < INFINITY);
+    if (vm > M + HEADROOM || (M == E::LOW && vm > E::LOW)) rise(vm);
+    if (k > 0 && vm >= thr_x) offer_vector(x4, v);
+    if (vm >= xt) {
+      const int id0 = head + v * VE;
+      if (tok >= id0 && tok < id0 + VE) {
+        float x[VE];
+        E::unpack(x4, x);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) above += x[i] > xt || (x[i] == xt && id0 + i < tok);
+      } else {
+        above += E::above(x4, xt, id0 < tok);
+      }
+    }
+  };
+
+  if (rank == 0 && tid < head + tail) {
+    const int32_t id = tid < head ? tid : a.V - tail + (tid - head);
+    const float x = E::load(base, id);
+    bad = !(x < INFINITY);
+    rmax = x;
+    if (x > E::LOW) {
+      rise(x);
+      s2 = pack2(1.f, 0.f);
+      t2 = pack2(fmaf(x, LOG2E, -r), 0.f);
+    }
+    if (k > 0) offer(x, id);
+    above = x > xt || (x == xt && id < tok);
   }
-  s = block_reduce(s, addf, shf);
-  t = block_reduce(t, addf, shf);
-  above = block_reduce(above, addf, shf);
-  const float ls = logf(s);
+
+  for (int b = 0; b < nblk; ++b) {
+    const uint4* blk = ring + (b % STAGES) * BLOCK + tid;
+    const int v0 = vbeg + b * BLOCK + tid;
+    (void)mbar_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err);
+    if (b == 0 && k > 0) {
+      // the first bound: the k-th largest of 32 groups' largest keys (k different logits are at
+      // least that; ids included, so that a row of ties is bounded too)
+      uint64_t g = 0;
+#pragma unroll
+      for (int j = 0; j < RV; ++j) {
+        const int v = v0 + j * THREADS;
+        if (v < vend) g = max(g, order_key(E::vmax(blk[j * THREADS]), head + v * VE + VE - 1));
+      }
+#pragma unroll
+      for (int o = 1; o < THREADS / 32; o <<= 1) g = max(g, shfl_xor_u64(g, o));
+      if (tid % (THREADS / 32) == 0) group[tid / (THREADS / 32)] = g;
+      __syncthreads();
+      settled = cnt;  // the logits beside the vectors
+      g = group[lane];
+      int before = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) before += group[i] > g || (group[i] == g && i < lane);
+      const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, before == k - 1)) - 1;
+      g = __shfl_sync(0xFFFFFFFFu, (unsigned long long)g, owner);
+      if (g > thr) {
+        thr = g;
+        thr_x = value_of(g);
+      }
+      __syncthreads();  // cnt has been read
+    }
+#pragma unroll
+    for (int j = 0; j < RV; ++j) {
+      const int v = v0 + j * THREADS;
+      if (v >= vend) break;
+      const uint4 x4 = blk[j * THREADS];
+      const float vm = E::vmax(x4);
+      rmax = fmaxf(rmax, vm);
+      const float gate = fminf(fminf(thr_x, xt), M == E::LOW ? E::LOW : M + HEADROOM);
+      if (!(vm < gate)) special(x4, vm, v);
+      if (vm > E::LOW) {
+        float x[VE];
+        E::unpack_floored(x4, x);
+        const uint64_t l2 = pack2(LOG2E, LOG2E), nr = pack2(-r, -r);
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) {
+          const uint64_t y = fma2(pack2(x[i], x[i + 1]), l2, nr);
+          const float2 yy = unpack2(y);
+          const uint64_t e = pack2(ex2(yy.x), ex2(yy.y));
+          s2 = add2(s2, e);
+          t2 = fma2(e, y, t2);
+        }
+      }
+    }
+    while (__syncthreads_or(over)) {
+      if (!cut()) break;
+#pragma unroll 1
+      for (int j = 0; j < RV; ++j) {
+        const int v = v0 + j * THREADS;
+        if (v < vend) offer_vector(blk[j * THREADS], v);
+      }
+    }
+    // every thread is done with the block
+    if (abort_flag) {
+      // a wait gave up: let the copies in flight land before shared memory goes away
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = b; tid == 0 && i < min(nblk, b + STAGES); ++i)
+        while (!mbar_try_wait(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u))
+          if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+      break;
+    }
+    if (tid == 0 && b + STAGES < nblk) fetch(b + STAGES);
+  }
+  if (k > 0) {
+    __syncthreads();
+    cut();  // never after an overflow: more than CUT candidates were cut with their block
+  }
+
+  // threads -> warps -> the CTA
+  const float2 ss = unpack2(s2), tt = unpack2(t2);
+  float s = ss.x + ss.y, t = tt.x + tt.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float r_o = __shfl_xor_sync(0xFFFFFFFFu, r, o), s_o = __shfl_xor_sync(0xFFFFFFFFu, s, o),
+                t_o = __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    merge(r, s, t, r_o, s_o, t_o);
+    rmax = fmaxf(rmax, __shfl_xor_sync(0xFFFFFFFFu, rmax, o));
+    above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+  }
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if (lane == 0) wpart[warp] = Part{rmax, r, s, t, above, bad ? 1 : 0, 0};
+  __syncthreads();
+  if (tid == 0) {
+    Part p = wpart[0];
+    for (int w = 1; w < WARPS; ++w) {
+      merge(p.r, p.s, p.t, wpart[w].r, wpart[w].s, wpart[w].t);
+      p.rmax = fmaxf(p.rmax, wpart[w].rmax);
+      p.above += wpart[w].above;
+      p.bad |= wpart[w].bad;
+    }
+    p.n = settled;
+    part = p;
+  }
+  if (csize > 1) {
+    cluster_sync();  // every CTA's part and list are written
+    if (rank == 0) {
+      if (tid == 0) {
+        Part p = part;
+        for (int c = 1; c < csize; ++c) {
+          const uint32_t q = mapa_shared(smem_u32(&part), (uint32_t)c);
+          merge(p.r, p.s, p.t, ld_shared_cluster_f32(q + 4), ld_shared_cluster_f32(q + 8),
+                ld_shared_cluster_f32(q + 12));
+          p.rmax = fmaxf(p.rmax, ld_shared_cluster_f32(q));
+          p.above += (int32_t)ld_cluster_u32(q + 16);
+          p.bad |= (int32_t)ld_cluster_u32(q + 20);
+        }
+        part = p;
+      }
+      for (int i = tid; i < csize * k; i += THREADS) {
+        const int c = i / k, j = i - c * k;
+        if (c > 0 && j < (int)ld_cluster_u32(mapa_shared(smem_u32(&part), (uint32_t)c) + 24))
+          buf[atomicAdd(&cnt, 1)] = ld_cluster_u64(mapa_shared(smem_u32(&sorted[j]), (uint32_t)c));
+      }
+    }
+    cluster_sync();  // rank 0 has read; the others may leave
+    if (rank != 0) return;
+    if (k > 0) cut();
+  }
+  __syncthreads();
+
+  const Part p = part;
+  const bool none = p.rmax == -INFINITY;
+  const bool low = !none && !p.bad && p.rmax <= E::LOW;
+  const float ref = p.r;
+  float l2s = log2f(p.s), ent = (l2s - p.t / p.s) * LN2;
+  if (low) {
+    // every logit is at or below LOW: sum against the maximum itself
+    float sl = 0.f, tl = 0.f;
+    for (int32_t i = tid; i < a.V; i += THREADS) {
+      const float y = fmaxf((E::load(base, i) - p.rmax) * LOG2E, -1e4f), e = ex2(y);
+      sl += e;
+      tl += e * y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sl += __shfl_xor_sync(0xFFFFFFFFu, sl, o);
+      tl += __shfl_xor_sync(0xFFFFFFFFu, tl, o);
+    }
+    if (lane == 0) {
+      wpart[warp].s = sl;
+      wpart[warp].t = tl;
+    }
+    __syncthreads();
+    sl = tl = 0.f;
+    for (int w = 0; w < WARPS; ++w) {
+      sl += wpart[w].s;
+      tl += wpart[w].t;
+    }
+    l2s = log2f(sl);
+    ent = (l2s - tl / sl) * LN2;
+  }
   const float nan = __uint_as_float(0x7FC00000u);
-  auto logp = [&](float x) { return bad ? nan : none ? -INFINITY : (x - m) - ls; };
-  if (threadIdx.x == 0) {
-    if (bad) set_error(a.err, QW_ERR_VALUE);
+  auto logp = [&](float x) {
+    if (p.bad) return nan;
+    if (none) return -INFINITY;
+    if (low) return (x - p.rmax) - l2s * LN2;
+    if (x < -1e30f) return x - p.rmax;  // x log2(e) may overflow; log s is lost beside it
+    return (fmaf(x, LOG2E, -ref) - l2s) * LN2;
+  };
+  if (tid == 0) {
+    if (p.bad) set_error(a.err, QW_ERR_VALUE);
     if (a.tokens && !tok_ok) set_error(a.err, QW_ERR_INVALID_ARG);
-    if (a.token_logprob) a.token_logprob[row] = tok_ok ? logp(xt) : nan;
-    if (a.token_rank) a.token_rank[row] = tok_ok ? 1 + (int32_t)above : 0;
-    if (a.entropy) a.entropy[row] = bad ? nan : none ? 0.f : ls - t / s;
+    if (a.token_logprob) a.token_logprob[row] = tok_ok ? logp(E::load(base, tok)) : nan;
+    if (a.token_rank) a.token_rank[row] = tok_ok ? 1 + p.above : 0;
+    if (a.entropy) a.entropy[row] = p.bad ? nan : none ? 0.f : ent;
   }
-  unsigned long long last = ~0ull;
-  for (int j = 0; j < a.topk; ++j) {
-    unsigned long long best = 0;
-    for (int32_t i = threadIdx.x; i < a.V; i += blockDim.x) {
-      const unsigned long long k = order_key(load_logit<TYPE>(a.logits, off + i), i);
-      if (k < last && k > best) best = k;
-    }
-    best = block_reduce(best, [](unsigned long long x, unsigned long long y) { return x > y ? x : y; }, shk);
-    last = best;
-    if (threadIdx.x == 0) {
-      const int32_t id = (int32_t)(0xFFFFFFFFu - (uint32_t)best);
-      a.top_ids[row * a.topk + j] = id;
-      a.top_logprobs[row * a.topk + j] = logp(load_logit<TYPE>(a.logits, off + id));
+  if (k > settled && warp == 0) {
+    // fewer ids than asked for are left by the mask: the masked ones follow in id order
+    for (int32_t i0 = 0, n = settled; i0 < a.V && n < k; i0 += 32) {
+      const bool gone = i0 + lane < a.V && E::load(base, i0 + lane) == -INFINITY;
+      const uint32_t set = __ballot_sync(0xFFFFFFFFu, gone);
+      const int at = n + __popc(set & ((1u << lane) - 1u));
+      if (gone && at < k) sorted[at] = order_key(-INFINITY, i0 + lane);
+      n += __popc(set);
+      if (lane == 0) cnt = min(n, k);
     }
   }
+  if (k > settled) __syncthreads();
+  if (tid < k) {
+    // (a row with NaN may not have that many: what is missing names id 0)
+    const uint64_t key = tid < max(cnt, settled) ? sorted[tid] : 0xFFFFFFFFull;
+    a.top_ids[row * k + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
+    a.top_logprobs[row * k + tid] = logp(value_of(key));
+  }
+}
+
+template <int TYPE>
+qw_status launch_type(const LogprobsArgs& a, int64_t T, int csize, cudaStream_t st) {
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      logprobs_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES);
+  if (attr != cudaSuccess) return QW_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.dynamicSmemBytes = RING_BYTES;
+  cfg.gridDim = dim3((unsigned)(T * csize));
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)csize;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = csize > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<TYPE>, a, csize) == cudaSuccess ? QW_OK
+                                                                                   : QW_ERR_CUDA;
 }
 
 }  // namespace
 
 qw_status launch_logprobs(const LogprobsArgs& a, int32_t type, int64_t T, cudaStream_t st) {
-  const dim3 grid((unsigned)T);
-  if (type == QW_T_F32)
-    logprobs_kernel<QW_T_F32><<<grid, 512, 0, st>>>(a);
-  else if (type == QW_T_F16)
-    logprobs_kernel<QW_T_F16><<<grid, 512, 0, st>>>(a);
-  else
-    logprobs_kernel<QW_T_BF16><<<grid, 512, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? QW_OK : QW_ERR_CUDA;
+  int csize = 1;
+  while (csize < MAX_CLUSTER && T * csize < 2 * device_sm_count() && a.V / csize > 4096) csize *= 2;
+  if (type == QW_T_F32) return launch_type<QW_T_F32>(a, T, csize, st);
+  if (type == QW_T_F16) return launch_type<QW_T_F16>(a, T, csize, st);
+  return launch_type<QW_T_BF16>(a, T, csize, st);
 }
 
 }  // namespace qw
