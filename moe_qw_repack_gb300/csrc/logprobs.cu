@@ -68,14 +68,19 @@ struct El<QW_T_F32> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = fmaxf(x[i], LOW);
   }
-  // how many of the vector's values are above t (or equal, with `equal`)
-  static __device__ __forceinline__ int above(const uint4& v, float t, bool equal) {
+  // counters of values at or above t, kept per thread and read out once per block
+  using Count = int;
+  static __device__ __forceinline__ void count(const uint4& v, float t, Count& c) {
     float x[4];
     unpack(v, x);
-    int n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n += equal ? x[i] >= t : x[i] > t;
-    return n;
+    for (int i = 0; i < 4; ++i) c += x[i] >= t;
+  }
+  static __device__ __forceinline__ int total(Count c) { return c; }
+  // the next value of the type above x
+  static __device__ __forceinline__ float next_up(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return __uint_as_float(x == 0.f ? 1u : (b & 0x80000000u) ? b - 1 : b + 1);
   }
 };
 
@@ -129,15 +134,21 @@ struct El16 {
                       as_u32(__hmax2(pair(v.z), f)), as_u32(__hmax2(pair(v.w), f))),
            x);
   }
-  static __device__ __forceinline__ int above(const uint4& v, float t, bool equal) {
+  // 1.0 or 0.0 added in each half: exact, as at most 4 RV are added between two read-outs
+  using Count = H2;
+  static __device__ __forceinline__ void count(const uint4& v, float t, Count& c) {
     const H2 tt = Pair<H2>::splat(t);  // t is a value of the type: exact
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t ones = 0;  // 1.0 or 0.0 in each half, summed
-    H2 sum = *reinterpret_cast<H2*>(&ones);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum = __hadd2(sum, equal ? __hge2(pair(w[i]), tt) : __hgt2(pair(w[i]), tt));
-    const uint32_t s = as_u32(sum);
-    return (int)(Pair<H2>::lo(s) + Pair<H2>::hi(s));
+    for (int i = 0; i < 4; ++i) c = __hadd2(c, __hge2(pair(w[i]), tt));
+  }
+  static __device__ __forceinline__ int total(const Count& c) {
+    return (int)(Pair<H2>::lo(as_u32(c)) + Pair<H2>::hi(as_u32(c)));
+  }
+  static __device__ __forceinline__ float next_up(float x) {
+    uint32_t b = as_u32(Pair<H2>::splat(x)) & 0xFFFFu;
+    b = x == 0.f ? 1u : (b & 0x8000u) ? b - 1 : b + 1;
+    return Pair<H2>::lo(b);
   }
 };
 template <>
@@ -200,10 +211,6 @@ __device__ __forceinline__ float value_of(uint64_t key) {
   return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
 }
 
-__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t v, int o) {
-  return __shfl_xor_sync(0xFFFFFFFFu, (unsigned long long)v, o);
-}
-
 // Partial result of some of a row's logits.
 struct Part {
   float rmax;  // largest logit
@@ -248,7 +255,8 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   __shared__ uint64_t buf[CAP];
   __shared__ uint64_t sorted[kLogprobsMaxTop];
   __shared__ int cnt;
-  __shared__ uint64_t group[32];
+  __shared__ uint32_t group[32], first;
+  static_assert(WARPS * RV == 32, "one group for each candidate of the first bound");
   __shared__ Part wpart[WARPS];
   __shared__ Part part;  // this CTA's result; on rank 0, at the end, the row's
   __shared__ uint64_t full[STAGES];
@@ -291,7 +299,9 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   const int32_t tok = a.tokens ? __ldg(a.tokens + row) : -1;
   const bool tok_ok = tok >= 0 && tok < a.V;
   // a value above every logit counts nothing
-  const float xt = tok_ok && a.token_rank ? E::load(base, tok) : INFINITY;
+  const bool want_rank = tok_ok && a.token_rank;
+  const float xt = want_rank ? E::load(base, tok) : INFINITY;
+  const float xt_up = want_rank ? E::next_up(xt) : INFINITY;
 
   // M: the logit the reference r was made from (LOW: none yet)
   float rmax = -INFINITY, M = E::LOW, r = E::LOW * LOG2E;
@@ -358,17 +368,6 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     bad = bad || !(vm < INFINITY);
     if (vm > M + HEADROOM || (M == E::LOW && vm > E::LOW)) rise(vm);
     if (k > 0 && vm >= thr_x) offer_vector(x4, v);
-    if (vm >= xt) {
-      const int id0 = head + v * VE;
-      if (tok >= id0 && tok < id0 + VE) {
-        float x[VE];
-        E::unpack(x4, x);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) above += x[i] > xt || (x[i] == xt && id0 + i < tok);
-      } else {
-        above += E::above(x4, xt, id0 < tok);
-      }
-    }
   };
 
   if (rank == 0 && tid < head + tail) {
@@ -390,39 +389,42 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     const int v0 = vbeg + b * BLOCK + tid;
     (void)mbar_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err);
     if (b == 0 && k > 0) {
-      // the first bound: the k-th largest of 32 groups' largest keys (k different logits are at
-      // least that; ids included, so that a row of ties is bounded too)
-      uint64_t g = 0;
+      // the first bound: the k-th largest of the maxima of 32 groups, a group being what a
+      // warp takes at a time (k different logits are at least that)
 #pragma unroll
       for (int j = 0; j < RV; ++j) {
-        const int v = v0 + j * THREADS;
-        if (v < vend) g = max(g, order_key(E::vmax(blk[j * THREADS]), head + v * VE + VE - 1));
+        const float vm = v0 + j * THREADS < vend ? E::vmax(blk[j * THREADS]) : -INFINITY;
+        const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, order_of(vm));
+        if (lane == 0) group[warp * RV + j] = g;
       }
-#pragma unroll
-      for (int o = 1; o < THREADS / 32; o <<= 1) g = max(g, shfl_xor_u64(g, o));
-      if (tid % (THREADS / 32) == 0) group[tid / (THREADS / 32)] = g;
       __syncthreads();
       settled = cnt;  // the logits beside the vectors
-      g = group[lane];
-      int before = 0;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) before += group[i] > g || (group[i] == g && i < lane);
-      const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, before == k - 1)) - 1;
-      g = __shfl_sync(0xFFFFFFFFu, (unsigned long long)g, owner);
-      if (g > thr) {
-        thr = g;
-        thr_x = value_of(g);
+      if (warp == 0) {
+        const uint32_t g = group[lane];
+        int before = 0;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, g, i);
+          before += o > g || (o == g && i < lane);
+        }
+        if (before == k - 1) first = g;
       }
-      __syncthreads();  // cnt has been read
+      __syncthreads();
+      if ((uint64_t)first << 32 > thr) {
+        thr = (uint64_t)first << 32;
+        thr_x = value_of(thr);
+      }
     }
-#pragma unroll
+    typename E::Count count{};
+#pragma unroll 1
     for (int j = 0; j < RV; ++j) {
       const int v = v0 + j * THREADS;
       if (v >= vend) break;
       const uint4 x4 = blk[j * THREADS];
       const float vm = E::vmax(x4);
       rmax = fmaxf(rmax, vm);
-      const float gate = fminf(fminf(thr_x, xt), M == E::LOW ? E::LOW : M + HEADROOM);
+      if (vm >= xt) E::count(x4, head + v * VE < tok ? xt : xt_up, count);
+      const float gate = fminf(thr_x, M == E::LOW ? E::LOW : M + HEADROOM);
       if (!(vm < gate)) special(x4, vm, v);
       if (vm > E::LOW) {
         float x[VE];
@@ -438,7 +440,11 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
         }
       }
     }
-    while (__syncthreads_or(over)) {
+    if (want_rank) above += E::total(count);
+    // the buffer is cut when it fills up, and whenever the row has doubled: what passes a bound
+    // from the last cut is then about k logits
+    const bool doubled = k > 0 && ((b + 1) & b) == 0 && b + 1 < nblk;
+    while (__syncthreads_or(over || doubled)) {
       if (!cut()) break;
 #pragma unroll 1
       for (int j = 0; j < RV; ++j) {
@@ -485,6 +491,11 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
       p.bad |= wpart[w].bad;
     }
     p.n = settled;
+    // the vector that holds the token was counted as lying before it: take back the equal
+    // logits from the token on
+    const int vt = tok >= head ? (tok - head) / VE : -1;
+    if (want_rank && vt >= vbeg && vt < vend && head + vt * VE < tok)
+      for (int i = tok; i < head + (vt + 1) * VE; ++i) p.above -= E::load(base, i) == xt;
     part = p;
   }
   if (csize > 1) {
