@@ -57,6 +57,12 @@ struct El<QW_T_F32> {
     return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
                    max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
+  static __device__ __forceinline__ float vmax(const uint4& v, const uint4& w) {
+    return max_nan(vmax(v), vmax(w));
+  }
+  static __device__ __forceinline__ uint4 masked() {  // a vector of -inf
+    return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  }
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x);
     x[1] = __uint_as_float(v.y);
@@ -115,10 +121,20 @@ template <class H2>
 struct El16 {
   static constexpr int VE = 8;
   static __device__ __forceinline__ H2 pair(uint32_t w) { return *reinterpret_cast<const H2*>(&w); }
+  static __device__ __forceinline__ H2 pmax(const uint4& v) {
+    return __hmax2_nan(__hmax2_nan(pair(v.x), pair(v.y)), __hmax2_nan(pair(v.z), pair(v.w)));
+  }
   static __device__ __forceinline__ float vmax(const uint4& v) {
-    const uint32_t m = as_u32(__hmax2_nan(__hmax2_nan(pair(v.x), pair(v.y)),
-                                          __hmax2_nan(pair(v.z), pair(v.w))));
+    const uint32_t m = as_u32(pmax(v));
     return El<QW_T_F32>::max_nan(Pair<H2>::lo(m), Pair<H2>::hi(m));
+  }
+  static __device__ __forceinline__ float vmax(const uint4& v, const uint4& w) {
+    const uint32_t m = as_u32(__hmax2_nan(pmax(v), pmax(w)));
+    return El<QW_T_F32>::max_nan(Pair<H2>::lo(m), Pair<H2>::hi(m));
+  }
+  static __device__ __forceinline__ uint4 masked() {  // a vector of -inf
+    const uint32_t m = as_u32(Pair<H2>::splat(-INFINITY));
+    return make_uint4(m, m, m, m);
   }
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -363,13 +379,6 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     return lost;
   };
 
-  // what a vector needs besides its sums when its maximum is not below `gate`
-  auto special = [&](const uint4& x4, float vm, int v) {
-    bad = bad || !(vm < INFINITY);
-    if (vm > M + HEADROOM || (M == E::LOW && vm > E::LOW)) rise(vm);
-    if (k > 0 && vm >= thr_x) offer_vector(x4, v);
-  };
-
   if (rank == 0 && tid < head + tail) {
     const int32_t id = tid < head ? tid : a.V - tail + (tid - head);
     const float x = E::load(base, id);
@@ -416,28 +425,45 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
       }
     }
     typename E::Count count{};
+    // two vectors at a time, so that their maximum is looked at once for both
 #pragma unroll 1
-    for (int j = 0; j < RV; ++j) {
+    for (int j = 0; j < RV; j += 2) {
       const int v = v0 + j * THREADS;
       if (v >= vend) break;
       const uint4 x4 = blk[j * THREADS];
-      const float vm = E::vmax(x4);
+      const bool second = v + THREADS < vend;
+      const uint4 z4 = second ? blk[(j + 1) * THREADS] : E::masked();
+      const float vm = E::vmax(x4, z4);
       rmax = fmaxf(rmax, vm);
-      if (vm >= xt) E::count(x4, head + v * VE < tok ? xt : xt_up, count);
+      if (vm >= xt) {
+        E::count(x4, head + v * VE < tok ? xt : xt_up, count);
+        if (second) E::count(z4, head + (v + THREADS) * VE < tok ? xt : xt_up, count);
+      }
       const float gate = fminf(thr_x, M == E::LOW ? E::LOW : M + HEADROOM);
-      if (!(vm < gate)) special(x4, vm, v);
-      if (vm > E::LOW) {
-        float x[VE];
-        E::unpack_floored(x4, x);
-        const uint64_t l2 = pack2(LOG2E, LOG2E), nr = pack2(-r, -r);
-#pragma unroll
-        for (int i = 0; i < VE; i += 2) {
-          const uint64_t y = fma2(pack2(x[i], x[i + 1]), l2, nr);
-          const float2 yy = unpack2(y);
-          const uint64_t e = pack2(ex2(yy.x), ex2(yy.y));
-          s2 = add2(s2, e);
-          t2 = fma2(e, y, t2);
+      if (!(vm < gate)) {
+        bad = bad || !(vm < INFINITY);
+        if (vm > M + HEADROOM || (M == E::LOW && vm > E::LOW)) rise(vm);
+        if (k > 0 && vm >= thr_x) {
+          if (E::vmax(x4) >= thr_x) offer_vector(x4, v);
+          if (second && E::vmax(z4) >= thr_x) offer_vector(z4, v + THREADS);
         }
+      }
+      if (vm > E::LOW) {
+        const uint64_t l2 = pack2(LOG2E, LOG2E), nr = pack2(-r, -r);
+        auto sum = [&](const uint4& q) {
+          float x[VE];
+          E::unpack_floored(q, x);
+#pragma unroll
+          for (int i = 0; i < VE; i += 2) {
+            const uint64_t y = fma2(pack2(x[i], x[i + 1]), l2, nr);
+            const float2 yy = unpack2(y);
+            const uint64_t e = pack2(ex2(yy.x), ex2(yy.y));
+            s2 = add2(s2, e);
+            t2 = fma2(e, y, t2);
+          }
+        };
+        sum(x4);
+        sum(z4);
       }
     }
     if (want_rank) above += E::total(count);
