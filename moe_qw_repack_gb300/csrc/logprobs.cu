@@ -46,7 +46,7 @@ struct El<QW_T_F32> {
   static constexpr int VE = 4;
   static constexpr float LOW = -1e30f;
   static __device__ __forceinline__ float load(const void* p, int64_t i) {
-    return __ldg(static_cast<const float*>(p) + i);
+    return static_cast<const float*>(p)[i];
   }
   static __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   // follow are added at the end)
   constexpr float kLowest = -3.4028234663852886e38f;
   uint64_t thr = (uint64_t)order_of(kLowest) << 32;
-  float thr_x = k > 0 ? kLowest : INFINITY;
+  float thr_x = k > 0 ? kLowest : __uint_as_float(0x7FC00000u);  // NaN: nothing passes
   int settled = 0;  // entries at the front of buf that are there before the current block
 
   auto rise = [&](float m) {  // a new reference
@@ -348,11 +348,16 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
       over = over || pos >= CUT;
     }
   };
-  auto offer_vector = [&](const uint4& v, int vi) {
-    float x[VE];
-    E::unpack(v, x);
-#pragma unroll
-    for (int i = 0; i < VE; ++i) offer(x[i], head + vi * VE + i);
+  // Vectors j and j + 1 of the lanes in `hits` of this warp: a lane for each of their logits.
+  auto offer_hits = [&](uint32_t hits, int b, int j) {
+    const int pos = j * THREADS + warp * 32 + (lane / VE) * THREADS;
+    while (hits) {
+      const int p = pos + __ffs(hits) - 1;
+      hits &= hits - 1;
+      const int v = vbeg + b * BLOCK + p;
+      if (lane < 2 * VE && v < vend)
+        offer(E::load(ring + (b % STAGES) * BLOCK + p, lane % VE), head + v * VE + lane % VE);
+    }
   };
 
   // cut the buffer back to the k largest keys and raise thr to the last of them; after an
@@ -429,24 +434,20 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
 #pragma unroll 1
     for (int j = 0; j < RV; j += 2) {
       const int v = v0 + j * THREADS;
-      if (v >= vend) break;
-      const uint4 x4 = blk[j * THREADS];
-      const bool second = v + THREADS < vend;
+      const bool first = v < vend, second = v + THREADS < vend;
+      const uint4 x4 = first ? blk[j * THREADS] : E::masked();
       const uint4 z4 = second ? blk[(j + 1) * THREADS] : E::masked();
       const float vm = E::vmax(x4, z4);
       rmax = fmaxf(rmax, vm);
       if (vm >= xt) {
-        E::count(x4, head + v * VE < tok ? xt : xt_up, count);
+        if (first) E::count(x4, head + v * VE < tok ? xt : xt_up, count);
         if (second) E::count(z4, head + (v + THREADS) * VE < tok ? xt : xt_up, count);
       }
-      const float gate = fminf(thr_x, M == E::LOW ? E::LOW : M + HEADROOM);
-      if (!(vm < gate)) {
+      const uint32_t hits = __ballot_sync(0xFFFFFFFFu, vm >= thr_x);
+      if (hits) offer_hits(hits, b, j);
+      if (!(vm < (M == E::LOW ? E::LOW : M + HEADROOM))) {
         bad = bad || !(vm < INFINITY);
-        if (vm > M + HEADROOM || (M == E::LOW && vm > E::LOW)) rise(vm);
-        if (k > 0 && vm >= thr_x) {
-          if (E::vmax(x4) >= thr_x) offer_vector(x4, v);
-          if (second && E::vmax(z4) >= thr_x) offer_vector(z4, v + THREADS);
-        }
+        if (vm > E::LOW) rise(vm);
       }
       if (vm > E::LOW) {
         const uint64_t l2 = pack2(LOG2E, LOG2E), nr = pack2(-r, -r);
@@ -473,10 +474,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     while (__syncthreads_or(over || doubled)) {
       if (!cut()) break;
 #pragma unroll 1
-      for (int j = 0; j < RV; ++j) {
-        const int v = v0 + j * THREADS;
-        if (v < vend) offer_vector(blk[j * THREADS], v);
-      }
+      for (int j = 0; j < RV; j += 2) offer_hits(0xFFFFFFFFu, b, j);
     }
     // every thread is done with the block
     if (abort_flag) {
