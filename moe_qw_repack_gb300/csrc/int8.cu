@@ -112,57 +112,189 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// 64 x 64 output tile, dp4a over 64-byte K steps.
-constexpr int TILE = 64, KSTEP = 64;
-template <bool GATED>
-__global__ void __launch_bounds__(256) int8_tile_kernel(const Int8Problem p) {
-  __shared__ uint32_t sa[TILE][KSTEP / 4 + 1];
-  __shared__ uint32_t sw[GATED ? 2 : 1][TILE][KSTEP / 4 + 1];
-  const int64_t m0 = (int64_t)blockIdx.y * TILE;
-  const int64_t n0 = (int64_t)blockIdx.x * TILE;
-  const int64_t cols = GATED ? p.N / 2 : p.N;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[GATED ? 2 : 1][4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += KSTEP) {
-    for (int i = threadIdx.x; i < TILE * (KSTEP / 4); i += 256) {
-      const int r = i / (KSTEP / 4), c = i % (KSTEP / 4);
-      const bool kin = k0 + 4 * c < p.K;
-      sa[r][c] = kin && m0 + r < p.M
-                     ? *reinterpret_cast<const uint32_t*>(p.A + (m0 + r) * p.lda + k0 + 4 * c)
-                     : 0u;
-      for (int h = 0; h < (GATED ? 2 : 1); ++h)
-        sw[h][r][c] = kin && n0 + r < cols ? *reinterpret_cast<const uint32_t*>(
-                                                 p.W + (h * cols + n0 + r) * p.K + k0 + 4 * c)
-                                           : 0u;
+// ------------------------------------------------------------------ up to 16 tokens
+// The weights are streamed once; integer sums are exact, so any order gives the same result.
+// A CTA of four warps takes RB blocks of 16 weight rows (gated: 16 gate rows and the 16 up rows
+// of the same outputs) and a slice of K; its warps take 64 x U bytes of every row in turn.  A lane
+// of mma.m16n8k32 (s8) owns rows g and g + 8 and, as k may be permuted if both operands agree,
+// 16 consecutive bytes of each per two MMAs: weights and tokens come in 16-byte loads in
+// fragment order, with nothing staged.  Partial sums meet in shared memory, those of a K split
+// over a cluster's CTAs in rank 0's.
+constexpr int GW = 4, GTHREADS = GW * 32;
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 ldg_stream(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <int NT, int RB, bool GATED>
+__global__ void __launch_bounds__(GTHREADS, 8)
+    gemv_int8_kernel(const Int8Problem p, const int csize, const bool early) {
+  static_assert(!GATED || RB == 2, "a gate block and its up block");
+  constexpr int U = 4 / RB / NT;              // steps of 64 k loaded at a time
+  constexpr int ROWS = GATED ? 16 : 16 * RB;  // outputs of a CTA
+  __shared__ int part[GW][RB][NT][128];
+  __shared__ int total[RB][NT][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = csize > 1 ? (int)(blockIdx.x % csize) : 0;
+  const int32_t cols = GATED ? p.N / 2 : p.N;
+  const int32_t n0 = (int32_t)(blockIdx.x / csize) * ROWS;
+
+  // this CTA's 64-k steps, and this lane's first byte of each of its rows
+  const int steps = (p.K + 63) / 64, per = (steps + csize - 1) / csize;
+  const int sbeg = min(steps, rank * per), send = min(steps, sbeg + per);
+  const int8_t* wp[RB][2];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // rows past the last are read as the last and not stored
+      const int32_t n = min(n0 + (GATED ? 0 : 16 * b) + g + 8 * h, cols - 1);
+      wp[b][h] = p.W + ((int64_t)(GATED && b ? cols : 0) + n) * p.K + 16 * t;
     }
-    __syncthreads();
-    for (int c = 0; c < KSTEP / 4; ++c)
+  const int8_t* xp[NT];
 #pragma unroll
-      for (int h = 0; h < (GATED ? 2 : 1); ++h)
+  for (int i = 0; i < NT; ++i) xp[i] = p.A + (int64_t)min((int64_t)(8 * i + g), p.M - 1) * p.lda + 16 * t;
+
+  int acc[RB][NT][4] = {};
+  uint4 w[U][RB][2], x[U][NT];
+  auto load_w = [&](int s0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[h][i][j] = __dp4a((int)sa[ty + 16 * i][c], (int)sw[h][tx + 16 * j][c], acc[h][i][j]);
-    __syncthreads();
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = (s0 + u) * 64;
+          w[u][b][h] = s0 + u < send && k + 16 * t < p.K ? ldg_stream(wp[b][h] + k)
+                                                         : make_uint4(0, 0, 0, 0);
+        }
+  };
+  // `early`: the previous kernel on the stream is this call's own quantiser, which waited for
+  // everything before it; the weights may be read while it runs
+  if (early) load_w(sbeg + warp * U);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!early) load_w(sbeg + warp * U);
+  for (int s0 = sbeg + warp * U; s0 < send; s0 += GW * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int k = (s0 + u) * 64;
+        x[u][i] = s0 + u < send && k + 16 * t < p.K && 8 * i + g < p.M
+                      ? __ldg(reinterpret_cast<const uint4*>(xp[i] + k))
+                      : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          mma_s8(acc[b][i], w[u][b][0].x, w[u][b][1].x, w[u][b][0].y, w[u][b][1].y, x[u][i].x,
+                 x[u][i].y);
+          mma_s8(acc[b][i], w[u][b][0].z, w[u][b][1].z, w[u][b][0].w, w[u][b][1].w, x[u][i].z,
+                 x[u][i].w);
+        }
+    load_w(s0 + GW * U);
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= p.M || n >= cols) continue;
-      float v[2];
-      for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-        const int64_t c = h * cols + n;
-        v[h] = (float)acc[h][i][j] * (p.a_scale[m] * p.w_scale[c]);
-        if (p.bias) v[h] += __uint_as_float((uint32_t)p.bias[c] << 16);
-      }
-      const float y = GATED ? v[0] / (1.f + expf(-v[0])) * v[1] : v[0];
-      if (p.c_f32) {
-        static_cast<float*>(p.C)[m * p.ldc + n] = y;
-      } else {
-        static_cast<__nv_bfloat16*>(p.C)[m * p.ldc + n] = __float2bfloat16_rn(y);
+
+  // element (row r, token c) of an accumulator at 16 c + r
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        part[warp][b][i][16 * (2 * t + (e & 1)) + g + 8 * (e >> 1)] = acc[b][i][e];
+  __syncthreads();
+  int sum[RB][NT];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      sum[b][i] = 0;
+#pragma unroll
+      for (int v = 0; v < GW; ++v) sum[b][i] += part[v][b][i][threadIdx.x];
+    }
+  if (csize > 1) {
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) total[b][i][threadIdx.x] = sum[b][i];
+    cluster_sync();
+    if (rank == 0)
+      for (int c = 1; c < csize; ++c)
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            sum[b][i] += __float_as_int(ld_shared_cluster_f32(
+                mapa_shared(smem_u32(&total[b][i][threadIdx.x]), (uint32_t)c)));
+    cluster_sync();
+    if (rank != 0) return;
+  }
+  const int r = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int64_t m = 8 * i + (threadIdx.x >> 4);
+    if (m >= p.M) continue;
+    const float sa = p.a_scale[m];
+    float v[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int32_t n = n0 + (GATED ? 0 : 16 * b) + r;
+      if (n >= cols) continue;
+      const int64_t wr = (GATED && b ? cols : 0) + (int64_t)n;
+      v[b] = (float)sum[b][i] * (sa * __ldg(p.w_scale + wr));
+      if (p.bias) v[b] += __uint_as_float((uint32_t)__ldg(p.bias + wr) << 16);
+      if constexpr (!GATED) {
+        if (p.c_f32)
+          static_cast<float*>(p.C)[m * p.ldc + n] = v[b];
+        else
+          static_cast<__nv_bfloat16*>(p.C)[m * p.ldc + n] = __float2bfloat16_rn(v[b]);
       }
     }
+    if constexpr (GATED)
+      if (n0 + r < cols)
+        static_cast<__nv_bfloat16*>(p.C)[m * p.ldc + n0 + r] =
+            __float2bfloat16_rn(v[0] / (1.f + expf(-v[0])) * v[1]);
+  }
+}
+
+template <int NT, int RB, bool GATED>
+qw_status launch_gemv(const Int8Problem& p, bool early, cudaStream_t st) {
+  const int32_t cols = GATED ? p.N / 2 : p.N, rows = GATED ? 16 : 16 * RB;
+  const int64_t blocks = ((int64_t)cols + rows - 1) / rows;
+  int csize = 1;
+  while (csize < 8 && blocks * csize < 4 * device_sm_count() && p.K / csize >= 2048) csize *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(blocks * csize));
+  cfg.blockDim = dim3(GTHREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)csize;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = csize > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, gemv_int8_kernel<NT, RB, GATED>, p, csize, early) == cudaSuccess
+             ? QW_OK
+             : QW_ERR_CUDA;
 }
 
 }  // namespace
@@ -184,14 +316,10 @@ qw_status launch_widen_int8(const void* A, int64_t lda, int64_t M, int32_t K, vo
                     static_cast<const int8_t*>(A), lda, M, K, static_cast<uint4*>(Q));
 }
 
-qw_status launch_gemv_int8(const Int8Problem& p, bool gated, int32_t* err, cudaStream_t st) {
-  const int64_t cols = gated ? p.N / 2 : p.N;
-  const dim3 grid((unsigned)((cols + TILE - 1) / TILE), (unsigned)((p.M + TILE - 1) / TILE));
+qw_status launch_gemv_int8(const Int8Problem& p, bool gated, bool early, cudaStream_t st) {
   if (gated)
-    int8_tile_kernel<true><<<grid, 256, 0, st>>>(p);
-  else
-    int8_tile_kernel<false><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? QW_OK : QW_ERR_CUDA;
+    return p.M <= 8 ? launch_gemv<1, 2, true>(p, early, st) : launch_gemv<2, 2, true>(p, early, st);
+  return p.M <= 8 ? launch_gemv<1, 1, false>(p, early, st) : launch_gemv<2, 2, false>(p, early, st);
 }
 
 }  // namespace qw

@@ -128,7 +128,8 @@ qw_status launch_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t
                                float* scale, bool f16, int32_t* err, cudaStream_t st);
 qw_status launch_widen_int8(const void* A, int64_t lda, int64_t M, int32_t K, void* Q,
                             cudaStream_t st);
-qw_status launch_gemv_int8(const Int8Problem& p, bool gated, int32_t* err, cudaStream_t st);
+// early: the call's own quantiser was enqueued directly before
+qw_status launch_gemv_int8(const Int8Problem& p, bool gated, bool early, cudaStream_t st);
 // codes16: the activations' codes as FP16 [M][K] (p.A is not read)
 qw_status launch_gemm_int8_tc(const Int8Problem& p, const void* codes16, bool gated, int32_t* err,
                               cudaStream_t st);
