@@ -9,7 +9,7 @@
 // Structure (persistent, one CTA per SM; a tile is 128 weight rows x BT tokens):
 //   warp 0      TMA producer of the tokens' tile: FP16 codes [M][K] of the workspace, 64 k
 //               (128-byte swizzle) a stage;
-//   warp 2      TMA producer of the weights: INT8, 128 rows x 128 k a stage;
+//   warp 2      TMA producer of the weights: INT8, 128 rows x 128 k a stage of their own ring;
 //   warp 1      TMEM owner and MMA issuer: weights are the A operand, read from tensor memory,
 //               tokens the B operand, read from shared memory;
 //   warps 4-11  converters: warp w covers TMEM lanes 32 (w % 4) .. + 31 and one 64-k half of a
@@ -17,9 +17,15 @@
 //               the FP16 number 1024 + (b + 128), minus 1152: exact) and stores them as the
 //               MMA's A operand with one tcgen05.st;
 //   warps 12-19 epilogue: tcgen05.ld the accumulator (a lane holds one weight row, a register
-//               one token), scale, add bias, (gated) exchange gate and up, round and store.
+//               one token), release it, scale, add bias, (gated) exchange gate and up, round and
+//               store while the next tile's MMAs run.  They take registers from the other warps
+//               (setmaxnreg) so that a tile's share fits.
+// A token stage and an operand slot of tensor memory belong together: one barrier says that both
+// are full and one commit that both are free (a second commit per stage cost 8 % of the MMA rate).
 // The gated form gives each 32 TMEM lanes 16 gate rows and the 16 up rows of the same outputs,
 // so that a gate and its up value meet through one shuffle.
+// Few tiles of long K are split: the CTAs of a cluster take slices of K, leave their FP32 sums in
+// shared memory, and each finishes a share of the tile's tokens, adding the slices in rank order.
 // Every wait is bounded; on expiry the kernel reports QW_ERR_TIMEOUT and shuts down.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -42,17 +48,34 @@ constexpr int EPI_WARP0 = CVT_WARP0 + NUM_CVT_WARPS, NUM_EPI_WARPS = 8;
 constexpr int NUM_THREADS = (EPI_WARP0 + NUM_EPI_WARPS) * 32;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int A_SLOT_COLS = KA / 2;  // 32-bit columns of one operand slot
+constexpr int A_COL0 = 256;          // the accumulator uses columns [0, BT)
+
+// Registers: launched with 96 a thread, then shared out by warpgroup (sum below what the launch
+// holds; launch() checks that the kernel was compiled to LAUNCH_REGS).
+constexpr int LAUNCH_REGS = 96, MISC_REGS = 40, CVT_REGS = 72, EPI_REGS = 144;
+static_assert(128 * MISC_REGS + NUM_CVT_WARPS * 32 * CVT_REGS + NUM_EPI_WARPS * 32 * EPI_REGS <=
+                  NUM_THREADS * LAUNCH_REGS,
+              "a split above the launch's registers would wait forever");
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <int BT>
 struct Geo {
   static constexpr int B_BYTES = BT * KA * 2;
-  static constexpr int B_STAGES = BT == 256 ? 5 : 8;
+  static constexpr int STAGES = BT == 256 ? 5 : 8;  // token stages and operand slots
   static constexpr int W_STAGES = BT == 256 ? 3 : 5;
-  static constexpr int A_SLOTS = 8;
-  static constexpr int A_COL0 = 256;
-  static constexpr size_t SMEM = (size_t)B_STAGES * B_BYTES + W_STAGES * W_BYTES +
+  static constexpr int PARTIAL_BYTES = BT == 256 ? 0 : BW * BT * 4;  // over the ring, at the end
+  static constexpr size_t SMEM = (size_t)STAGES * B_BYTES + W_STAGES * W_BYTES +
                                  NUM_EPI_WARPS * (BT / 2) * 4 + 512 + 1024;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
+  static_assert(PARTIAL_BYTES <= STAGES * B_BYTES, "partial sums fit the token ring");
+  static_assert(A_COL0 + STAGES * A_SLOT_COLS <= 512, "tensor memory");
   // kind::f16: FP32 accumulator (bit 4), A = B = FP16 (0), both K-major, N >> 3 at bit 17,
   // M >> 4 at bit 24
   static constexpr uint32_t IDESC =
@@ -70,6 +93,7 @@ struct Params {
   void* C;
   int64_t ldc;
   int32_t c_f32;
+  int32_t csize;      // CTAs that share a tile's K (1 where tiles fill the GPU)
   int32_t* err;
 };
 
@@ -101,25 +125,52 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     if (globaltimer_ns() - t0 > kWaitLimitNs) break;
 }
 
+// What a thread does with the finished sums of its weight row: scale, bias, gate, round, store.
+template <bool GATED>
+struct Out {
+  void* C;
+  int64_t ldc;
+  int32_t n;       // output column of this lane
+  bool nvalid, c_f32;
+  float sw, bias;  // of the lane's weight row
+  int lane;
+
+  __device__ __forceinline__ float value(float sum, float sa) const {
+    return fmaf(sum, sa * sw, bias);
+  }
+  // (gated) lanes 0-15 hold the gate rows and finish the first of two tokens, lanes 16-31 the up
+  // rows and finish the second
+  __device__ __forceinline__ float gate(float a, float b) const {
+    const bool odd = lane >= 16;
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 16);
+    const float g = odd ? other : a, u = odd ? b : other;
+    return __fdividef(g, 1.f + __expf(-g)) * u;
+  }
+  __device__ __forceinline__ void put(int64_t m, float v) const {
+    if (c_f32)
+      static_cast<float*>(C)[m * ldc + n] = v;
+    else
+      static_cast<__nv_bfloat16*>(C)[m * ldc + n] = __float2bfloat16_rn(v);
+  }
+};
+
 template <int BT, bool GATED>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_int8_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmW, const Params p) {
   using GE = Geo<BT>;
-  constexpr int B_STAGES = GE::B_STAGES, W_STAGES = GE::W_STAGES, A_SLOTS = GE::A_SLOTS;
+  constexpr int STAGES = GE::STAGES, W_STAGES = GE::W_STAGES;
   constexpr int TILE_COLS = GATED ? BW / 2 : BW;  // output columns of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sB = smem;
-  uint8_t* sW = sB + B_STAGES * GE::B_BYTES;
+  uint8_t* sW = sB + STAGES * GE::B_BYTES;
   float* sScale = reinterpret_cast<float*>(sW + W_STAGES * W_BYTES);  // [8 warps][BT/2]
-  uint64_t* b_full = reinterpret_cast<uint64_t*>(sScale + NUM_EPI_WARPS * (BT / 2));
-  uint64_t* b_empty = b_full + B_STAGES;
-  uint64_t* w_full = b_empty + B_STAGES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sScale + NUM_EPI_WARPS * (BT / 2));
+  uint64_t* empty = full + STAGES;
+  uint64_t* w_full = empty + STAGES;
   uint64_t* w_empty = w_full + W_STAGES;
-  uint64_t* a_full = w_empty + W_STAGES;
-  uint64_t* a_empty = a_full + A_SLOTS;
-  uint64_t* acc_full = a_empty + A_SLOTS;
+  uint64_t* acc_full = w_empty + W_STAGES;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* final_bar = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
@@ -128,17 +179,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < B_STAGES; ++s) {
-      mbar_init(&b_full[s], 1);
-      mbar_init(&b_empty[s], 1);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1 + NUM_CVT_WARPS / 2);  // the tokens' copy and four converter warps
+      mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < W_STAGES; ++s) {
       mbar_init(&w_full[s], 1);
       mbar_init(&w_empty[s], NUM_CVT_WARPS);
-    }
-    for (int s = 0; s < A_SLOTS; ++s) {
-      mbar_init(&a_full[s], NUM_CVT_WARPS / 2);
-      mbar_init(&a_empty[s], 1);
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, NUM_EPI_WARPS);
@@ -158,60 +205,64 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  // set-up above overlaps the previous kernel's tail; every global access comes after this
-  pdl_wait();
+  // The previous kernel on the stream is this call's own quantiser (or widener), which waited for
+  // everything before it: the weights may be read while it runs, and only what needs its output
+  // (tokens, scales) or writes C waits for it.
 
+  const int csize = p.csize;
+  const int rank = (int)(blockIdx.x % csize);
+  const int64_t cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
   const int64_t num_tiles = (int64_t)p.num_m_tiles * p.num_n_tiles;
-  const int KB = (p.K + KA - 1) / KA;  // token stages and operand slots per tile
-  const int KWB = (p.K + KW - 1) / KW;
+  // this CTA's k stages of every tile, in weight stages of two
+  const int KWB = (p.K + KW - 1) / KW, kw_per = (KWB + csize - 1) / csize;
+  const int kw_beg = min(KWB, rank * kw_per), kw_end = min(KWB, kw_beg + kw_per);
+  const int kb_beg = 2 * kw_beg, kb_end = min((p.K + KA - 1) / KA, 2 * kw_end);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ tokens
-    if (lane == 0) {
+  if (warp < CVT_WARP0) {
+    regs_dec<MISC_REGS>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- tokens
+      pdl_wait();
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
         const int32_t m0 = (int32_t)(t / p.num_n_tiles) * BT;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(&b_empty[stage], phase ^ 1u, abort_flag, p.err)) {
+        for (int kb = kb_beg; kb < kb_end; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&b_full[stage], GE::B_BYTES);
-          tma_load_2d(sB + stage * GE::B_BYTES, &tmA, &b_full[stage], kb * KA, m0);
+          mbar_arrive_expect_tx(&full[stage], GE::B_BYTES);
+          tma_load_2d(sB + stage * GE::B_BYTES, &tmA, &full[stage], kb * KA, m0);
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == B_STAGES) {
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      for (int s = 0; s < B_STAGES; ++s)
-        if (issued & (1u << s)) drain_wait(&b_full[s], (issued_phase >> s) & 1u);
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ weights
-    if (lane == 0) {
+      // (after a wait that gave up, a stage may also lack its converters: bounded either way)
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) drain_wait(&full[s], (issued_phase >> s) & 1u);
+    } else if (warp == 2 && lane == 0) {
+      // ---------------------------------------------------------- weights
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
         const int32_t n0 = (int32_t)(t % p.num_n_tiles) * TILE_COLS;
-        for (int kb = 0; kb < KWB; ++kb) {
+        for (int kb = kw_beg; kb < kw_end; ++kb) {
           if (!mbar_wait(&w_empty[stage], phase ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&w_full[stage], W_BYTES);
-          if constexpr (GATED) {
-            tma_load_2d(sW + stage * W_BYTES, &tmW, &w_full[stage], kb * KW, n0);
+          tma_load_2d(sW + stage * W_BYTES, &tmW, &w_full[stage], kb * KW, n0);
+          if constexpr (GATED)
             tma_load_2d(sW + stage * W_BYTES + W_BYTES / 2, &tmW, &w_full[stage], kb * KW,
                         p.cols + n0);
-          } else {
-            tma_load_2d(sW + stage * W_BYTES, &tmW, &w_full[stage], kb * KW, n0);
-          }
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == W_STAGES) {
@@ -222,18 +273,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       for (int s = 0; s < W_STAGES; ++s)
         if (issued & (1u << s)) drain_wait(&w_full[s], (issued_phase >> s) & 1u);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, sphase = 0, acc_phase = 0;
+    } else if (warp == 1 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
         if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, p.err)) break;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(&b_full[stage], phase, abort_flag, p.err) ||
-              !mbar_wait(&a_full[slot], sphase, abort_flag, p.err)) {
+        for (int kb = kb_beg; kb < kb_end; ++kb) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, p.err)) {
             ok = false;
             break;
           }
@@ -241,18 +289,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint32_t b0 = smem_u32(sB + stage * GE::B_BYTES);
 #pragma unroll
           for (int s = 0; s < KA / 16; ++s)
-            tc_mma_f16_tmem_a(tbase, tbase + GE::A_COL0 + slot * A_SLOT_COLS + 8 * s,
+            tc_mma_f16_tmem_a(tbase, tbase + A_COL0 + stage * A_SLOT_COLS + 8 * s,
                               smem_desc(b0 + s * 32, 16, 1024, 2), GE::IDESC,
-                              (kb | s) != 0 ? 1u : 0u);
-          tc_commit(&b_empty[stage]);
-          tc_commit(&a_empty[slot]);
-          if (++stage == B_STAGES) {
+                              kb != kb_beg || s != 0 ? 1u : 0u);
+          tc_commit(&empty[stage]);
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
-          }
-          if (++slot == A_SLOTS) {
-            slot = 0;
-            sphase ^= 1u;
           }
         }
         if (!ok) break;
@@ -262,24 +305,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_commit(final_bar);
       drain_wait(final_bar, 0);
     }
-  } else if (warp >= CVT_WARP0 && warp < EPI_WARP0) {
+  } else if (warp < EPI_WARP0) {
     // ------------------------------------------------------------ converters
+    regs_dec<CVT_REGS>();
     const int q = warp & 3, half = (warp - CVT_WARP0) >> 2;
     const int row = GATED ? (lane < 16 ? 16 * q + lane : 64 + 16 * q + lane - 16) : 32 * q + lane;
     const uint32_t roff = (uint32_t)row * KW, rx = row & 7;
-    int stage = 0, slot = half;  // this half's next operand slot: slots advance in k order
-    uint32_t phase = 0, sphase = 0;
+    int wstage = 0, slot = half;  // this half's next operand slot: slots advance in k order
+    uint32_t wphase = 0, phase = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
-      for (int kb = 0; kb < KB; kb += 2) {
-        if (!mbar_wait(&w_full[stage], phase, abort_flag, p.err)) {
+    for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
+      for (int kb = kb_beg; kb < kb_end; kb += 2) {
+        if (!mbar_wait(&w_full[wstage], wphase, abort_flag, p.err)) {
           ok = false;
           break;
         }
-        const bool live = kb + half < KB;
+        const bool live = kb + half < kb_end;
         uint32_t v[32];
         if (live) {
-          const uint32_t src = smem_u32(sW + stage * W_BYTES) + roff;
+          const uint32_t src = smem_u32(sW + wstage * W_BYTES) + roff;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint4 x = lds128(src + (((uint32_t)(4 * half + c) ^ rx) << 4));
@@ -290,103 +334,184 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&w_empty[stage]);
+        if (lane == 0) mbar_arrive(&w_empty[wstage]);
         if (live) {
-          if (!mbar_wait(&a_empty[slot], sphase ^ 1u, abort_flag, p.err)) {
+          if (!mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          tc_st_32x32b_x32(tbase + ((uint32_t)(32 * q) << 16) + GE::A_COL0 + slot * A_SLOT_COLS, v);
+          tc_st_32x32b_x32(tbase + ((uint32_t)(32 * q) << 16) + A_COL0 + slot * A_SLOT_COLS, v);
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&a_full[slot]);
+          if (lane == 0) mbar_arrive(&full[slot]);
         }
-        if (++stage == W_STAGES) {
-          stage = 0;
+        if (++wstage == W_STAGES) {
+          wstage = 0;
+          wphase ^= 1u;
+        }
+        // both halves move on by the number of slots this weight stage filled
+        slot += kb + 1 < kb_end ? 2 : 1;
+        if (slot >= STAGES) {
+          slot -= STAGES;
           phase ^= 1u;
-        }
-        // the pair of slots moves on by the number of halves this stage had
-        const int step = kb + 1 < KB ? 2 : 1;
-        slot += step;
-        if (slot >= A_SLOTS) {
-          slot -= A_SLOTS;
-          sphase ^= 1u;
         }
       }
     }
-  } else if (warp >= EPI_WARP0) {
+  } else {
     // ------------------------------------------------------------ epilogue
+    regs_inc<EPI_REGS>();
+    pdl_wait();
     const int q = warp & 3;                    // TMEM lane quadrant: 32 weight rows
     const int part = (warp - EPI_WARP0) >> 2;  // tokens [part BT/2, + BT/2) of the tile
+    const uint32_t lane_base = (uint32_t)(32 * q) << 16;
     // the scales of this warp's tokens: kept per warp, so that no barrier among the epilogue
     // warps is needed (one that gave up would leave the others waiting in it)
     float* sc = sScale + (warp - EPI_WARP0) * (BT / 2);
+    Out<GATED> out{};
+    out.C = p.C;
+    out.ldc = p.ldc;
+    out.c_f32 = p.c_f32;
+    out.lane = lane;
     uint32_t acc_phase = 0;
-    for (int64_t t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+    for (int64_t t = cluster; t < num_tiles; t += clusters) {
       const int64_t m0 = (t / p.num_n_tiles) * BT;
-      const int32_t n0 = (int32_t)(t % p.num_n_tiles) * TILE_COLS;
-      // output column of this lane, and the weight row its accumulator belongs to
-      const int32_t n = n0 + (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
-      const bool nvalid = n < p.cols;
-      const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + n : n;
-      const float sw = nvalid ? __ldg(p.w_scale + wrow) : 0.f;
-      const float bias =
-          p.bias && nvalid ? __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16) : 0.f;
+      out.n = (int32_t)(t % p.num_n_tiles) * TILE_COLS + (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
+      out.nvalid = out.n < p.cols;
+      const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + out.n : out.n;
+      out.sw = out.nvalid ? __ldg(p.w_scale + wrow) : 0.f;
+      out.bias = p.bias && out.nvalid ? __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16) : 0.f;
       __syncwarp();  // the previous tile's scales have been read
+      const int64_t mw = m0 + part * (BT / 2);  // first token of this warp
 #pragma unroll
-      for (int i = lane; i < BT / 2; i += 32) {
-        const int64_t m = m0 + part * (BT / 2) + i;
-        sc[i] = m < p.M ? __ldg(p.a_scale + m) : 0.f;
-      }
+      for (int i = lane; i < BT / 2; i += 32) sc[i] = mw + i < p.M ? __ldg(p.a_scale + mw + i) : 0.f;
       __syncwarp();
       if (!mbar_wait(acc_full, acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
       acc_phase ^= 1u;
-      constexpr int CHUNKS = BT / 64;
-#pragma unroll 1
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int col0 = part * (BT / 2) + 32 * c;
-        uint32_t r[32];
-        tc_ld_32x32b_x32(tbase + ((uint32_t)(32 * q) << 16) + col0, r);
-        tc_wait_ld();
-        if (c == CHUNKS - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(acc_empty);
-        }
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          v[i] = fmaf(__uint_as_float(r[i]), sc[32 * c + i] * sw, bias);
-        const int64_t left = p.M - (m0 + col0);  // tokens of this chunk
+      const uint32_t acc = tbase + lane_base + part * (BT / 2);
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+      };
+      // two tokens' sums -> the lane's finished value(s)
+      auto pair = [&](uint32_t r0, uint32_t r1, int i, float& a, float& b) {
+        const float2 s2 = *reinterpret_cast<const float2*>(sc + i);
+        a = out.value(__uint_as_float(r0), s2.x);
+        b = out.value(__uint_as_float(r1), s2.y);
+        if constexpr (GATED) a = out.gate(a, b);
+      };
+      const int64_t left = out.nvalid ? p.M - mw : 0;  // tokens to store
+      const int odd = lane >> 4;                        // (gated) which of two tokens this lane has
+      auto store_pair = [&](int i, float a, float b) {
         if constexpr (GATED) {
-          const int odd = lane >> 4;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 16);
-            const float g = odd ? other : v[i], u = odd ? v[i + 1] : other;
-            const float y = g / (1.f + expf(-g)) * u;
-            if (nvalid && i + odd < left)
-              static_cast<__nv_bfloat16*>(p.C)[(m0 + col0 + i + odd) * p.ldc + n] =
-                  __float2bfloat16_rn(y);
-          }
-        } else if (p.c_f32) {
-          float* out = static_cast<float*>(p.C) + (m0 + col0) * p.ldc + n;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (nvalid && i < left) out[i * p.ldc] = v[i];
+          if (i + odd < left) out.put(mw + i + odd, a);
         } else {
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + (m0 + col0) * p.ldc + n;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (nvalid && i < left) out[i * p.ldc] = __float2bfloat16_rn(v[i]);
+          if (i < left) out.put(mw + i, a);
+          if (i + 1 < left) out.put(mw + i + 1, b);
         }
+      };
+      constexpr int COLS = BT / 2;
+      constexpr int EARLY = COLS > 64 ? COLS - 64 : 0;  // finished before the release
+      static_assert(EARLY == 0 || EARLY == 64, "columns of a warp");
+      uint32_t packed[EARLY > 0 ? 32 : 1];
+      uint32_t r[2][32];
+      if constexpr (EARLY > 0) {
+        tc_ld_32x32b_x32(acc, r[0]);
+        tc_ld_32x32b_x32(acc + 32, r[1]);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          float a, b = 0.f;
+          pair(r[i / 32][i % 32], r[i / 32][i % 32 + 1], i, a, b);
+          if (p.c_f32)
+            store_pair(i, a, b);  // FP32 results are not held back
+          else
+            packed[i / 2] = pack_bf16x2(a, b);
+        }
+      }
+      tc_ld_32x32b_x32(acc + EARLY, r[0]);
+      if constexpr (COLS > 32) tc_ld_32x32b_x32(acc + EARLY + 32, r[1]);
+      tc_wait_ld();
+      if (csize > 1) {
+        // ---------------------------------------------------------- K split over the cluster
+        // sums of [token][row], over the token ring, which every MMA has read
+        if constexpr (BT < 256) {
+          float* sum = reinterpret_cast<float*>(sB) + (int64_t)part * COLS * BW + 32 * q + lane;
+#pragma unroll
+          for (int i = 0; i < COLS; ++i) sum[i * BW] = __uint_as_float(r[i / 32][i % 32]);
+        }
+        release();
+        break;  // one tile per cluster; finished below, with every warp of the CTAs
+      }
+      release();
+      if constexpr (EARLY > 0) {
+        if (!p.c_f32) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            const float a = __uint_as_float(packed[i / 2] << 16);
+            const float b = __uint_as_float(packed[i / 2] & 0xFFFF0000u);
+            store_pair(i, a, b);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < COLS - EARLY; i += 2) {
+        float a, b = 0.f;
+        pair(r[i / 32][i % 32], r[i / 32][i % 32 + 1], EARLY + i, a, b);
+        store_pair(EARLY + i, a, b);
       }
     }
   }
 
+  if constexpr (BT < 256) {
+    if (csize > 1) {
+      // every CTA's sums are in its shared memory; this one finishes tokens rank, rank + csize, ..
+      // of the tile (in pairs), adding the slices in rank order
+      __syncwarp();  // single-lane roles have left their warps apart
+      cluster_sync();
+      if (warp >= EPI_WARP0 && *abort_flag == 0) {
+        const int q = warp & 3, w = (warp - EPI_WARP0) >> 2;
+        const int64_t m0 = (cluster / p.num_n_tiles) * BT;
+        Out<GATED> out{};
+        out.C = p.C;
+        out.ldc = p.ldc;
+        out.c_f32 = p.c_f32;
+        out.lane = lane;
+        out.n = (int32_t)(cluster % p.num_n_tiles) * TILE_COLS +
+                (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
+        out.nvalid = out.n < p.cols;
+        const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + out.n : out.n;
+        out.sw = out.nvalid ? __ldg(p.w_scale + wrow) : 0.f;
+        out.bias =
+            p.bias && out.nvalid ? __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16) : 0.f;
+        const int tokens = (int)min64(BT, p.M - m0);
+        for (int i = 2 * (rank + csize * w); i < tokens; i += 4 * csize) {
+          float s0 = 0.f, s1 = 0.f;
+          for (int c = 0; c < csize; ++c) {
+            const uint32_t a = mapa_shared(smem_u32(sB) + (uint32_t)(i * BW + 32 * q + lane) * 4, c);
+            s0 += ld_shared_cluster_f32(a);
+            s1 += ld_shared_cluster_f32(a + BW * 4);
+          }
+          const bool second = i + 1 < tokens;
+          float a = out.value(s0, __ldg(p.a_scale + m0 + i));
+          const float b = out.value(s1, second ? __ldg(p.a_scale + m0 + i + 1) : 0.f);
+          if constexpr (GATED) {
+            a = out.gate(a, b);
+            const int odd = lane >> 4;
+            if (out.nvalid && (second || !odd)) out.put(m0 + i + odd, a);
+          } else if (out.nvalid) {
+            out.put(m0 + i, a);
+            if (second) out.put(m0 + i + 1, b);
+          }
+        }
+      }
+      __syncwarp();
+      cluster_sync();  // nobody leaves while its sums are read
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -445,21 +570,48 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   p.ldc = pr.ldc;
   p.c_f32 = pr.c_f32;
   p.err = err;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      gemm_int8_tc_kernel<BT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GE::SMEM);
-  if (attr != cudaSuccess) return QW_ERR_CUDA;
+  static const bool ready = [] {
+    cudaFuncAttributes fa{};
+    return cudaFuncSetAttribute(gemm_int8_tc_kernel<BT, GATED>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)GE::SMEM) == cudaSuccess &&
+           cudaFuncGetAttributes(&fa, gemm_int8_tc_kernel<BT, GATED>) == cudaSuccess &&
+           fa.numRegs >= LAUNCH_REGS;  // the register split depends on it
+  }();
+  if (!ready) return QW_ERR_CUDA;
   const int64_t tiles = (int64_t)p.num_n_tiles * p.num_m_tiles;
   const int sms = device_sm_count();
-  return launch_pdl(gemm_int8_tc_kernel<BT, GATED>, dim3((unsigned)(tiles < sms ? tiles : sms)),
-                    dim3(NUM_THREADS), GE::SMEM, st, tmA, tmW, p);
+  // a tile's K is split while the CTAs still fit the GPU at once and keep 1024 k each
+  int csize = 1;
+  if (BT < 256)
+    while (csize < 8 && tiles * csize * 2 <= sms && pr.K / (csize * 2) >= 1024) csize *= 2;
+  p.csize = csize;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(csize > 1 || tiles < sms ? tiles * csize : sms));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = GE::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)csize;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = csize > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, gemm_int8_tc_kernel<BT, GATED>, tmA, tmW, p) == cudaSuccess
+             ? QW_OK
+             : QW_ERR_CUDA;
 }
 
 }  // namespace
 
 qw_status launch_gemm_int8_tc(const Int8Problem& p, const void* codes16, bool gated, int32_t* err,
                               cudaStream_t st) {
-  if (p.M <= 64) return gated ? launch<64, true>(p, codes16, err, st) : launch<64, false>(p, codes16, err, st);
-  if (p.M <= 128) return gated ? launch<128, true>(p, codes16, err, st) : launch<128, false>(p, codes16, err, st);
+  if (p.M <= 64)
+    return gated ? launch<64, true>(p, codes16, err, st) : launch<64, false>(p, codes16, err, st);
+  if (p.M <= 128)
+    return gated ? launch<128, true>(p, codes16, err, st) : launch<128, false>(p, codes16, err, st);
   return gated ? launch<256, true>(p, codes16, err, st) : launch<256, false>(p, codes16, err, st);
 }
 

@@ -16,16 +16,15 @@ namespace {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// A signed 8-bit integer as its FP16 number's bits (exact).
-__device__ __forceinline__ uint32_t f16_of(float q) {
-  return (uint32_t)__half_as_ushort(__float2half_rn(q));
-}
+// x rounded to an integer (ties to even), |x| < 2^22: adding 1.5 * 2^23 rounds at the units.
+// The sum's low bits are the integer in two's complement.
+constexpr float kRound = 12582912.f;
 
 // Row r of A -> codes (INT8, or the same integers as FP16 for the tensor cores) and the row's
-// scale.  One CTA per row.  A thread keeps its part of rows of up to 256 x 8 vectors of 16 bytes
-// (K <= 16384) in registers, so the row is read once; what lies beyond is read a second time.
-constexpr int QTHREADS = 256, QVEC = 8;
-template <bool F16>
+// scale.  One CTA per row.  A thread keeps VEC 16-byte vectors of the row (K <= 2048 VEC) in
+// registers, so the row is read once; what lies beyond is read a second time.
+constexpr int QTHREADS = 256;
+template <bool F16, int VEC>
 __global__ void __launch_bounds__(QTHREADS)
     quantize_int8_kernel(const uint16_t* __restrict__ A, int64_t lda, int32_t K,
                          void* __restrict__ Q, float* __restrict__ S, int32_t* err) {
@@ -34,7 +33,7 @@ __global__ void __launch_bounds__(QTHREADS)
   const int64_t r = blockIdx.x;
   const uint4* src = reinterpret_cast<const uint4*>(A + r * lda);
   const int n8 = K / 8;
-  uint4 keep[QVEC];
+  uint4 keep[VEC];
   uint32_t amax = 0;  // largest |v| as BF16 bits (finite values order like their bit patterns)
   auto fold = [&](const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -42,13 +41,13 @@ __global__ void __launch_bounds__(QTHREADS)
     for (int j = 0; j < 4; ++j) amax = max(amax, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
   };
 #pragma unroll
-  for (int j = 0; j < QVEC; ++j) {
+  for (int j = 0; j < VEC; ++j) {
     const int i = threadIdx.x + j * QTHREADS;
     keep[j] = i < n8 ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int j = 0; j < QVEC; ++j) fold(keep[j]);
-  for (int i = threadIdx.x + QVEC * QTHREADS; i < n8; i += QTHREADS) fold(__ldg(src + i));
+  for (int j = 0; j < VEC; ++j) fold(keep[j]);
+  for (int i = threadIdx.x + VEC * QTHREADS; i < n8; i += QTHREADS) fold(__ldg(src + i));
   __shared__ uint32_t part[QTHREADS / 32];
   amax = __reduce_max_sync(0xFFFFFFFFu, amax);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
@@ -58,36 +57,46 @@ __global__ void __launch_bounds__(QTHREADS)
   for (int i = 1; i < QTHREADS / 32; ++i) amax = max(amax, part[i]);
   const float top = __uint_as_float(amax << 16);
   const bool finite = amax < 0x7F80u;
-  const float inv = finite ? fminf(127.0f / top, 3.4028234663852886e38f) : 0.f;
+  const float inv = fminf(127.0f / top, 3.4028234663852886e38f);
   if (threadIdx.x == 0) {
     S[r] = finite ? top / 127.0f : __uint_as_float(0x7FC00000u);
     if (!finite) set_error(err, QW_ERR_VALUE);
   }
-  auto put = [&](int i, const uint4& v) {
+  auto put = [&](int i, uint4 v) {
+    if (!finite) v = make_uint4(0, 0, 0, 0);  // codes 0 (0 * inv is 0: inv is finite there too)
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // the product is rounded to FP32 before the code is (no fused multiply-add)
+      q[2 * j] = __fadd_rn(__fmul_rn(bf16_lo(w[j]), inv), kRound);
+      q[2 * j + 1] = __fadd_rn(__fmul_rn(bf16_hi(w[j]), inv), kRound);
+    }
     if constexpr (F16) {
       uint32_t o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[j] = finite ? f16_of(rintf(bf16_lo(w[j]) * inv)) | (f16_of(rintf(bf16_hi(w[j]) * inv)) << 16)
-                      : 0u;
+      for (int j = 0; j < 4; ++j) {
+        const __half2 h = __floats2half2_rn(q[2 * j] - kRound, q[2 * j + 1] - kRound);
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
       reinterpret_cast<uint4*>(Q)[r * (K / 8) + i] = make_uint4(o[0], o[1], o[2], o[3]);
     } else {
-      uint32_t o[2] = {0, 0};
+      uint32_t o[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int q = finite ? __float2int_rn(((j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1])) * inv) : 0;
-        o[j >> 2] |= ((uint32_t)q & 0xFFu) << (8 * (j & 3));
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t lo = __byte_perm(__float_as_uint(q[4 * j]), __float_as_uint(q[4 * j + 1]), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(q[4 * j + 2]), __float_as_uint(q[4 * j + 3]), 0x0040);
+        o[j] = __byte_perm(lo, hi, 0x5410);
       }
       reinterpret_cast<uint2*>(Q)[r * (K / 8) + i] = make_uint2(o[0], o[1]);
     }
   };
 #pragma unroll
-  for (int j = 0; j < QVEC; ++j) {
+  for (int j = 0; j < VEC; ++j) {
     const int i = threadIdx.x + j * QTHREADS;
     if (i < n8) put(i, keep[j]);
   }
-  for (int i = threadIdx.x + QVEC * QTHREADS; i < n8; i += QTHREADS) put(i, __ldg(src + i));
+  for (int i = threadIdx.x + VEC * QTHREADS; i < n8; i += QTHREADS) put(i, __ldg(src + i));
 }
 
 // INT8 codes [M][lda] -> the same integers as FP16 [M][K]; a thread takes 16 codes at a time.
@@ -302,11 +311,10 @@ qw_status launch_gemv(const Int8Problem& p, bool early, cudaStream_t st) {
 qw_status launch_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, void* Q,
                                float* scale, bool f16, int32_t* err, cudaStream_t st) {
   const uint16_t* a = static_cast<const uint16_t*>(A);
-  if (f16)
-    return launch_pdl(quantize_int8_kernel<true>, dim3((unsigned)rows), dim3(QTHREADS), 0, st, a,
-                      lda, K, Q, scale, err);
-  return launch_pdl(quantize_int8_kernel<false>, dim3((unsigned)rows), dim3(QTHREADS), 0, st, a,
-                    lda, K, Q, scale, err);
+  const bool wide = K > 2 * 8 * QTHREADS;
+  auto* kern = f16 ? (wide ? quantize_int8_kernel<true, 8> : quantize_int8_kernel<true, 2>)
+                   : (wide ? quantize_int8_kernel<false, 8> : quantize_int8_kernel<false, 2>);
+  return launch_pdl(kern, dim3((unsigned)rows), dim3(QTHREADS), 0, st, a, lda, K, Q, scale, err);
 }
 
 qw_status launch_widen_int8(const void* A, int64_t lda, int64_t M, int32_t K, void* Q,
