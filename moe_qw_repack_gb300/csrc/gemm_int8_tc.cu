@@ -12,10 +12,10 @@
 //   warp 2      TMA producer of the weights: INT8, 128 rows x 128 k a stage of their own ring;
 //   warp 1      TMEM owner and MMA issuer: weights are the A operand, read from tensor memory,
 //               tokens the B operand, read from shared memory;
-//   warps 4-11  converters: warp w covers TMEM lanes 32 (w % 4) .. + 31 and one 64-k half of a
-//               weight stage; a lane takes 64 codes of its own row, makes them FP16 (byte b ->
-//               the FP16 number 1024 + (b + 128), minus 1152: exact) and stores them as the
-//               MMA's A operand with one tcgen05.st;
+//   warps 4-11  converters: warp w covers TMEM lanes 32 (w % 4) .. + 31 of every second weight
+//               stage; a lane takes the 128 codes of its own row, makes them FP16 (byte b -> the
+//               FP16 number 1024 + (b + 128), minus 1152: exact) and stores them as the MMA's A
+//               operand with one tcgen05.st for each of two operand slots;
 //   warps 12-19 epilogue: tcgen05.ld the accumulator (a lane holds one weight row, a register
 //               one token), release it, scale, add bias, (gated) exchange gate and up, round and
 //               store while the next tile's MMAs run.  They take registers from the other warps
@@ -50,9 +50,12 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr int A_SLOT_COLS = KA / 2;  // 32-bit columns of one operand slot
 constexpr int A_COL0 = 256;          // the accumulator uses columns [0, BT)
 
+// BF16 results of 16 tokens x 32 columns on their way from a lane per column to 16-byte stores
+constexpr int STAGE_OUT = 16 * 32 * 2;
+
 // Registers: launched with 96 a thread, then shared out by warpgroup (sum below what the launch
 // holds; launch() checks that the kernel was compiled to LAUNCH_REGS).
-constexpr int LAUNCH_REGS = 96, MISC_REGS = 40, CVT_REGS = 72, EPI_REGS = 144;
+constexpr int LAUNCH_REGS = 96, MISC_REGS = 40, CVT_REGS = 80, EPI_REGS = 136;
 static_assert(128 * MISC_REGS + NUM_CVT_WARPS * 32 * CVT_REGS + NUM_EPI_WARPS * 32 * EPI_REGS <=
                   NUM_THREADS * LAUNCH_REGS,
               "a split above the launch's registers would wait forever");
@@ -72,7 +75,7 @@ struct Geo {
   static constexpr int W_STAGES = BT == 256 ? 3 : 5;
   static constexpr int PARTIAL_BYTES = BT == 256 ? 0 : BW * BT * 4;  // over the ring, at the end
   static constexpr size_t SMEM = (size_t)STAGES * B_BYTES + W_STAGES * W_BYTES +
-                                 NUM_EPI_WARPS * (BT / 2) * 4 + 512 + 1024;
+                                 NUM_EPI_WARPS * (STAGE_OUT + BT / 2 * 4) + 512 + 1024;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
   static_assert(PARTIAL_BYTES <= STAGES * B_BYTES, "partial sums fit the token ring");
   static_assert(A_COL0 + STAGES * A_SLOT_COLS <= 512, "tensor memory");
@@ -93,6 +96,7 @@ struct Params {
   void* C;
   int64_t ldc;
   int32_t c_f32;
+  int32_t c_vec;      // rows of C start on 16-byte boundaries
   int32_t csize;      // CTAs that share a tile's K (1 where tiles fill the GPU)
   int32_t* err;
 };
@@ -119,6 +123,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "r"(addr));
   return v;
 }
+// one lane of the warp (converged), the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity))
@@ -130,8 +142,11 @@ template <bool GATED>
 struct Out {
   void* C;
   int64_t ldc;
+  int32_t cols;    // output columns in all
+  int32_t n_first; // first output column of the warp
   int32_t n;       // output column of this lane
   bool nvalid, c_f32;
+  bool vec;        // the warp's columns exist and can be stored 16 bytes at a time
   float sw, bias;  // of the lane's weight row
   int lane;
 
@@ -152,6 +167,74 @@ struct Out {
     else
       static_cast<__nv_bfloat16*>(C)[m * ldc + n] = __float2bfloat16_rn(v);
   }
+  // FP32 results (BT <= 128: for 256 tokens a tile the registers do not reach): 128 contiguous
+  // bytes a token as they are.
+  __device__ __forceinline__ void store_f32(const uint32_t (&r)[2][32], const float* sc, int step,
+                                            int64_t m, int64_t left) const {
+    float* o = static_cast<float*>(C) + m * ldc + n;
+    const int count = nvalid ? (int)min64(left, step) : 0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+      if (i < count) *o = value(__uint_as_float(r[i / 32][i % 32]), sc[i]);
+      o += ldc;
+    }
+  }
+  // Sums of STEP tokens -> BF16, two to a register: tokens 2j and 2j + 1, or (gated) what the lane
+  // has of the token pairs 2j and 2j + 1.
+  template <int STEP>
+  __device__ __forceinline__ void pack(const uint32_t (&r)[2][32], const float* sc,
+                                       uint32_t (&packed)[STEP / (GATED ? 4 : 2)]) const {
+#pragma unroll
+    for (int i = 0; i < STEP; i += 4) {
+      const float4 s = *reinterpret_cast<const float4*>(sc + i);
+      const float a = value(__uint_as_float(r[i / 32][i % 32]), s.x);
+      const float b = value(__uint_as_float(r[i / 32][i % 32 + 1]), s.y);
+      const float c = value(__uint_as_float(r[i / 32][i % 32 + 2]), s.z);
+      const float d = value(__uint_as_float(r[i / 32][i % 32 + 3]), s.w);
+      if constexpr (GATED) {
+        packed[i / 4] = pack_bf16x2(gate(a, b), gate(c, d));
+      } else {
+        packed[i / 2] = pack_bf16x2(a, b);
+        packed[i / 2 + 1] = pack_bf16x2(c, d);
+      }
+    }
+  }
+  // ... to memory, 16 tokens at a time through the warp's 1 KB at `stage`: [token][column], a lane
+  // writing its column and reading 8 columns of a token.
+  template <int STEP>
+  __device__ __forceinline__ void store(const uint32_t (&packed)[STEP / (GATED ? 4 : 2)], int64_t m,
+                                        int64_t left, uint8_t* stage) const {
+    constexpr int W = GATED ? 16 : 32;             // columns of the warp
+    constexpr int REGS = GATED ? 4 : 8;            // registers of 16 tokens
+    constexpr int APART = GATED ? 2 * W : W;       // between a register's two values
+    uint16_t* st = reinterpret_cast<uint16_t*>(stage);
+    uint16_t* o = static_cast<uint16_t*>(C) + m * ldc + n_first;
+#pragma unroll
+    for (int g = 0; g < STEP / 16; ++g, o += 16 * ldc) {
+      const int count = (int)min64(left - 16 * g, 16);
+      if (count <= 0) break;
+      __syncwarp();  // the previous 16 tokens have been read
+#pragma unroll
+      for (int i = 0; i < REGS; ++i) {
+        const uint32_t v = packed[g * REGS + i];
+        st[2 * i * APART + lane] = (uint16_t)v;  // (gated: lanes 16-31 land in the next token)
+        st[(2 * i + 1) * APART + lane] = (uint16_t)(v >> 16);
+      }
+      __syncwarp();
+      if (vec) {
+#pragma unroll
+        for (int j = 0; j < W / 16; ++j) {
+          const int e = (j * 32 + lane) * 8, tok = e / W, col = e % W;  // 8 columns of token tok
+          if (tok < count)
+            *reinterpret_cast<uint4*>(o + tok * ldc + col) = *reinterpret_cast<const uint4*>(st + e);
+        }
+      } else {
+#pragma unroll 1
+        for (int e = lane; e < count * W; e += 32)
+          if (n_first + e % W < cols) o[(e / W) * ldc + e % W] = st[e];
+      }
+    }
+  }
 };
 
 template <int BT, bool GATED>
@@ -165,7 +248,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sB = smem;
   uint8_t* sW = sB + STAGES * GE::B_BYTES;
-  float* sScale = reinterpret_cast<float*>(sW + W_STAGES * W_BYTES);  // [8 warps][BT/2]
+  uint8_t* sOut = sW + W_STAGES * W_BYTES;                                       // [8 warps]
+  float* sScale = reinterpret_cast<float*>(sOut + NUM_EPI_WARPS * STAGE_OUT);  // [8 warps][BT/2]
   uint64_t* full = reinterpret_cast<uint64_t*>(sScale + NUM_EPI_WARPS * (BT / 2));
   uint64_t* empty = full + STAGES;
   uint64_t* w_full = empty + STAGES;
@@ -185,7 +269,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int s = 0; s < W_STAGES; ++s) {
       mbar_init(&w_full[s], 1);
-      mbar_init(&w_empty[s], NUM_CVT_WARPS);
+      mbar_init(&w_empty[s], NUM_CVT_WARPS / 2);
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, NUM_EPI_WARPS);
@@ -273,8 +357,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       for (int s = 0; s < W_STAGES; ++s)
         if (issued & (1u << s)) drain_wait(&w_full[s], (issued_phase >> s) & 1u);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
+      // The whole warp runs the loop and one elected lane issues: descriptors, addresses and
+      // loop state then stay in uniform registers.  (With a single-lane loop a stage's issue took
+      // 600 cycles, more than its MMAs.)
+      const bool leader = elect_one();
+      const uint64_t desc0 = smem_desc(smem_u32(sB), 16, 1024, 2);
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -286,73 +375,89 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t b0 = smem_u32(sB + stage * GE::B_BYTES);
+          const uint64_t desc = desc0 + (uint32_t)(stage * (GE::B_BYTES >> 4));
+          const uint32_t a = tbase + A_COL0 + stage * A_SLOT_COLS;
+          if (leader) {
 #pragma unroll
-          for (int s = 0; s < KA / 16; ++s)
-            tc_mma_f16_tmem_a(tbase, tbase + A_COL0 + stage * A_SLOT_COLS + 8 * s,
-                              smem_desc(b0 + s * 32, 16, 1024, 2), GE::IDESC,
-                              kb != kb_beg || s != 0 ? 1u : 0u);
-          tc_commit(&empty[stage]);
+            for (int s = 0; s < KA / 16; ++s)  // 32 bytes of k: 2 in the descriptor's units
+              tc_mma_f16_tmem_a(tbase, a + 8 * s, desc + 2 * s, GE::IDESC,
+                                kb != kb_beg || s != 0 ? 1u : 0u);
+            tc_commit(&empty[stage]);
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        tc_commit(acc_full);
+        if (leader) tc_commit(acc_full);
+        __syncwarp();
         acc_phase ^= 1u;
       }
-      tc_commit(final_bar);
-      drain_wait(final_bar, 0);
+      if (leader) {
+        tc_commit(final_bar);
+        drain_wait(final_bar, 0);
+      }
     }
   } else if (warp < EPI_WARP0) {
     // ------------------------------------------------------------ converters
     regs_dec<CVT_REGS>();
-    const int q = warp & 3, half = (warp - CVT_WARP0) >> 2;
+    const int q = warp & 3, group = (warp - CVT_WARP0) >> 2;
     const int row = GATED ? (lane < 16 ? 16 * q + lane : 64 + 16 * q + lane - 16) : 32 * q + lane;
     const uint32_t roff = (uint32_t)row * KW, rx = row & 7;
-    int wstage = 0, slot = half;  // this half's next operand slot: slots advance in k order
-    uint32_t wphase = 0, phase = 0;
+    int wstage = 0, slot = 0;
+    uint32_t wphase = 0, phase = 0, wi = 0;  // wi: weight stages so far
     bool ok = true;
     for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
-      for (int kb = kb_beg; kb < kb_end; kb += 2) {
-        if (!mbar_wait(&w_full[wstage], wphase, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
-        const bool live = kb + half < kb_end;
-        uint32_t v[32];
-        if (live) {
-          const uint32_t src = smem_u32(sW + wstage * W_BYTES) + roff;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 x = lds128(src + (((uint32_t)(4 * half + c) ^ rx) << 4));
-            int8x4_to_f16x2(x.x, v[8 * c + 0], v[8 * c + 1]);
-            int8x4_to_f16x2(x.y, v[8 * c + 2], v[8 * c + 3]);
-            int8x4_to_f16x2(x.z, v[8 * c + 4], v[8 * c + 5]);
-            int8x4_to_f16x2(x.w, v[8 * c + 6], v[8 * c + 7]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&w_empty[wstage]);
-        if (live) {
-          if (!mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.err)) {
+      for (int kb = kb_beg; kb < kb_end; kb += 2, ++wi) {
+        const bool two = kb + 1 < kb_end;  // operand slots of this weight stage: two, or one
+        if ((int)(wi & 1u) == group) {
+          if (!mbar_wait(&w_full[wstage], wphase, abort_flag, p.err)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          tc_st_32x32b_x32(tbase + ((uint32_t)(32 * q) << 16) + A_COL0 + slot * A_SLOT_COLS, v);
-          tc_wait_st();
-          tc_fence_before();
+          uint4 x[8];
+          const uint32_t src = smem_u32(sW + wstage * W_BYTES) + roff;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] = lds128(src + (((uint32_t)c ^ rx) << 4));
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[slot]);
+          if (lane == 0) mbar_arrive(&w_empty[wstage]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && !two) break;
+            int sl = slot + h;
+            uint32_t ph = phase;
+            if (sl >= STAGES) {
+              sl -= STAGES;
+              ph ^= 1u;
+            }
+            uint32_t v[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              int8x4_to_f16x2(x[4 * h + c].x, v[8 * c + 0], v[8 * c + 1]);
+              int8x4_to_f16x2(x[4 * h + c].y, v[8 * c + 2], v[8 * c + 3]);
+              int8x4_to_f16x2(x[4 * h + c].z, v[8 * c + 4], v[8 * c + 5]);
+              int8x4_to_f16x2(x[4 * h + c].w, v[8 * c + 6], v[8 * c + 7]);
+            }
+            if (!mbar_wait(&empty[sl], ph ^ 1u, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            tc_st_32x32b_x32(tbase + ((uint32_t)(32 * q) << 16) + A_COL0 + sl * A_SLOT_COLS, v);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[sl]);
+          }
+          if (!ok) break;
         }
         if (++wstage == W_STAGES) {
           wstage = 0;
           wphase ^= 1u;
         }
-        // both halves move on by the number of slots this weight stage filled
-        slot += kb + 1 < kb_end ? 2 : 1;
+        slot += two ? 2 : 1;
         if (slot >= STAGES) {
           slot -= STAGES;
           phase ^= 1u;
@@ -372,13 +477,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     Out<GATED> out{};
     out.C = p.C;
     out.ldc = p.ldc;
+    out.cols = p.cols;
     out.c_f32 = p.c_f32;
     out.lane = lane;
     uint32_t acc_phase = 0;
     for (int64_t t = cluster; t < num_tiles; t += clusters) {
       const int64_t m0 = (t / p.num_n_tiles) * BT;
-      out.n = (int32_t)(t % p.num_n_tiles) * TILE_COLS + (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
+      out.n_first = (int32_t)(t % p.num_n_tiles) * TILE_COLS + (GATED ? 16 : 32) * q;
+      out.n = out.n_first + (GATED ? lane & 15 : lane);
       out.nvalid = out.n < p.cols;
+      out.vec = p.c_vec && out.n_first + (GATED ? 16 : 32) <= p.cols;
       const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + out.n : out.n;
       out.sw = out.nvalid ? __ldg(p.w_scale + wrow) : 0.f;
       out.bias = p.bias && out.nvalid ? __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16) : 0.f;
@@ -396,72 +504,42 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty);
       };
-      // two tokens' sums -> the lane's finished value(s)
-      auto pair = [&](uint32_t r0, uint32_t r1, int i, float& a, float& b) {
-        const float2 s2 = *reinterpret_cast<const float2*>(sc + i);
-        a = out.value(__uint_as_float(r0), s2.x);
-        b = out.value(__uint_as_float(r1), s2.y);
-        if constexpr (GATED) a = out.gate(a, b);
-      };
-      const int64_t left = out.nvalid ? p.M - mw : 0;  // tokens to store
-      const int odd = lane >> 4;                        // (gated) which of two tokens this lane has
-      auto store_pair = [&](int i, float a, float b) {
-        if constexpr (GATED) {
-          if (i + odd < left) out.put(mw + i + odd, a);
-        } else {
-          if (i < left) out.put(mw + i, a);
-          if (i + 1 < left) out.put(mw + i + 1, b);
-        }
-      };
-      constexpr int COLS = BT / 2;
-      constexpr int EARLY = COLS > 64 ? COLS - 64 : 0;  // finished before the release
-      static_assert(EARLY == 0 || EARLY == 64, "columns of a warp");
-      uint32_t packed[EARLY > 0 ? 32 : 1];
+      // 64 tokens at a time, in a loop that is kept short (fully unrolled for 128 tokens, the
+      // epilogue spent most of its time fetching instructions).  The first 64 are rounded and
+      // packed, which frees their registers for the others; then the accumulator is released,
+      // and only then does anything go to memory.
+      constexpr int COLS = BT / 2, STEP = COLS < 64 ? COLS : 64;
       uint32_t r[2][32];
-      if constexpr (EARLY > 0) {
-        tc_ld_32x32b_x32(acc, r[0]);
-        tc_ld_32x32b_x32(acc + 32, r[1]);
+      auto load = [&](int c0) {
+        tc_ld_32x32b_x32(acc + c0, r[0]);
+        if constexpr (STEP > 32) tc_ld_32x32b_x32(acc + c0 + 32, r[1]);
         tc_wait_ld();
+        if (c0 + STEP == COLS) release();
+      };
+      load(0);
+      if constexpr (BT < 256) {
+        if (csize > 1) {
+          // K split over the cluster: sums of [token][row] over the token ring, which every MMA
+          // has read; finished below, with every warp of the CTAs
+          float* sum = reinterpret_cast<float*>(sB) + (int64_t)(part * COLS) * BW + 32 * q + lane;
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          float a, b = 0.f;
-          pair(r[i / 32][i % 32], r[i / 32][i % 32 + 1], i, a, b);
-          if (p.c_f32)
-            store_pair(i, a, b);  // FP32 results are not held back
-          else
-            packed[i / 2] = pack_bf16x2(a, b);
+          for (int i = 0; i < STEP; ++i) sum[i * BW] = __uint_as_float(r[i / 32][i % 32]);
+          break;  // one tile per cluster
         }
       }
-      tc_ld_32x32b_x32(acc + EARLY, r[0]);
-      if constexpr (COLS > 32) tc_ld_32x32b_x32(acc + EARLY + 32, r[1]);
-      tc_wait_ld();
-      if (csize > 1) {
-        // ---------------------------------------------------------- K split over the cluster
-        // sums of [token][row], over the token ring, which every MMA has read
-        if constexpr (BT < 256) {
-          float* sum = reinterpret_cast<float*>(sB) + (int64_t)part * COLS * BW + 32 * q + lane;
-#pragma unroll
-          for (int i = 0; i < COLS; ++i) sum[i * BW] = __uint_as_float(r[i / 32][i % 32]);
-        }
-        release();
-        break;  // one tile per cluster; finished below, with every warp of the CTAs
-      }
-      release();
-      if constexpr (EARLY > 0) {
-        if (!p.c_f32) {
-#pragma unroll
-          for (int i = 0; i < 64; i += 2) {
-            const float a = __uint_as_float(packed[i / 2] << 16);
-            const float b = __uint_as_float(packed[i / 2] & 0xFFFF0000u);
-            store_pair(i, a, b);
+#pragma unroll 1
+      for (int c0 = 0; c0 < COLS; c0 += STEP) {
+        const int64_t m = mw + c0, left = p.M - m;  // tokens of this step
+        if constexpr (!GATED && BT < 256) {
+          if (p.c_f32) {
+            out.store_f32(r, sc, STEP, m, left);
+            break;  // one step: COLS <= 64
           }
         }
-      }
-#pragma unroll
-      for (int i = 0; i < COLS - EARLY; i += 2) {
-        float a, b = 0.f;
-        pair(r[i / 32][i % 32], r[i / 32][i % 32 + 1], EARLY + i, a, b);
-        store_pair(EARLY + i, a, b);
+        uint32_t packed[STEP / (GATED ? 4 : 2)];
+        out.template pack<STEP>(r, sc + c0, packed);
+        if (c0 + STEP < COLS) load(c0 + STEP);
+        out.template store<STEP>(packed, m, left, sOut + (warp - EPI_WARP0) * STAGE_OUT);
       }
     }
   }
@@ -569,6 +647,7 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   p.C = pr.C;
   p.ldc = pr.ldc;
   p.c_f32 = pr.c_f32;
+  p.c_vec = pr.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(pr.C) % 16 == 0;
   p.err = err;
   static const bool ready = [] {
     cudaFuncAttributes fa{};
@@ -610,7 +689,7 @@ qw_status launch_gemm_int8_tc(const Int8Problem& p, const void* codes16, bool ga
                               cudaStream_t st) {
   if (p.M <= 64)
     return gated ? launch<64, true>(p, codes16, err, st) : launch<64, false>(p, codes16, err, st);
-  if (p.M <= 128)
+  if (p.M <= 128 || p.c_f32)
     return gated ? launch<128, true>(p, codes16, err, st) : launch<128, false>(p, codes16, err, st);
   return gated ? launch<256, true>(p, codes16, err, st) : launch<256, false>(p, codes16, err, st);
 }
