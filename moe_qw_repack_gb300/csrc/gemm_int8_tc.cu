@@ -50,9 +50,6 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr int A_SLOT_COLS = KA / 2;  // 32-bit columns of one operand slot
 constexpr int A_COL0 = 256;          // the accumulator uses columns [0, BT)
 
-// BF16 results of 16 tokens x 32 columns on their way from a lane per column to 16-byte stores
-constexpr int STAGE_OUT = 16 * 32 * 2;
-
 // Registers: launched with 96 a thread, then shared out by warpgroup (sum below what the launch
 // holds; launch() checks that the kernel was compiled to LAUNCH_REGS).
 constexpr int LAUNCH_REGS = 96, MISC_REGS = 40, CVT_REGS = 80, EPI_REGS = 136;
@@ -75,7 +72,7 @@ struct Geo {
   static constexpr int W_STAGES = BT == 256 ? 3 : 5;
   static constexpr int PARTIAL_BYTES = BT == 256 ? 0 : BW * BT * 4;  // over the ring, at the end
   static constexpr size_t SMEM = (size_t)STAGES * B_BYTES + W_STAGES * W_BYTES +
-                                 NUM_EPI_WARPS * (STAGE_OUT + BT / 2 * 4) + 512 + 1024;
+                                 NUM_EPI_WARPS * (BT / 2) * 4 + 512 + 1024;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
   static_assert(PARTIAL_BYTES <= STAGES * B_BYTES, "partial sums fit the token ring");
   static_assert(A_COL0 + STAGES * A_SLOT_COLS <= 512, "tensor memory");
@@ -96,7 +93,6 @@ struct Params {
   void* C;
   int64_t ldc;
   int32_t c_f32;
-  int32_t c_vec;      // rows of C start on 16-byte boundaries
   int32_t csize;      // CTAs that share a tile's K (1 where tiles fill the GPU)
   int32_t* err;
 };
@@ -142,11 +138,8 @@ template <bool GATED>
 struct Out {
   void* C;
   int64_t ldc;
-  int32_t cols;    // output columns in all
-  int32_t n_first; // first output column of the warp
   int32_t n;       // output column of this lane
   bool nvalid, c_f32;
-  bool vec;        // the warp's columns exist and can be stored 16 bytes at a time
   float sw, bias;  // of the lane's weight row
   int lane;
 
@@ -199,40 +192,22 @@ struct Out {
       }
     }
   }
-  // ... to memory, 16 tokens at a time through the warp's 1 KB at `stage`: [token][column], a lane
-  // writing its column and reading 8 columns of a token.
+  // ... to memory: a warp's 32 columns of a token are 64 contiguous bytes (gated: 16 of each of
+  // two tokens).  Through shared memory into 16-byte stores the same took five times as long: the
+  // detour costs more shared-memory passes than the narrow stores do.
   template <int STEP>
   __device__ __forceinline__ void store(const uint32_t (&packed)[STEP / (GATED ? 4 : 2)], int64_t m,
-                                        int64_t left, uint8_t* stage) const {
-    constexpr int W = GATED ? 16 : 32;             // columns of the warp
-    constexpr int REGS = GATED ? 4 : 8;            // registers of 16 tokens
-    constexpr int APART = GATED ? 2 * W : W;       // between a register's two values
-    uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-    uint16_t* o = static_cast<uint16_t*>(C) + m * ldc + n_first;
+                                        int64_t left) const {
+    constexpr int APART = GATED ? 2 : 1;  // tokens between a register's two values
+    uint16_t* o = static_cast<uint16_t*>(C) + (m + (GATED ? lane >> 4 : 0)) * ldc + n;
+    const int count = nvalid ? (int)min64(left, STEP) - (GATED ? lane >> 4 : 0) : 0;
+    const int64_t apart = APART * ldc;
 #pragma unroll
-    for (int g = 0; g < STEP / 16; ++g, o += 16 * ldc) {
-      const int count = (int)min64(left - 16 * g, 16);
-      if (count <= 0) break;
-      __syncwarp();  // the previous 16 tokens have been read
-#pragma unroll
-      for (int i = 0; i < REGS; ++i) {
-        const uint32_t v = packed[g * REGS + i];
-        st[2 * i * APART + lane] = (uint16_t)v;  // (gated: lanes 16-31 land in the next token)
-        st[(2 * i + 1) * APART + lane] = (uint16_t)(v >> 16);
-      }
-      __syncwarp();
-      if (vec) {
-#pragma unroll
-        for (int j = 0; j < W / 16; ++j) {
-          const int e = (j * 32 + lane) * 8, tok = e / W, col = e % W;  // 8 columns of token tok
-          if (tok < count)
-            *reinterpret_cast<uint4*>(o + tok * ldc + col) = *reinterpret_cast<const uint4*>(st + e);
-        }
-      } else {
-#pragma unroll 1
-        for (int e = lane; e < count * W; e += 32)
-          if (n_first + e % W < cols) o[(e / W) * ldc + e % W] = st[e];
-      }
+    for (int i = 0; i < STEP / (GATED ? 4 : 2); ++i) {
+      if (2 * i * APART < count) *o = (uint16_t)packed[i];
+      o += apart;
+      if ((2 * i + 1) * APART < count) *o = (uint16_t)(packed[i] >> 16);
+      o += apart;
     }
   }
 };
@@ -248,8 +223,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sB = smem;
   uint8_t* sW = sB + STAGES * GE::B_BYTES;
-  uint8_t* sOut = sW + W_STAGES * W_BYTES;                                       // [8 warps]
-  float* sScale = reinterpret_cast<float*>(sOut + NUM_EPI_WARPS * STAGE_OUT);  // [8 warps][BT/2]
+  float* sScale = reinterpret_cast<float*>(sW + W_STAGES * W_BYTES);  // [8 warps][BT/2]
   uint64_t* full = reinterpret_cast<uint64_t*>(sScale + NUM_EPI_WARPS * (BT / 2));
   uint64_t* empty = full + STAGES;
   uint64_t* w_full = empty + STAGES;
@@ -477,16 +451,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     Out<GATED> out{};
     out.C = p.C;
     out.ldc = p.ldc;
-    out.cols = p.cols;
     out.c_f32 = p.c_f32;
     out.lane = lane;
     uint32_t acc_phase = 0;
     for (int64_t t = cluster; t < num_tiles; t += clusters) {
       const int64_t m0 = (t / p.num_n_tiles) * BT;
-      out.n_first = (int32_t)(t % p.num_n_tiles) * TILE_COLS + (GATED ? 16 : 32) * q;
-      out.n = out.n_first + (GATED ? lane & 15 : lane);
+      out.n = (int32_t)(t % p.num_n_tiles) * TILE_COLS + (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
       out.nvalid = out.n < p.cols;
-      out.vec = p.c_vec && out.n_first + (GATED ? 16 : 32) <= p.cols;
       const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + out.n : out.n;
       out.sw = out.nvalid ? __ldg(p.w_scale + wrow) : 0.f;
       out.bias = p.bias && out.nvalid ? __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16) : 0.f;
@@ -539,7 +510,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t packed[STEP / (GATED ? 4 : 2)];
         out.template pack<STEP>(r, sc + c0, packed);
         if (c0 + STEP < COLS) load(c0 + STEP);
-        out.template store<STEP>(packed, m, left, sOut + (warp - EPI_WARP0) * STAGE_OUT);
+        out.template store<STEP>(packed, m, left);
       }
     }
   }
@@ -647,7 +618,6 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   p.C = pr.C;
   p.ldc = pr.ldc;
   p.c_f32 = pr.c_f32;
-  p.c_vec = pr.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(pr.C) % 16 == 0;
   p.err = err;
   static const bool ready = [] {
     cudaFuncAttributes fa{};
