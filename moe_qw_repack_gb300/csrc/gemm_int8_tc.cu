@@ -51,8 +51,10 @@ constexpr int A_SLOT_COLS = KA / 2;  // 32-bit columns of one operand slot
 constexpr int A_COL0 = 256;          // the accumulator uses columns [0, BT)
 
 // Registers: launched with 96 a thread, then shared out by warpgroup (sum below what the launch
-// holds; launch() checks that the kernel was compiled to LAUNCH_REGS).
-constexpr int LAUNCH_REGS = 96, MISC_REGS = 40, CVT_REGS = 80, EPI_REGS = 136;
+// holds; launch() checks that the kernel was compiled to LAUNCH_REGS).  No role may call a
+// subroutine, whose registers do not follow its warpgroup's share: a 64-bit division is one, so
+// tiles are counted in 32 bits and stepped by additions.
+constexpr int LAUNCH_REGS = 96, MISC_REGS = 56, CVT_REGS = 72, EPI_REGS = 136;
 static_assert(128 * MISC_REGS + NUM_CVT_WARPS * 32 * CVT_REGS + NUM_EPI_WARPS * 32 * EPI_REGS <=
                   NUM_THREADS * LAUNCH_REGS,
               "a split above the launch's registers would wait forever");
@@ -263,14 +265,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  __syncwarp();
   // The previous kernel on the stream is this call's own quantiser (or widener), which waited for
   // everything before it: the weights may be read while it runs, and only what needs its output
   // (tokens, scales) or writes C waits for it.
 
   const int csize = p.csize;
-  const int rank = (int)(blockIdx.x % csize);
-  const int64_t cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
-  const int64_t num_tiles = (int64_t)p.num_m_tiles * p.num_n_tiles;
+  const int rank = (int)(blockIdx.x % (unsigned)csize);
+  const uint32_t cluster = blockIdx.x / (unsigned)csize, clusters = gridDim.x / (unsigned)csize;
+  const uint32_t num_n = (uint32_t)p.num_n_tiles, num_tiles = (uint32_t)p.num_m_tiles * num_n;
+  // tile t = mt num_n + nt: the first of this cluster, and the step to its next
+  struct Tile {
+    uint32_t t, mt, nt;
+  };
+  const Tile first{cluster, cluster / num_n, cluster % num_n};
+  const uint32_t step_m = clusters / num_n, step_n = clusters % num_n;
+  auto next = [&](Tile& x) {
+    x.t += clusters;
+    x.mt += step_m;
+    x.nt += step_n;
+    if (x.nt >= num_n) {
+      x.nt -= num_n;
+      ++x.mt;
+    }
+  };
   // this CTA's k stages of every tile, in weight stages of two
   const int KWB = (p.K + KW - 1) / KW, kw_per = (KWB + csize - 1) / csize;
   const int kw_beg = min(KWB, rank * kw_per), kw_end = min(KWB, kw_beg + kw_per);
@@ -284,8 +302,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
-        const int32_t m0 = (int32_t)(t / p.num_n_tiles) * BT;
+      for (Tile x = first; ok && x.t < num_tiles; next(x)) {
+        const int32_t m0 = (int32_t)(x.mt * BT);
         for (int kb = kb_beg; kb < kb_end; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) {
             ok = false;
@@ -309,8 +327,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
-        const int32_t n0 = (int32_t)(t % p.num_n_tiles) * TILE_COLS;
+      for (Tile x = first; ok && x.t < num_tiles; next(x)) {
+        const int32_t n0 = (int32_t)(x.nt * TILE_COLS);
         for (int kb = kw_beg; kb < kw_end; ++kb) {
           if (!mbar_wait(&w_empty[stage], phase ^ 1u, abort_flag, p.err)) {
             ok = false;
@@ -341,7 +359,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
+      for (Tile x = first; ok && x.t < num_tiles; next(x)) {
         if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, p.err)) break;
         for (int kb = kb_beg; kb < kb_end; ++kb) {
           if (!mbar_wait(&full[stage], phase, abort_flag, p.err)) {
@@ -383,7 +401,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int wstage = 0, slot = 0;
     uint32_t wphase = 0, phase = 0, wi = 0;  // wi: weight stages so far
     bool ok = true;
-    for (int64_t t = cluster; ok && t < num_tiles; t += clusters) {
+    for (Tile x = first; ok && x.t < num_tiles; next(x)) {
       for (int kb = kb_beg; kb < kb_end; kb += 2, ++wi) {
         const bool two = kb + 1 < kb_end;  // operand slots of this weight stage: two, or one
         if ((int)(wi & 1u) == group) {
@@ -391,10 +409,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ok = false;
             break;
           }
-          uint4 x[8];
+          uint4 w[8];
           const uint32_t src = smem_u32(sW + wstage * W_BYTES) + roff;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = lds128(src + (((uint32_t)c ^ rx) << 4));
+          for (int c = 0; c < 8; ++c) w[c] = lds128(src + (((uint32_t)c ^ rx) << 4));
           __syncwarp();
           if (lane == 0) mbar_arrive(&w_empty[wstage]);
 #pragma unroll
@@ -409,16 +427,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t v[32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              int8x4_to_f16x2(x[4 * h + c].x, v[8 * c + 0], v[8 * c + 1]);
-              int8x4_to_f16x2(x[4 * h + c].y, v[8 * c + 2], v[8 * c + 3]);
-              int8x4_to_f16x2(x[4 * h + c].z, v[8 * c + 4], v[8 * c + 5]);
-              int8x4_to_f16x2(x[4 * h + c].w, v[8 * c + 6], v[8 * c + 7]);
+              int8x4_to_f16x2(w[4 * h + c].x, v[8 * c + 0], v[8 * c + 1]);
+              int8x4_to_f16x2(w[4 * h + c].y, v[8 * c + 2], v[8 * c + 3]);
+              int8x4_to_f16x2(w[4 * h + c].z, v[8 * c + 4], v[8 * c + 5]);
+              int8x4_to_f16x2(w[4 * h + c].w, v[8 * c + 6], v[8 * c + 7]);
             }
             if (!mbar_wait(&empty[sl], ph ^ 1u, abort_flag, p.err)) {
               ok = false;
               break;
             }
             tc_fence_after();
+            __syncwarp();  // .sync.aligned wants the whole warp, and every lane waited by itself
             tc_st_32x32b_x32(tbase + ((uint32_t)(32 * q) << 16) + A_COL0 + sl * A_SLOT_COLS, v);
             tc_wait_st();
             tc_fence_before();
@@ -454,9 +473,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     out.c_f32 = p.c_f32;
     out.lane = lane;
     uint32_t acc_phase = 0;
-    for (int64_t t = cluster; t < num_tiles; t += clusters) {
-      const int64_t m0 = (t / p.num_n_tiles) * BT;
-      out.n = (int32_t)(t % p.num_n_tiles) * TILE_COLS + (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
+    for (Tile x = first; x.t < num_tiles; next(x)) {
+      const int64_t m0 = (int64_t)x.mt * BT;
+      out.n = (int32_t)(x.nt * TILE_COLS) + (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
       out.nvalid = out.n < p.cols;
       const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + out.n : out.n;
       out.sw = out.nvalid ? __ldg(p.w_scale + wrow) : 0.f;
@@ -482,6 +501,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       constexpr int COLS = BT / 2, STEP = COLS < 64 ? COLS : 64;
       uint32_t r[2][32];
       auto load = [&](int c0) {
+        __syncwarp();  // .sync.aligned wants the whole warp, and every lane waited by itself
         tc_ld_32x32b_x32(acc + c0, r[0]);
         if constexpr (STEP > 32) tc_ld_32x32b_x32(acc + c0 + 32, r[1]);
         tc_wait_ld();
@@ -523,13 +543,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       cluster_sync();
       if (warp >= EPI_WARP0 && *abort_flag == 0) {
         const int q = warp & 3, w = (warp - EPI_WARP0) >> 2;
-        const int64_t m0 = (cluster / p.num_n_tiles) * BT;
+        const int64_t m0 = (int64_t)first.mt * BT;
         Out<GATED> out{};
         out.C = p.C;
         out.ldc = p.ldc;
         out.c_f32 = p.c_f32;
         out.lane = lane;
-        out.n = (int32_t)(cluster % p.num_n_tiles) * TILE_COLS +
+        out.n = (int32_t)(first.nt * TILE_COLS) +
                 (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
         out.nvalid = out.n < p.cols;
         const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + out.n : out.n;
@@ -561,10 +581,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       cluster_sync();  // nobody leaves while its sums are read
     }
   }
+  __syncwarp();  // single-lane roles have left their warps apart
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
+    __syncwarp();
     tmem_dealloc(tbase, TMEM_COLS);
   }
 }
@@ -630,6 +652,7 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   if (!ready) return QW_ERR_CUDA;
   const int64_t tiles = (int64_t)p.num_n_tiles * p.num_m_tiles;
   const int sms = device_sm_count();
+  if (tiles > 0x7FFFFFFF - sms) return QW_ERR_UNSUPPORTED;  // counted in 32 bits
   // a tile's K is split while the CTAs still fit the GPU at once and keep 1024 k each
   int csize = 1;
   if (BT < 256)
