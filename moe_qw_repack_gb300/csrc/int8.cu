@@ -121,187 +121,180 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// ------------------------------------------------------------------ up to 16 tokens
+// ------------------------------------------------------------------ one or two tokens
 // The weights are streamed once; integer sums are exact, so any order gives the same result.
-// A CTA of four warps takes RB blocks of 16 weight rows (gated: 16 gate rows and the 16 up rows
-// of the same outputs) and a slice of K; its warps take 64 x U bytes of every row in turn.  A lane
-// of mma.m16n8k32 (s8) owns rows g and g + 8 and, as k may be permuted if both operands agree,
-// 16 consecutive bytes of each per two MMAs: weights and tokens come in 16-byte loads in
-// fragment order, with nothing staged.  Partial sums meet in shared memory, those of a K split
-// over a cluster's CTAs in rank 0's.
-constexpr int GW = 4, GTHREADS = GW * 32;
+// A CTA of four warps takes R = 4 RW weight rows (gated: gate rows and the up rows of the same
+// outputs) and a slice of at most SLICE of their k.  Its rows arrive in shared memory by bulk
+// copies that one warp issues before anything else, so that all of a CTA's bytes are in flight
+// at once, however few its threads; a lane then multiplies 16 consecutive k of RW rows with the
+// same k of every token (dp4a), and one warp reduction per row and token ends the slice.  Partial
+// sums of slices meet in rank 0 of a cluster.
+constexpr int GW = 4, GTHREADS = GW * 32, SLICE = 4096;
 
-__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                       uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint4 ldg_stream(const int8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
+struct GemvShape {
+  int32_t len;     // k of a slice (a multiple of 16)
+  int32_t slices;
+  int32_t csize;   // CTAs that share a block of rows
+};
 
-template <int NT, int RB, bool GATED>
-__global__ void __launch_bounds__(GTHREADS, 8)
-    gemv_int8_kernel(const Int8Problem p, const int csize, const bool early) {
-  static_assert(!GATED || RB == 2, "a gate block and its up block");
-  constexpr int U = 4 / RB / NT;              // steps of 64 k loaded at a time
-  constexpr int ROWS = GATED ? 16 : 16 * RB;  // outputs of a CTA
-  __shared__ int part[GW][RB][NT][128];
-  __shared__ int total[RB][NT][128];
+template <int MT, int RW, bool GATED>
+__global__ void __launch_bounds__(GTHREADS)
+    gemv_int8_kernel(const Int8Problem p, const GemvShape g, const bool early, int32_t* err) {
+  constexpr int R = GW * RW;                     // weight rows of a CTA
+  constexpr int OUTS = GATED ? R / 2 : R;        // outputs of a CTA
+  static_assert(!GATED || RW % 2 == 0, "a warp has its gate rows' up rows");
+  extern __shared__ __align__(128) uint8_t smem[];  // [R][pitch] weights
+  __shared__ uint64_t full;
+  __shared__ int abort_flag;
+  __shared__ int part[R * MT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int rank = csize > 1 ? (int)(blockIdx.x % csize) : 0;
+  const int rank = g.csize > 1 ? (int)(blockIdx.x % (unsigned)g.csize) : 0;
   const int32_t cols = GATED ? p.N / 2 : p.N;
-  const int32_t n0 = (int32_t)(blockIdx.x / csize) * ROWS;
+  const int32_t n0 = (int32_t)(blockIdx.x / (unsigned)g.csize) * OUTS;
+  const int pitch = (g.len + 511) / 512 * 512;
 
-  // this CTA's 64-k steps, and this lane's first byte of each of its rows
-  const int steps = (p.K + 63) / 64, per = (steps + csize - 1) / csize;
-  const int sbeg = min(steps, rank * per), send = min(steps, sbeg + per);
-  const int8_t* wp[RB][2];
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // rows past the last are read as the last and not stored
-      const int32_t n = min(n0 + (GATED ? 0 : 16 * b) + g + 8 * h, cols - 1);
-      wp[b][h] = p.W + ((int64_t)(GATED && b ? cols : 0) + n) * p.K + 16 * t;
-    }
-  const int8_t* xp[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) xp[i] = p.A + (int64_t)min((int64_t)(8 * i + g), p.M - 1) * p.lda + 16 * t;
-
-  int acc[RB][NT][4] = {};
-  uint4 w[U][RB][2], x[U][NT];
-  auto load_w = [&](int s0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = (s0 + u) * 64;
-          w[u][b][h] = s0 + u < send && k + 16 * t < p.K ? ldg_stream(wp[b][h] + k)
-                                                         : make_uint4(0, 0, 0, 0);
-        }
+  if (threadIdx.x == 0) {
+    mbar_init(&full, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  // Row i of the CTA: warp i / RW's row i % RW; gated: outputs n0 + (i / RW) RW / 2 + .., the gate
+  // rows in the first half of a warp's rows.  -1: no such row.
+  auto row_of = [&](int i) -> int64_t {
+    const int w = i / RW, r = i % RW;
+    const int32_t n = GATED ? n0 + w * (RW / 2) + r % (RW / 2) : n0 + i;
+    if (n >= cols) return -1;
+    return (GATED && r >= RW / 2) ? (int64_t)cols + n : n;
+  };
+  auto fetch = [&](int s) {  // warp 0
+    const int k0 = s * g.len, len = min(g.len, p.K - k0);
+    const int64_t row = lane < R ? row_of(lane) : -1;
+    const int rows = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
+    if (lane == 0) mbar_arrive_expect_tx(&full, (uint32_t)(rows * len));
+    __syncwarp();
+    if (row >= 0) bulk_load(smem + lane * pitch, p.W + row * p.K + k0, (uint32_t)len, &full);
   };
   // `early`: the previous kernel on the stream is this call's own quantiser, which waited for
   // everything before it; the weights may be read while it runs
-  if (early) load_w(sbeg + warp * U);
+  if (early && warp == 0) fetch(rank);
   pdl_wait();
   pdl_launch_dependents();
-  if (!early) load_w(sbeg + warp * U);
-  for (int s0 = sbeg + warp * U; s0 < send; s0 += GW * U) {
+  if (!early && warp == 0) fetch(rank);
+
+  int acc[RW][MT] = {};
+  uint32_t phase = 0;
+  for (int s = rank; s < g.slices; s += g.csize, phase ^= 1u) {
+    const int k0 = s * g.len, len = min(g.len, p.K - k0);
+    if (s != rank) {  // more slices than CTAs of the cluster: the buffer is used again
+      __syncthreads();
+      if (warp == 0) fetch(s);
+    }
+    // a lane's k of every token, for all of its warp's rows; zeros past the slice and the tokens
+    constexpr int XREG = SLICE / 512;
+    uint4 x[XREG][MT];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int j = 0; j < XREG; ++j)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int k = (s0 + u) * 64;
-        x[u][i] = s0 + u < send && k + 16 * t < p.K && 8 * i + g < p.M
-                      ? __ldg(reinterpret_cast<const uint4*>(xp[i] + k))
+      for (int m = 0; m < MT; ++m) {
+        const int k = j * 512 + lane * 16;
+        x[j][m] = k < len && m < p.M
+                      ? __ldg(reinterpret_cast<const uint4*>(p.A + m * p.lda + k0 + k))
                       : make_uint4(0, 0, 0, 0);
       }
+    (void)warp_wait(&full, phase, &abort_flag, err);
+    const uint8_t* wrow = smem + warp * RW * pitch + lane * 16;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int j = 0; j < XREG; ++j) {
+      if (j * 512 >= len) break;
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
+      for (int r = 0; r < RW; ++r) {
+        // (rows that do not exist, and k past the slice, hold anything: their products are
+        // not stored, or are with zeros)
+        const uint4 w = *reinterpret_cast<const uint4*>(wrow + r * pitch + j * 512);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          mma_s8(acc[b][i], w[u][b][0].x, w[u][b][1].x, w[u][b][0].y, w[u][b][1].y, x[u][i].x,
-                 x[u][i].y);
-          mma_s8(acc[b][i], w[u][b][0].z, w[u][b][1].z, w[u][b][0].w, w[u][b][1].w, x[u][i].z,
-                 x[u][i].w);
+        for (int m = 0; m < MT; ++m) {
+          acc[r][m] = __dp4a((int)w.x, (int)x[j][m].x, acc[r][m]);
+          acc[r][m] = __dp4a((int)w.y, (int)x[j][m].y, acc[r][m]);
+          acc[r][m] = __dp4a((int)w.z, (int)x[j][m].z, acc[r][m]);
+          acc[r][m] = __dp4a((int)w.w, (int)x[j][m].w, acc[r][m]);
         }
-    load_w(s0 + GW * U);
-  }
-
-  // element (row r, token c) of an accumulator at 16 c + r
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        part[warp][b][i][16 * (2 * t + (e & 1)) + g + 8 * (e >> 1)] = acc[b][i][e];
-  __syncthreads();
-  int sum[RB][NT];
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      sum[b][i] = 0;
-#pragma unroll
-      for (int v = 0; v < GW; ++v) sum[b][i] += part[v][b][i][threadIdx.x];
-    }
-  if (csize > 1) {
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) total[b][i][threadIdx.x] = sum[b][i];
-    cluster_sync();
-    if (rank == 0)
-      for (int c = 1; c < csize; ++c)
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-            sum[b][i] += __float_as_int(ld_shared_cluster_f32(
-                mapa_shared(smem_u32(&total[b][i][threadIdx.x]), (uint32_t)c)));
-    cluster_sync();
-    if (rank != 0) return;
-  }
-  const int r = threadIdx.x & 15;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int64_t m = 8 * i + (threadIdx.x >> 4);
-    if (m >= p.M) continue;
-    const float sa = p.a_scale[m];
-    float v[RB];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const int32_t n = n0 + (GATED ? 0 : 16 * b) + r;
-      if (n >= cols) continue;
-      const int64_t wr = (GATED && b ? cols : 0) + (int64_t)n;
-      v[b] = (float)sum[b][i] * (sa * __ldg(p.w_scale + wr));
-      if (p.bias) v[b] += __uint_as_float((uint32_t)__ldg(p.bias + wr) << 16);
-      if constexpr (!GATED) {
-        if (p.c_f32)
-          static_cast<float*>(p.C)[m * p.ldc + n] = v[b];
-        else
-          static_cast<__nv_bfloat16*>(p.C)[m * p.ldc + n] = __float2bfloat16_rn(v[b]);
       }
     }
-    if constexpr (GATED)
-      if (n0 + r < cols)
-        static_cast<__nv_bfloat16*>(p.C)[m * p.ldc + n0 + r] =
-            __float2bfloat16_rn(v[0] / (1.f + expf(-v[0])) * v[1]);
   }
+
+  // sum (row i, token m) of the slices this CTA had at i MT + m
+#pragma unroll
+  for (int r = 0; r < RW; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int v = __reduce_add_sync(0xFFFFFFFFu, acc[r][m]);
+      if (lane == 0) part[(warp * RW + r) * MT + m] = v;
+    }
+  if (g.csize > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (rank == 0) {
+    for (int i = threadIdx.x; i < OUTS * MT; i += GTHREADS) {
+      const int o = i / MT, m = i % MT;  // output n0 + o
+      const int32_t n = n0 + o;
+      if (n >= cols || m >= p.M) continue;
+      float v[GATED ? 2 : 1];
+#pragma unroll
+      for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        const int row = GATED ? o / (RW / 2) * RW + o % (RW / 2) + h * (RW / 2) : o;
+        int sum = part[row * MT + m];
+        for (int c = 1; c < g.csize; ++c)
+          sum += __float_as_int(
+              ld_shared_cluster_f32(mapa_shared(smem_u32(&part[row * MT + m]), (uint32_t)c)));
+        const int64_t wr = (int64_t)(h ? cols : 0) + n;
+        v[h] = (float)sum * (p.a_scale[m] * __ldg(p.w_scale + wr));
+        if (p.bias) v[h] += __uint_as_float((uint32_t)__ldg(p.bias + wr) << 16);
+      }
+      const float y = GATED ? v[0] / (1.f + expf(-v[0])) * v[GATED ? 1 : 0] : v[0];
+      if (p.c_f32)
+        static_cast<float*>(p.C)[m * p.ldc + n] = y;
+      else
+        static_cast<__nv_bfloat16*>(p.C)[m * p.ldc + n] = __float2bfloat16_rn(y);
+    }
+  }
+  if (g.csize > 1) cluster_sync();  // nobody leaves while its sums are read
 }
 
-template <int NT, int RB, bool GATED>
-qw_status launch_gemv(const Int8Problem& p, bool early, cudaStream_t st) {
-  const int32_t cols = GATED ? p.N / 2 : p.N, rows = GATED ? 16 : 16 * RB;
-  const int64_t blocks = ((int64_t)cols + rows - 1) / rows;
-  int csize = 1;
-  while (csize < 8 && blocks * csize < 4 * device_sm_count() && p.K / csize >= 2048) csize *= 2;
+template <int MT, int RW, bool GATED>
+qw_status launch_gemv(const Int8Problem& p, bool early, int32_t* err, cudaStream_t st) {
+  constexpr int R = GW * RW, OUTS = GATED ? R / 2 : R;
+  const int32_t cols = GATED ? p.N / 2 : p.N;
+  const int64_t blocks = ((int64_t)cols + OUTS - 1) / OUTS;
+  // slices of at most SLICE; shorter ones while the GPU is not full and each keeps 1024
+  int slices = (p.K + SLICE - 1) / SLICE;
+  while (slices < 8 && blocks * slices < 2 * device_sm_count() && p.K / (2 * slices) >= 1024)
+    slices *= 2;
+  GemvShape g;
+  g.len = ((p.K + slices - 1) / slices + 15) / 16 * 16;
+  g.slices = (p.K + g.len - 1) / g.len;
+  g.csize = g.slices < 8 ? g.slices : 8;
+  const int pitch = (g.len + 511) / 512 * 512;
+  constexpr int kMaxSmem = R * SLICE;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(gemv_int8_kernel<MT, RW, GATED>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (attr != cudaSuccess) return QW_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(blocks * csize));
+  cfg.gridDim = dim3((unsigned)(blocks * g.csize));
   cfg.blockDim = dim3(GTHREADS);
+  cfg.dynamicSmemBytes = (size_t)R * pitch;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)csize;
+  at[1].val.clusterDim.x = (unsigned)g.csize;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = csize > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemv_int8_kernel<NT, RB, GATED>, p, csize, early) == cudaSuccess
+  cfg.numAttrs = g.csize > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, gemv_int8_kernel<MT, RW, GATED>, p, g, early, err) == cudaSuccess
              ? QW_OK
              : QW_ERR_CUDA;
 }
@@ -324,10 +317,13 @@ qw_status launch_widen_int8(const void* A, int64_t lda, int64_t M, int32_t K, vo
                     static_cast<const int8_t*>(A), lda, M, K, static_cast<uint4*>(Q));
 }
 
-qw_status launch_gemv_int8(const Int8Problem& p, bool gated, bool early, cudaStream_t st) {
+qw_status launch_gemv_int8(const Int8Problem& p, bool gated, bool early, int32_t* err,
+                           cudaStream_t st) {
   if (gated)
-    return p.M <= 8 ? launch_gemv<1, 2, true>(p, early, st) : launch_gemv<2, 2, true>(p, early, st);
-  return p.M <= 8 ? launch_gemv<1, 1, false>(p, early, st) : launch_gemv<2, 2, false>(p, early, st);
+    return p.M == 1 ? launch_gemv<1, 2, true>(p, early, err, st)
+                    : launch_gemv<2, 2, true>(p, early, err, st);
+  return p.M == 1 ? launch_gemv<1, 2, false>(p, early, err, st)
+                  : launch_gemv<2, 2, false>(p, early, err, st);
 }
 
 }  // namespace qw

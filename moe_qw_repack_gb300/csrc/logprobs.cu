@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   for (int b = 0; b < nblk; ++b) {
     const uint4* blk = ring + (b % STAGES) * BLOCK + tid;
     const int v0 = vbeg + b * BLOCK + tid;
-    (void)mbar_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err);
+    (void)warp_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err);
     if (b == 0 && k > 0) {
       // the first bound: the k-th largest of the maxima of 32 groups, a group being what a
       // warp takes at a time (k different logits are at least that)

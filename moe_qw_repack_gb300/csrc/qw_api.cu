@@ -505,7 +505,7 @@ static qw_status int8_product(int32_t afmt, const void* A, int64_t lda, const fl
   }
   if (s != QW_OK) return s;
   return tensor ? launch_gemm_int8_tc(p, workspace, gated, d_err, st)
-                : launch_gemv_int8(p, gated, quantise, st);
+                : launch_gemv_int8(p, gated, quantise, d_err, st);
 }
 
 qw_status qgemm_int8(int32_t afmt, const void* A, int64_t lda, const float* a_scale,

@@ -102,6 +102,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The same wait by a whole warp, which leaves it together: the vote makes the result uniform and
+// joins the lanes, which may leave their polling one by one.  Without it a warp can go on in two
+// groups, and loop state that the compiler keeps in uniform registers (one copy for the warp) is
+// then stepped twice.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int32_t* err) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, err)) != 0;
+}
+
 // ------------------------------------------------------------------ thread-block clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
