@@ -12,15 +12,19 @@
 //   warp 2      TMA producer of the weights: INT8, 128 rows x 128 k a stage of their own ring;
 //   warp 1      TMEM owner and MMA issuer: weights are the A operand, read from tensor memory,
 //               tokens the B operand, read from shared memory;
-//   warps 4-11  converters: warp w covers TMEM lanes 32 (w % 4) .. + 31 and 32 of the 64 k of
-//               every operand slot; a lane takes codes of its own row, makes them FP16 (byte b ->
-//               the FP16 number 1024 + (b + 128), minus 1152: exact) and stores them as the MMA's
-//               A operand, one tcgen05.st for each of a weight stage's two slots;
+//   warps 4-11  converters in two groups that take weight stages in turn: warp w covers TMEM lanes
+//               32 (w % 4) .. + 31; a lane takes the 128 codes of its own row, makes them FP16
+//               (byte b -> the FP16 number 1024 + (b + 128), minus 1152: exact) and stores them as
+//               the MMA's A operand with one tcgen05.st for each of two operand slots.  (All eight
+//               warps on every slot pay a slot's waits twice as often: 318 us for 251.)
 //   warps 12-19 epilogue: tcgen05.ld the accumulator (a lane holds one weight row, a register
 //               one token), release it, scale, add bias, (gated) exchange gate and up, round and
-//               store while the next tile's MMAs run.
-// Who waits on a barrier sees every phase of it (a wait by parity cannot tell a phase from the one
-// two before): all converters take part in every slot, rather than groups of them in turn.
+//               store while the next tile's MMAs run.  They take registers from the other warps
+//               (setmaxnreg), so that half a tile's share and the packed other half fit.
+// Who waits on a barrier has to see every phase of it (a wait by parity cannot tell a phase from
+// the one two before).  So each weight buffer and each operand slot belongs to one converter group
+// for good: the rings are even in weight stages, and a weight stage always fills two slots (past K
+// both operands are zeros).
 // A token stage and an operand slot of tensor memory belong together: one barrier says that both
 // are full and one commit that both are free (a second commit per stage cost 8 % of the MMA rate).
 // The gated form gives each 32 TMEM lanes 16 gate rows and the 16 up rows of the same outputs,
@@ -51,11 +55,29 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr int A_SLOT_COLS = KA / 2;  // 32-bit columns of one operand slot
 constexpr int A_COL0 = 256;          // the accumulator uses columns [0, BT)
 
+// Registers: launched with 96 a thread, then shared out by warpgroup (the sum below is not above what
+// the launch holds; launch() checks that the kernel was compiled to LAUNCH_REGS).  No role calls a
+// subroutine, whose registers would not follow the share: a 64-bit division is one, so tiles are
+// counted in 32 bits and stepped by additions.
+constexpr int LAUNCH_REGS = 96, MISC_REGS = 56, CVT_REGS = 72, EPI_REGS = 136;
+static_assert(128 * MISC_REGS + NUM_CVT_WARPS * 32 * CVT_REGS + NUM_EPI_WARPS * 32 * EPI_REGS <=
+                  NUM_THREADS * LAUNCH_REGS,
+              "a split above the launch's registers would wait forever");
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int BT>
 struct Geo {
   static constexpr int B_BYTES = BT * KA * 2;
-  static constexpr int STAGES = BT == 256 ? 5 : 8;  // token stages and operand slots
-  static constexpr int W_STAGES = BT == 256 ? 3 : 5;
+  static constexpr int STAGES = BT == 256 ? 4 : 8;  // token stages and operand slots
+  static constexpr int W_STAGES = BT == 64 ? 6 : 4;
+  static_assert(STAGES % 4 == 0 && W_STAGES % 2 == 0, "one converter group to a slot and a buffer");
   static constexpr int PARTIAL_BYTES = BT == 256 ? 0 : BW * BT * 4;  // over the ring, at the end
   static constexpr size_t SMEM = (size_t)STAGES * B_BYTES + W_STAGES * W_BYTES +
                                  NUM_EPI_WARPS * (BT / 2) * 4 + 512 + 1024;
@@ -83,12 +105,16 @@ struct Params {
   int32_t* err;
 };
 
-__device__ __forceinline__ void tc_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() {
@@ -220,12 +246,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1 + NUM_CVT_WARPS);  // the tokens' copy and the converters
+      mbar_init(&full[s], 1 + NUM_CVT_WARPS / 2);  // the tokens' copy and a converter group
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < W_STAGES; ++s) {
       mbar_init(&w_full[s], 1);
-      mbar_init(&w_empty[s], NUM_CVT_WARPS);
+      mbar_init(&w_empty[s], NUM_CVT_WARPS / 2);
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, NUM_EPI_WARPS);
@@ -268,9 +294,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // this CTA's k stages of every tile, in weight stages of two
   const int KWB = (p.K + KW - 1) / KW, kw_per = (KWB + csize - 1) / csize;
   const int kw_beg = min(KWB, rank * kw_per), kw_end = min(KWB, kw_beg + kw_per);
-  const int kb_beg = 2 * kw_beg, kb_end = min((p.K + KA - 1) / KA, 2 * kw_end);
+  const int kb_beg = 2 * kw_beg, kb_end = 2 * kw_end;
 
   if (warp < CVT_WARP0) {
+    regs_dec<MISC_REGS>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- tokens
       int stage = 0;
@@ -368,62 +395,66 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp < EPI_WARP0) {
     // ------------------------------------------------------------ converters
-    const int q = warp & 3, kh = (warp - CVT_WARP0) >> 2;  // kh: which 32 k of a slot
+    regs_dec<CVT_REGS>();
+    const int q = warp & 3, group = (warp - CVT_WARP0) >> 2;
     const int row = GATED ? (lane < 16 ? 16 * q + lane : 64 + 16 * q + lane - 16) : 32 * q + lane;
     const uint32_t roff = (uint32_t)row * KW, rx = row & 7;
-    const uint32_t dst = tbase + ((uint32_t)(32 * q) << 16) + A_COL0 + 16 * kh;
-    int wstage = 0, slot = 0;
+    const uint32_t dst = tbase + ((uint32_t)(32 * q) << 16) + A_COL0;
+    // this group's next weight buffer and first operand slot, and their phases
+    int wstage = group, slot = 2 * group;
     uint32_t wphase = 0, phase = 0;
     bool ok = true;
+    int mine = group;  // weight stages until this group's next
     for (Tile x = first; ok && x.t < num_tiles; next(x)) {
-      for (int kb = kb_beg; ok && kb < kb_end; kb += 2) {
-        const int slots = min(2, kb_end - kb);  // operand slots of this weight stage
+      for (int kw = kw_beg; kw < kw_end; ++kw, mine ^= 1) {
+        if (mine) continue;
         if (!warp_wait(&w_full[wstage], wphase, abort_flag, p.err)) {
           ok = false;
           break;
         }
-        uint4 w[4];
+        uint4 w[8];
         const uint32_t src = smem_u32(sW + wstage * W_BYTES) + roff;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)  // 16-byte chunks 2 kh, 2 kh + 1 of each slot's four
-          w[c] = lds128(src + (((uint32_t)(4 * (c >> 1) + 2 * kh + (c & 1)) ^ rx) << 4));
-        uint32_t v[2][16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t* o = v[c >> 1] + 8 * (c & 1);
-          int8x4_to_f16x2(w[c].x, o[0], o[1]);
-          int8x4_to_f16x2(w[c].y, o[2], o[3]);
-          int8x4_to_f16x2(w[c].z, o[4], o[5]);
-          int8x4_to_f16x2(w[c].w, o[6], o[7]);
-        }
+        for (int c = 0; c < 8; ++c) w[c] = lds128(src + (((uint32_t)c ^ rx) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(&w_empty[wstage]);
-        if (++wstage == W_STAGES) {
-          wstage = 0;
+        wstage += 2;
+        if (wstage >= W_STAGES) {
+          wstage = group;
           wphase ^= 1u;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h == slots) break;
-          if (!warp_wait(&empty[slot], phase ^ 1u, abort_flag, p.err)) {
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            int8x4_to_f16x2(w[4 * h + c].x, v[8 * c + 0], v[8 * c + 1]);
+            int8x4_to_f16x2(w[4 * h + c].y, v[8 * c + 2], v[8 * c + 3]);
+            int8x4_to_f16x2(w[4 * h + c].z, v[8 * c + 4], v[8 * c + 5]);
+            int8x4_to_f16x2(w[4 * h + c].w, v[8 * c + 6], v[8 * c + 7]);
+          }
+          if (!warp_wait(&empty[slot + h], phase ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          tc_st_32x32b_x16(dst + slot * A_SLOT_COLS, v[h]);
+          tc_st_32x32b_x32(dst + (slot + h) * A_SLOT_COLS, v);
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[slot]);
-          if (++slot == STAGES) {
-            slot = 0;
-            phase ^= 1u;
-          }
+          if (lane == 0) mbar_arrive(&full[slot + h]);
+        }
+        if (!ok) break;
+        slot += 4;
+        if (slot >= STAGES) {
+          slot = 2 * group;
+          phase ^= 1u;
         }
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
+    regs_inc<EPI_REGS>();
     const int q = warp & 3;                    // TMEM lane quadrant: 32 weight rows
     const int part = (warp - EPI_WARP0) >> 2;  // tokens [part BT/2, + BT/2) of the tile
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
@@ -604,9 +635,15 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   p.ldc = pr.ldc;
   p.c_f32 = pr.c_f32;
   p.err = err;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      gemm_int8_tc_kernel<BT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GE::SMEM);
-  if (attr != cudaSuccess) return QW_ERR_CUDA;
+  static const bool ready = [] {
+    cudaFuncAttributes fa{};
+    return cudaFuncSetAttribute(gemm_int8_tc_kernel<BT, GATED>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)GE::SMEM) == cudaSuccess &&
+           cudaFuncGetAttributes(&fa, gemm_int8_tc_kernel<BT, GATED>) == cudaSuccess &&
+           fa.numRegs == LAUNCH_REGS;  // the register split depends on it
+  }();
+  if (!ready) return QW_ERR_CUDA;
   const int64_t tiles = (int64_t)p.num_n_tiles * p.num_m_tiles;
   const int sms = device_sm_count();
   if (tiles > 0x7FFFFFFF - sms) return QW_ERR_UNSUPPORTED;  // counted in 32 bits
