@@ -102,6 +102,7 @@ struct Params {
   int64_t ldc;
   int32_t c_f32;
   int32_t csize;      // CTAs that share a tile's K (1 where tiles fill the GPU)
+  uint32_t b_bytes;   // of a token stage's copy (fewer rows than BT where M has fewer)
   int32_t* err;
 };
 
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], GE::B_BYTES);
+          mbar_arrive_expect_tx(&full[stage], p.b_bytes);
           tma_load_2d(sB + stage * GE::B_BYTES, &tmA, &full[stage], kb * KA, m0);
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
@@ -616,8 +617,12 @@ template <int BT, bool GATED>
 qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaStream_t st) {
   using GE = Geo<BT>;
   CUtensorMap tmA, tmW;
+  // A tile's rows past M: none are copied where M is below BT (whatever the stage holds there
+  // ends in accumulator columns that nobody reads), zeros in the last of several token tiles.
+  // (Copies of 64 rows, most of them outside the tensor, cost 5 us of 20 at M = 4 to 8.)
+  const uint32_t box_rows = (uint32_t)min64(BT, (pr.M + 7) / 8 * 8);
   if (!encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes16, pr.K, pr.M, (uint64_t)pr.K * 2, KA,
-                 BT) ||
+                 box_rows) ||
       !encode_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, pr.W, pr.K, pr.N, pr.K, KW,
                  GATED ? BW / 2 : BW))
     return QW_ERR_CUDA;
@@ -634,6 +639,7 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   p.C = pr.C;
   p.ldc = pr.ldc;
   p.c_f32 = pr.c_f32;
+  p.b_bytes = box_rows * KA * 2;
   p.err = err;
   static const bool ready = [] {
     cudaFuncAttributes fa{};
