@@ -8,17 +8,21 @@
 // ln2 (log2 s - t / s): r's own rounding cancels, so rows of large logits lose nothing.
 //
 // Alternatives: ids are ordered by a 64-bit key (the value's bits as an ordered integer above the
-// complement of the id), so ties need no second pass.  Each CTA keeps a lower bound `thr` of its
-// topk-th key; a vector whose maximum is below it costs one comparison, what passes goes to a
-// shared buffer, and when that fills up it is cut back to the topk largest and thr rises to the
-// last of them.  The first bound is the smallest of 32 group maxima of the first block (32
-// different elements are at least that).  If one block overflows the buffer (ascending rows),
-// the bound still rises by what the buffer holds, and the block is offered again from registers.
+// complement of the id), so ties need no second pass.  While the row streams by, a thread only notes
+// the largest logit of its vectors of each block (rounded up to 16 bits).  At the end the topk-th
+// largest of 32 sets of threads' maxima bounds the topk-th key from below (topk different logits are
+// at least that); what reaches it, about topk threads' vectors of some block, is listed and read
+// once more, from L2, a vector to a thread, and the logits at or above the bound are ranked.  Where
+// very many reach it (rows of ties), the bound rises to the topk-th key of a full buffer until what
+// is left fits.
+// (Offering while streaming - a bound that rises, a buffer, cuts of it - left 4096 x 131072 BF16 with
+// 20 alternatives at 264 us: the candidates' latency stood in the stream's way.  Reading again whole
+// quarters of a thread's blocks: 304 us.)
 //
 // Bound: the row is read once (HBM); the work per logit is one exponential and about seven
-// instructions.  A CTA of 256 threads takes a row, each thread four 16-byte vectors at a time
-// with the next four in flight; few long rows are split over the CTAs of a cluster, whose
-// rank 0 merges the partial results through distributed shared memory in a fixed order.
+// instructions.  A CTA of 256 threads takes a row through a ring of bulk-copied blocks in shared
+// memory; few long rows are split over the CTAs of a cluster, whose rank 0 merges the partial
+// results through distributed shared memory in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,7 +35,8 @@ namespace {
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int RV = 4;               // vectors of a thread per block
 constexpr int CAP = 512;            // candidate buffer
-constexpr int CUT = 128;            // candidates from which the buffer is cut back
+constexpr int NOTES = 32;           // blocks (or runs of them) whose threads' maxima are noted
+constexpr int HITS = 512;           // of them that the bound lets through to the list
 constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
 
@@ -256,11 +261,17 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 
 // One block of a CTA's vectors, in shared memory.
 constexpr int BLOCK = THREADS * RV;
-constexpr int STAGES = 3;
+constexpr int STAGES = 2;
 constexpr size_t RING_BYTES = (size_t)STAGES * BLOCK * 16;
 // a reference is kept until a logit passes it by more than this (2^12 x 2^31 terms stay finite,
 // and the entropy, a difference of two numbers of that many bits, loses four of its own)
 constexpr float HEADROOM = 8.f;
+
+// BF16 bits of a number that is x or above it
+__device__ __forceinline__ uint16_t bf16_above(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return (uint16_t)(((b & 0x80000000u) ? b : b + 0xFFFFu) >> 16);
+}
 
 template <int TYPE>
 __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs a, const int csize) {
@@ -271,8 +282,10 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   __shared__ uint64_t buf[CAP];
   __shared__ uint64_t sorted[kLogprobsMaxTop];
   __shared__ int cnt;
-  __shared__ uint32_t group[32], first;
-  static_assert(WARPS * RV == 32, "one group for each candidate of the first bound");
+  __shared__ float sets[32];               // largest logits of 32 sets of threads
+  __shared__ uint16_t note[NOTES][THREADS];  // upper bounds (BF16 bits) of a thread's maxima
+  __shared__ uint16_t list[HITS];            // note x THREADS + thread
+  __shared__ int hits;
   __shared__ Part wpart[WARPS];
   __shared__ Part part;  // this CTA's result; on rank 0, at the end, the row's
   __shared__ uint64_t full[STAGES];
@@ -280,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    cnt = 0;
+    cnt = hits = 0;
     abort_flag = 0;
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
     fence_barrier_init();
@@ -288,8 +301,8 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
-  const int64_t row = blockIdx.x / csize;
-  const int rank = blockIdx.x % csize;
+  const int64_t row = blockIdx.x / (unsigned)csize;
+  const int rank = (int)(blockIdx.x % (unsigned)csize);
   const int64_t off = row * a.ld;
   const uint8_t* base = static_cast<const uint8_t*>(a.logits) + off * ES;
   const int k = a.topk;
@@ -299,9 +312,11 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   const int nv = (a.V - head) / VE;
   const int tail = a.V - head - nv * VE;
   const uint4* vec = reinterpret_cast<const uint4*>(base + (int64_t)head * ES);
-  const int per = (nv + csize - 1) / csize;
-  const int vbeg = min(nv, rank * per), vend = min(nv, vbeg + per);
+  // this CTA's: whole blocks, but for the row's end
+  const int per = ((nv + BLOCK - 1) / BLOCK + csize - 1) / csize * BLOCK;
+  const int vbeg = (int)min64(nv, (int64_t)rank * per), vend = min(nv, vbeg + per);
   const int nblk = (vend - vbeg + BLOCK - 1) / BLOCK;
+  const int run = max(1, (nblk + NOTES - 1) / NOTES);  // blocks to a note
 
   auto fetch = [&](int b) {  // thread 0
     const int v = vbeg + b * BLOCK;
@@ -318,19 +333,15 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   const bool want_rank = tok_ok && a.token_rank;
   const float xt = want_rank ? E::load(base, tok) : INFINITY;
   const float xt_up = want_rank ? E::next_up(xt) : INFINITY;
+  // vectors with a logit before the token: equal logits count in them (what is too much in the
+  // token's own vector is taken back at the end)
+  const int vlim = tok > head ? min(nv, (tok - head + VE - 1) / VE) : 0;
 
   // M: the logit the reference r was made from (LOW: none yet)
   float rmax = -INFINITY, M = E::LOW, r = E::LOW * LOG2E;
   uint64_t s2 = 0, t2 = 0;
   int above = 0;
-  bool bad = false, over = false;
-  // lower bound of the k-th key, and its value; -inf is never offered (the masked ids that
-  // follow are added at the end)
-  constexpr float kLowest = -3.4028234663852886e38f;
-  uint64_t thr = (uint64_t)order_of(kLowest) << 32;
-  float thr_x = k > 0 ? kLowest : __uint_as_float(0x7FC00000u);  // NaN: nothing passes
-  int settled = 0;  // entries at the front of buf that are there before the current block
-
+  bool bad = false;
   auto rise = [&](float m) {  // a new reference
     const float rn = m * LOG2E, d = r - rn, f = ex2(d);
     const uint64_t f2 = pack2(f, f);
@@ -339,112 +350,46 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     M = m;
     r = rn;
   };
-  auto offer = [&](float x, int32_t id) {
-    if (!(x >= thr_x)) return;
-    const uint64_t key = order_key(x, id);
-    if (key >= thr) {
-      const int pos = atomicAdd(&cnt, 1);
-      if (pos < CAP) buf[pos] = key;
-      over = over || pos >= CUT;
-    }
-  };
-  // Vectors j and j + 1 of the lanes in `hits` of this warp: a lane for each of their logits.
-  auto offer_hits = [&](uint32_t hits, int b, int j) {
-    const int pos = j * THREADS + warp * 32 + (lane / VE) * THREADS;
-    while (hits) {
-      const int p = pos + __ffs(hits) - 1;
-      hits &= hits - 1;
-      const int v = vbeg + b * BLOCK + p;
-      if (lane < 2 * VE && v < vend)
-        offer(E::load(ring + (b % STAGES) * BLOCK + p, lane % VE), head + v * VE + lane % VE);
-    }
-  };
 
-  // cut the buffer back to the k largest keys and raise thr to the last of them; after an
-  // overflow the entries of the current block are dropped instead (they are offered again)
-  auto cut = [&]() {
-    const int n = min(cnt, CAP);
-    const bool lost = cnt > CAP;
-    for (int i = tid; i < n; i += THREADS) {
-      const uint64_t key = buf[i];
-      int before = 0;
-      for (int j = 0; j < n; ++j) before += buf[j] > key;
-      if (before < k) sorted[before] = key;
-    }
-    __syncthreads();
-    if (n >= k && sorted[k - 1] > thr) {
-      thr = sorted[k - 1];
-      thr_x = value_of(thr);
-    }
-    if (!lost) settled = min(n, k);
-    if (!lost && tid < settled) buf[tid] = sorted[tid];
-    if (tid == 0) cnt = settled;
-    over = false;
-    __syncthreads();
-    return lost;
-  };
-
+  // the logits beside the vectors: one a thread of rank 0
+  float side = -INFINITY;
+  const int32_t side_id = tid < head ? tid : a.V - tail + (tid - head);
   if (rank == 0 && tid < head + tail) {
-    const int32_t id = tid < head ? tid : a.V - tail + (tid - head);
-    const float x = E::load(base, id);
-    bad = !(x < INFINITY);
-    rmax = x;
-    if (x > E::LOW) {
-      rise(x);
+    side = E::load(base, side_id);
+    bad = !(side < INFINITY);
+    rmax = side;
+    if (side > E::LOW) {
+      rise(side);
       s2 = pack2(1.f, 0.f);
-      t2 = pack2(fmaf(x, LOG2E, -r), 0.f);
+      t2 = pack2(fmaf(side, LOG2E, -r), 0.f);
     }
-    if (k > 0) offer(x, id);
-    above = x > xt || (x == xt && id < tok);
+    above = side > xt || (side == xt && side_id < tok);
   }
 
+  float pmax = -INFINITY;  // of this thread's vectors since the last note
+#pragma unroll 1
   for (int b = 0; b < nblk; ++b) {
-    const uint4* blk = ring + (b % STAGES) * BLOCK + tid;
+    uint4* blk = ring + (b % STAGES) * BLOCK + tid;
     const int v0 = vbeg + b * BLOCK + tid;
-    (void)warp_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err);
-    if (b == 0 && k > 0) {
-      // the first bound: the k-th largest of the maxima of 32 groups, a group being what a
-      // warp takes at a time (k different logits are at least that)
+    if (v0 - tid + BLOCK > vend) {  // the row's last block: masked vectors behind it
 #pragma unroll
-      for (int j = 0; j < RV; ++j) {
-        const float vm = v0 + j * THREADS < vend ? E::vmax(blk[j * THREADS]) : -INFINITY;
-        const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, order_of(vm));
-        if (lane == 0) group[warp * RV + j] = g;
-      }
-      __syncthreads();
-      settled = cnt;  // the logits beside the vectors
-      if (warp == 0) {
-        const uint32_t g = group[lane];
-        int before = 0;
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t o = __shfl_sync(0xFFFFFFFFu, g, i);
-          before += o > g || (o == g && i < lane);
-        }
-        if (before == k - 1) first = g;
-      }
-      __syncthreads();
-      if ((uint64_t)first << 32 > thr) {
-        thr = (uint64_t)first << 32;
-        thr_x = value_of(thr);
-      }
+      for (int j = 0; j < RV; ++j)
+        if (v0 + j * THREADS >= vend) blk[j * THREADS] = E::masked();
     }
+    // (a thread reads only vectors that it filled itself or that the copy brings)
+    (void)warp_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err);
     typename E::Count count{};
     // two vectors at a time, so that their maximum is looked at once for both
 #pragma unroll 1
     for (int j = 0; j < RV; j += 2) {
       const int v = v0 + j * THREADS;
-      const bool first = v < vend, second = v + THREADS < vend;
-      const uint4 x4 = first ? blk[j * THREADS] : E::masked();
-      const uint4 z4 = second ? blk[(j + 1) * THREADS] : E::masked();
+      const uint4 x4 = blk[j * THREADS], z4 = blk[(j + 1) * THREADS];
       const float vm = E::vmax(x4, z4);
-      rmax = fmaxf(rmax, vm);
-      if (vm >= xt) {
-        if (first) E::count(x4, head + v * VE < tok ? xt : xt_up, count);
-        if (second) E::count(z4, head + (v + THREADS) * VE < tok ? xt : xt_up, count);
+      pmax = fmaxf(pmax, vm);
+      if (vm >= xt) {  // (masked vectors behind the row are not above anything)
+        E::count(x4, v < vlim ? xt : xt_up, count);
+        E::count(z4, v + THREADS < vlim ? xt : xt_up, count);
       }
-      const uint32_t hits = __ballot_sync(0xFFFFFFFFu, vm >= thr_x);
-      if (hits) offer_hits(hits, b, j);
       if (!(vm < (M == E::LOW ? E::LOW : M + HEADROOM))) {
         bad = bad || !(vm < INFINITY);
         if (vm > E::LOW) rise(vm);
@@ -468,15 +413,12 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
       }
     }
     if (want_rank) above += E::total(count);
-    // the buffer is cut when it fills up, and whenever the row has doubled: what passes a bound
-    // from the last cut is then about k logits
-    const bool doubled = k > 0 && ((b + 1) & b) == 0 && b + 1 < nblk;
-    while (__syncthreads_or(over || doubled)) {
-      if (!cut()) break;
-#pragma unroll 1
-      for (int j = 0; j < RV; j += 2) offer_hits(0xFFFFFFFFu, b, j);
+    if (k > 0 && (b + 1 == nblk || (b + 1) % run == 0)) {
+      note[b / run][tid] = bf16_above(pmax);
+      rmax = fmaxf(rmax, pmax);
+      pmax = -INFINITY;
     }
-    // every thread is done with the block
+    __syncthreads();  // every thread is done with the block
     if (abort_flag) {
       // a wait gave up: let the copies in flight land before shared memory goes away
       const uint64_t t0 = globaltimer_ns();
@@ -487,9 +429,97 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     }
     if (tid == 0 && b + STAGES < nblk) fetch(b + STAGES);
   }
+
+  rmax = fmaxf(rmax, pmax);
+
+  int settled = 0;  // keys in `sorted`
   if (k > 0) {
+    // lower bound of the k-th key, and its value; -inf is never offered (the masked ids that
+    // follow are added at the end)
+    constexpr float kLowest = -3.4028234663852886e38f;
+    uint64_t thr = (uint64_t)order_of(kLowest) << 32;
+    float thr_x = kLowest;
+    {
+      // the k-th largest of the maxima of 32 sets of threads, one a lane (the logits beside the
+      // vectors may be among them: they are offered too)
+      float m = rmax;
+#pragma unroll
+      for (int o = 1; o < THREADS / 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      if (tid % (THREADS / 32) == 0) sets[tid / (THREADS / 32)] = m;
+      __syncthreads();
+      const uint32_t g = order_of(sets[lane]);
+      int before = 0;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, g, i);
+        before += o > g || (o == g && i < lane);
+      }
+      const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, before == k - 1)) - 1;
+      const uint64_t key = (uint64_t)__shfl_sync(0xFFFFFFFFu, g, owner) << 32;
+      if (key > thr) {
+        thr = key;
+        thr_x = value_of(key);
+      }
+    }
+    bool lost = false;
+    auto offer = [&](float x, int32_t id) {
+      if (!(x >= thr_x)) return;
+      const uint64_t key = order_key(x, id);
+      if (key < thr) return;
+      int pos = *(volatile int*)&cnt;  // (a full buffer costs a read, not an atomic)
+      if (pos < CAP) pos = atomicAdd(&cnt, 1);
+      if (pos < CAP)
+        buf[pos] = key;
+      else
+        lost = true;
+    };
+    auto offer_vector = [&](int v) {
+      const uint4 q = v < vend ? __ldg(vec + v) : E::masked();
+      if (!(E::vmax(q) >= thr_x)) return;
+      float f[VE];
+      E::unpack(q, f);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) offer(f[e], head + v * VE + e);
+    };
+    const int notes = (nblk + run - 1) / run;
+    for (int i = 0; i < notes; ++i)
+      if (__uint_as_float((uint32_t)note[i][tid] << 16) >= thr_x) {
+        const int pos = atomicAdd(&hits, 1);
+        if (pos < HITS) list[pos] = (uint16_t)(i * THREADS + tid);
+      }
     __syncthreads();
-    cut();  // never after an overflow: more than CUT candidates were cut with their block
+    const int listed = hits;
+    for (;;) {
+      if (side > -INFINITY) offer(side, side_id);
+      if (listed <= HITS) {
+        for (int b = 0; b < run; ++b)
+          for (int i = tid; i < listed * RV; i += THREADS) {
+            const int e = list[i / RV], gb = e / THREADS * run + b;
+            if (gb < nblk) offer_vector(vbeg + gb * BLOCK + i % RV * THREADS + e % THREADS);
+          }
+      } else {
+        for (int i = vbeg + tid; i < vend; i += THREADS) offer_vector(i);
+      }
+      const bool again = __syncthreads_or(lost);
+      const int n = min(cnt, CAP);
+      // the buffer's k largest keys, in order
+      for (int i = tid; i < n; i += THREADS) {
+        const uint64_t key = buf[i];
+        int before = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) before += buf[j] > key;
+        if (before < k) sorted[before] = key;
+      }
+      __syncthreads();
+      settled = min(n, k);
+      if (!again) break;
+      // overflow: the k-th of CAP keys is a bound above the last one
+      thr = sorted[k - 1];
+      thr_x = value_of(thr);
+      lost = false;
+      if (tid == 0) cnt = 0;
+      __syncthreads();
+    }
   }
 
   // threads -> warps -> the CTA
@@ -537,15 +567,25 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
         }
         part = p;
       }
+      if (tid == 0) cnt = 0;
+      __syncthreads();
       for (int i = tid; i < csize * k; i += THREADS) {
         const int c = i / k, j = i - c * k;
-        if (c > 0 && j < (int)ld_cluster_u32(mapa_shared(smem_u32(&part), (uint32_t)c) + 24))
+        if (j < (int)ld_cluster_u32(mapa_shared(smem_u32(&part), (uint32_t)c) + 24))
           buf[atomicAdd(&cnt, 1)] = ld_cluster_u64(mapa_shared(smem_u32(&sorted[j]), (uint32_t)c));
       }
     }
     cluster_sync();  // rank 0 has read; the others may leave
     if (rank != 0) return;
-    if (k > 0) cut();
+    const int n = cnt;
+    for (int i = tid; i < n; i += THREADS) {
+      const uint64_t key = buf[i];
+      int before = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) before += buf[j] > key;
+      if (before < k) sorted[before] = key;
+    }
+    settled = min(n, k);
   }
   __syncthreads();
 
@@ -595,6 +635,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     if (a.token_rank) a.token_rank[row] = tok_ok ? 1 + p.above : 0;
     if (a.entropy) a.entropy[row] = p.bad ? nan : none ? 0.f : ent;
   }
+  if (tid == 0) cnt = settled;
   if (k > settled && warp == 0) {
     // fewer ids than asked for are left by the mask: the masked ones follow in id order
     for (int32_t i0 = 0, n = settled; i0 < a.V && n < k; i0 += 32) {
@@ -609,7 +650,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   if (k > settled) __syncthreads();
   if (tid < k) {
     // (a row with NaN may not have that many: what is missing names id 0)
-    const uint64_t key = tid < max(cnt, settled) ? sorted[tid] : 0xFFFFFFFFull;
+    const uint64_t key = tid < (k > settled ? cnt : settled) ? sorted[tid] : 0xFFFFFFFFull;
     a.top_ids[row * k + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
     a.top_logprobs[row * k + tid] = logp(value_of(key));
   }
