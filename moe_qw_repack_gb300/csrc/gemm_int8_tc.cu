@@ -16,7 +16,7 @@
 //               32 (w % 4) .. + 31; a lane takes the 128 codes of its own row, makes them FP16
 //               (byte b -> the FP16 number 1024 + (b + 128), minus 1152: exact) and stores them as
 //               the MMA's A operand with one tcgen05.st for each of two operand slots.  (All eight
-//               warps on every slot pay a slot's waits twice as often: 318 us for 251.)
+//               warps on every slot pay a slot's waits twice as often: 318 us for 261.)
 //   warps 12-19 epilogue: tcgen05.ld the accumulator (a lane holds one weight row, a register
 //               one token), release it, scale, add bias, (gated) exchange gate and up, round and
 //               store while the next tile's MMAs run.  They take registers from the other warps
@@ -136,12 +136,6 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-}
-
 // What a thread does with the finished sums of its weight row: scale, bias, gate, round, store.
 template <bool GATED>
 struct Out {
@@ -323,7 +317,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       // (after a wait that gave up, a stage may also lack its converters: bounded either way)
       for (int s = 0; s < STAGES; ++s)
-        if (issued & (1u << s)) drain_wait(&full[s], (issued_phase >> s) & 1u);
+        if (issued & (1u << s)) wait_landed(&full[s], (issued_phase >> s) & 1u);
     } else if (warp == 2 && lane == 0) {
       // ---------------------------------------------------------- weights
       int stage = 0;
@@ -350,7 +344,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       for (int s = 0; s < W_STAGES; ++s)
-        if (issued & (1u << s)) drain_wait(&w_full[s], (issued_phase >> s) & 1u);
+        if (issued & (1u << s)) wait_landed(&w_full[s], (issued_phase >> s) & 1u);
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs the loop and one elected lane issues: descriptors, addresses and
@@ -391,7 +385,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (leader) {
         tc_commit(final_bar);
-        drain_wait(final_bar, 0);
+        wait_landed(final_bar, 0);
       }
     }
   } else if (warp < EPI_WARP0) {

@@ -16,9 +16,63 @@ namespace {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// x rounded to an integer (ties to even), |x| < 2^22: adding 1.5 * 2^23 rounds at the units.
-// The sum's low bits are the integer in two's complement.
-constexpr float kRound = 12582912.f;
+// largest |v| of eight BF16 values as BF16 bits (finite values order like their bit patterns)
+__device__ __forceinline__ uint32_t bf16x8_absmax(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+  return m;
+}
+
+// A row's scale and codes from its largest magnitude (BF16 bits).  A row with a non-finite value has
+// the scale NaN and codes 0.
+struct RowScale {
+  // adding 1.5 * 2^23 rounds |x| < 2^22 to an integer (ties to even), which the sum's low bits hold
+  // in two's complement
+  static constexpr float kRound = 12582912.f;
+  bool finite;
+  float scale, inv;
+  __device__ __forceinline__ explicit RowScale(uint32_t amax) {
+    const float top = __uint_as_float(amax << 16);
+    finite = amax < 0x7F80u;
+    scale = finite ? top / 127.0f : __uint_as_float(0x7FC00000u);
+    inv = fminf(127.0f / top, 3.4028234663852886e38f);
+  }
+  // eight values' codes plus kRound; the product is rounded to FP32 before the code is (no fused
+  // multiply-add)
+  __device__ __forceinline__ void rounded(const uint4& v, float (&q)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      q[2 * j] = finite ? __fadd_rn(__fmul_rn(bf16_lo(w[j]), inv), kRound) : kRound;
+      q[2 * j + 1] = finite ? __fadd_rn(__fmul_rn(bf16_hi(w[j]), inv), kRound) : kRound;
+    }
+  }
+  __device__ __forceinline__ uint2 codes(const uint4& v) const {
+    float q[8];
+    rounded(v, q);
+    uint32_t o[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t lo = __byte_perm(__float_as_uint(q[4 * j]), __float_as_uint(q[4 * j + 1]), 0x0040);
+      const uint32_t hi = __byte_perm(__float_as_uint(q[4 * j + 2]), __float_as_uint(q[4 * j + 3]), 0x0040);
+      o[j] = __byte_perm(lo, hi, 0x5410);
+    }
+    return make_uint2(o[0], o[1]);
+  }
+  __device__ __forceinline__ uint4 codes16(const uint4& v) const {  // as FP16 numbers
+    float q[8];
+    rounded(v, q);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 h = __floats2half2_rn(q[2 * j] - kRound, q[2 * j + 1] - kRound);
+      o[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+};
 
 // Row r of A -> codes (INT8, or the same integers as FP16 for the tensor cores) and the row's
 // scale.  One CTA per row.  A thread keeps VEC 16-byte vectors of the row (K <= 2048 VEC) in
@@ -34,20 +88,16 @@ __global__ void __launch_bounds__(QTHREADS)
   const uint4* src = reinterpret_cast<const uint4*>(A + r * lda);
   const int n8 = K / 8;
   uint4 keep[VEC];
-  uint32_t amax = 0;  // largest |v| as BF16 bits (finite values order like their bit patterns)
-  auto fold = [&](const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) amax = max(amax, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-  };
+  uint32_t amax = 0;
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
     const int i = threadIdx.x + j * QTHREADS;
     keep[j] = i < n8 ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) fold(keep[j]);
-  for (int i = threadIdx.x + VEC * QTHREADS; i < n8; i += QTHREADS) fold(__ldg(src + i));
+  for (int j = 0; j < VEC; ++j) amax = max(amax, bf16x8_absmax(keep[j]));
+  for (int i = threadIdx.x + VEC * QTHREADS; i < n8; i += QTHREADS)
+    amax = max(amax, bf16x8_absmax(__ldg(src + i)));
   __shared__ uint32_t part[QTHREADS / 32];
   amax = __reduce_max_sync(0xFFFFFFFFu, amax);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
@@ -55,41 +105,16 @@ __global__ void __launch_bounds__(QTHREADS)
   amax = part[0];
 #pragma unroll
   for (int i = 1; i < QTHREADS / 32; ++i) amax = max(amax, part[i]);
-  const float top = __uint_as_float(amax << 16);
-  const bool finite = amax < 0x7F80u;
-  const float inv = fminf(127.0f / top, 3.4028234663852886e38f);
+  const RowScale rs(amax);
   if (threadIdx.x == 0) {
-    S[r] = finite ? top / 127.0f : __uint_as_float(0x7FC00000u);
-    if (!finite) set_error(err, QW_ERR_VALUE);
+    S[r] = rs.scale;
+    if (!rs.finite) set_error(err, QW_ERR_VALUE);
   }
-  auto put = [&](int i, uint4 v) {
-    if (!finite) v = make_uint4(0, 0, 0, 0);  // codes 0 (0 * inv is 0: inv is finite there too)
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float q[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // the product is rounded to FP32 before the code is (no fused multiply-add)
-      q[2 * j] = __fadd_rn(__fmul_rn(bf16_lo(w[j]), inv), kRound);
-      q[2 * j + 1] = __fadd_rn(__fmul_rn(bf16_hi(w[j]), inv), kRound);
-    }
-    if constexpr (F16) {
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2 h = __floats2half2_rn(q[2 * j] - kRound, q[2 * j + 1] - kRound);
-        o[j] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      reinterpret_cast<uint4*>(Q)[r * (K / 8) + i] = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      uint32_t o[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t lo = __byte_perm(__float_as_uint(q[4 * j]), __float_as_uint(q[4 * j + 1]), 0x0040);
-        const uint32_t hi = __byte_perm(__float_as_uint(q[4 * j + 2]), __float_as_uint(q[4 * j + 3]), 0x0040);
-        o[j] = __byte_perm(lo, hi, 0x5410);
-      }
-      reinterpret_cast<uint2*>(Q)[r * (K / 8) + i] = make_uint2(o[0], o[1]);
-    }
+  auto put = [&](int i, const uint4& v) {
+    if constexpr (F16)
+      reinterpret_cast<uint4*>(Q)[r * (K / 8) + i] = rs.codes16(v);
+    else
+      reinterpret_cast<uint2*>(Q)[r * (K / 8) + i] = rs.codes(v);
   };
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
@@ -123,13 +148,16 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ one or two tokens
 // The weights are streamed once; integer sums are exact, so any order gives the same result.
-// A CTA of four warps takes R = 4 RW weight rows (gated: gate rows and the up rows of the same
-// outputs) and a slice of at most SLICE of their k.  Its rows arrive in shared memory by bulk
+// A CTA of two warps takes R = 2 RW weight rows (gated: gate rows and the up rows of the same
+// outputs) and slices of at most SLICE of their k, the next on its way while one is multiplied.  Its rows arrive in shared memory by bulk
 // copies that one warp issues before anything else, so that all of a CTA's bytes are in flight
 // at once, however few its threads; a lane then multiplies 16 consecutive k of RW rows with the
-// same k of every token (dp4a), and one warp reduction per row and token ends the slice.  Partial
-// sums of slices meet in rank 0 of a cluster.
-constexpr int GW = 4, GTHREADS = GW * 32, SLICE = 4096;
+// same k of every token (dp4a), and one warp reduction per row and token ends the work.  Where there
+// are few rows, the CTAs of a cluster share a block's slices and their sums meet in its rank 0.
+// (Quantising BF16 tokens in here instead of a kernel in front of it loses the weights' head start
+// under that kernel: 1 x 14336 x 4096 12.3 for 12.8 us, but gated 22.9 for 21.9, two tokens 14.6 for
+// 13.6 and 1 x 4096 x 4096 4.5 for 3.9.)
+constexpr int GW = 2, GTHREADS = GW * 32, SLICE = 4096;
 
 struct GemvShape {
   int32_t len;     // k of a slice (a multiple of 16)
@@ -143,8 +171,8 @@ __global__ void __launch_bounds__(GTHREADS)
   constexpr int R = GW * RW;                     // weight rows of a CTA
   constexpr int OUTS = GATED ? R / 2 : R;        // outputs of a CTA
   static_assert(!GATED || RW % 2 == 0, "a warp has its gate rows' up rows");
-  extern __shared__ __align__(128) uint8_t smem[];  // [R][pitch] weights
-  __shared__ uint64_t full;
+  extern __shared__ __align__(128) uint8_t smem[];  // [2 or 1][R][pitch] weights
+  __shared__ uint64_t full[2];
   __shared__ int abort_flag;
   __shared__ int part[R * MT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -154,7 +182,8 @@ __global__ void __launch_bounds__(GTHREADS)
   const int pitch = (g.len + 511) / 512 * 512;
 
   if (threadIdx.x == 0) {
-    mbar_init(&full, 1);
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
     abort_flag = 0;
     fence_barrier_init();
   }
@@ -167,29 +196,31 @@ __global__ void __launch_bounds__(GTHREADS)
     if (n >= cols) return -1;
     return (GATED && r >= RW / 2) ? (int64_t)cols + n : n;
   };
-  auto fetch = [&](int s) {  // warp 0
+  auto fetch = [&](int s, int buffer) {  // warp 0
+    if (s >= g.slices) return;
     const int k0 = s * g.len, len = min(g.len, p.K - k0);
     const int64_t row = lane < R ? row_of(lane) : -1;
     const int rows = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
-    if (lane == 0) mbar_arrive_expect_tx(&full, (uint32_t)(rows * len));
+    if (lane == 0) mbar_arrive_expect_tx(&full[buffer], (uint32_t)(rows * len));
     __syncwarp();
-    if (row >= 0) bulk_load(smem + lane * pitch, p.W + row * p.K + k0, (uint32_t)len, &full);
+    if (row >= 0)
+      bulk_load(smem + (buffer * R + lane) * pitch, p.W + row * p.K + k0, (uint32_t)len,
+                &full[buffer]);
   };
   // `early`: the previous kernel on the stream is this call's own quantiser, which waited for
   // everything before it; the weights may be read while it runs
-  if (early && warp == 0) fetch(rank);
+  if (early && warp == 0) fetch(rank, 0);
   pdl_wait();
   pdl_launch_dependents();
-  if (!early && warp == 0) fetch(rank);
+  if (!early && warp == 0) fetch(rank, 0);
 
   int acc[RW][MT] = {};
+  int buffer = 0;
   uint32_t phase = 0;
-  for (int s = rank; s < g.slices; s += g.csize, phase ^= 1u) {
+  for (int s = rank; s < g.slices; s += g.csize) {
     const int k0 = s * g.len, len = min(g.len, p.K - k0);
-    if (s != rank) {  // more slices than CTAs of the cluster: the buffer is used again
-      __syncthreads();
-      if (warp == 0) fetch(s);
-    }
+    if (s != rank) __syncthreads();  // the slice before, whose buffer the next one takes, is done
+    if (warp == 0) fetch(s + g.csize, buffer ^ 1);
     // a lane's k of every token, for all of its warp's rows; zeros past the slice and the tokens
     constexpr int XREG = SLICE / 512;
     uint4 x[XREG][MT];
@@ -202,8 +233,8 @@ __global__ void __launch_bounds__(GTHREADS)
                       ? __ldg(reinterpret_cast<const uint4*>(p.A + m * p.lda + k0 + k))
                       : make_uint4(0, 0, 0, 0);
       }
-    (void)warp_wait(&full, phase, &abort_flag, err);
-    const uint8_t* wrow = smem + warp * RW * pitch + lane * 16;
+    if (!warp_wait(&full[buffer], phase, &abort_flag, err)) wait_landed(&full[buffer], phase);
+    const uint8_t* wrow = smem + (buffer * R + warp * RW) * pitch + lane * 16;
 #pragma unroll
     for (int j = 0; j < XREG; ++j) {
       if (j * 512 >= len) break;
@@ -221,6 +252,8 @@ __global__ void __launch_bounds__(GTHREADS)
         }
       }
     }
+    phase ^= (uint32_t)buffer;  // a buffer's phase turns every second slice
+    buffer ^= 1;
   }
 
   // sum (row i, token m) of the slices this CTA had at i MT + m
@@ -267,16 +300,20 @@ qw_status launch_gemv(const Int8Problem& p, bool early, int32_t* err, cudaStream
   constexpr int R = GW * RW, OUTS = GATED ? R / 2 : R;
   const int32_t cols = GATED ? p.N / 2 : p.N;
   const int64_t blocks = ((int64_t)cols + OUTS - 1) / OUTS;
-  // slices of at most SLICE; shorter ones while the GPU is not full and each keeps 1024
-  int slices = (p.K + SLICE - 1) / SLICE;
-  while (slices < 8 && blocks * slices < 2 * device_sm_count() && p.K / (2 * slices) >= 1024)
-    slices *= 2;
+  // Slices of at most SLICE.  Few blocks share them out over clusters, shorter ones if need be, while
+  // each keeps 1024.  (A cluster costs more than it gives where there are blocks enough:
+  // 1 x 4096 x 14336 15.8 us with clusters of four, 12.0 without.)
+  const int sms = device_sm_count();
+  int slices = (p.K + SLICE - 1) / SLICE, csize = 1;
+  while (csize < 8 && blocks * csize < 4 * sms && p.K / (2 * csize) >= 1024) csize *= 2;
+  if (slices < csize) slices = csize;
   GemvShape g;
   g.len = ((p.K + slices - 1) / slices + 15) / 16 * 16;
   g.slices = (p.K + g.len - 1) / g.len;
-  g.csize = g.slices < 8 ? g.slices : 8;
+  g.csize = g.slices < csize ? g.slices : csize;
+  const int buffers = g.slices > g.csize ? 2 : 1;
   const int pitch = (g.len + 511) / 512 * 512;
-  constexpr int kMaxSmem = R * SLICE;
+  constexpr int kMaxSmem = 2 * R * SLICE;
   static const cudaError_t attr =
       cudaFuncSetAttribute(gemv_int8_kernel<MT, RW, GATED>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
@@ -284,7 +321,7 @@ qw_status launch_gemv(const Int8Problem& p, bool early, int32_t* err, cudaStream
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(blocks * g.csize));
   cfg.blockDim = dim3(GTHREADS);
-  cfg.dynamicSmemBytes = (size_t)R * pitch;
+  cfg.dynamicSmemBytes = (size_t)buffers * R * pitch;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

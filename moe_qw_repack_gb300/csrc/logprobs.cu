@@ -423,10 +423,8 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     __syncthreads();  // every thread is done with the block
     if (abort_flag) {
       // a wait gave up: let the copies in flight land before shared memory goes away
-      const uint64_t t0 = globaltimer_ns();
       for (int i = b; tid == 0 && i < min(nblk, b + STAGES); ++i)
-        while (!mbar_try_wait(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u))
-          if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        wait_landed(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u);
       break;
     }
     if (tid == 0 && b + STAGES < nblk) fetch(b + STAGES);

@@ -111,6 +111,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, err)) != 0;
 }
 
+// After a wait that gave up: wait once more, with a limit of its own, for the copies of a phase to
+// land before the shared memory they write to goes away.
+__device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+}
+
 // ------------------------------------------------------------------ thread-block clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
