@@ -32,12 +32,9 @@
 // Few tiles of long K are split: the CTAs of a cluster take slices of K, leave their FP32 sums in
 // shared memory, and each finishes a share of the tile's tokens, adding the slices in rank order.
 // Every wait is bounded; on expiry the kernel reports QW_ERR_TIMEOUT and shuts down.
-#include <cuda.h>
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
-#include <mutex>
-
+#include "int8_map.cuh"
 #include "qw_common.cuh"
 #include "qw_internal.h"
 
@@ -96,6 +93,7 @@ struct Params {
   int32_t K;
   int32_t num_n_tiles, num_m_tiles;
   const float* a_scale;
+  const int8_t* W;
   const float* w_scale;
   const uint16_t* bias;
   void* C;
@@ -262,11 +260,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  // The set-up above overlaps the previous kernel's tail; everything else comes after this, the
-  // first use of the tensor maps included: they lie in the launch's parameters, whose addresses
-  // are used again by later launches, and an SM may hold a map of an earlier one until here.
-  pdl_wait();
-
   const int csize = p.csize;
   const int rank = (int)(blockIdx.x % (unsigned)csize);
   const uint32_t cluster = blockIdx.x / (unsigned)csize, clusters = gridDim.x / (unsigned)csize;
@@ -290,6 +283,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int KWB = (p.K + KW - 1) / KW, kw_per = (KWB + csize - 1) / csize;
   const int kw_beg = min(KWB, rank * kw_per), kw_end = min(KWB, kw_beg + kw_per);
   const int kb_beg = 2 * kw_beg, kb_end = 2 * kw_end;
+
+  if constexpr (BT == 64) {
+    // the first weight stages on their way to L2 while the call's quantiser runs (32 and 64 tokens:
+    // 20.3 -> 19.5 us at 14336 x 4096)
+    const int r = threadIdx.x % BW, kw = kw_beg + threadIdx.x / BW;
+    const int32_t n = (int32_t)(first.nt * TILE_COLS) + r % TILE_COLS;
+    if (kw < kw_end && n < p.cols)
+      prefetch_l2(p.W + ((int64_t)(r / TILE_COLS ? p.cols : 0) + n) * p.K + kw * KW);
+  }
+  // What is above overlaps the previous kernel's tail; everything else comes after this, the
+  // first use of the tensor maps included: they lie in the launch's parameters, whose addresses
+  // are used again by later launches, and an SM may hold a map of an earlier one until here.
+  pdl_wait();
 
   if (warp < CVT_WARP0) {
     regs_dec<MISC_REGS>();
@@ -546,23 +552,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         out.bias =
             p.bias && out.nvalid ? __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16) : 0.f;
         const int tokens = (int)min64(BT, p.M - m0);
-        for (int i = 2 * (rank + csize * w); i < tokens; i += 4 * csize) {
-          float s0 = 0.f, s1 = 0.f;
-          for (int c = 0; c < csize; ++c) {
-            const uint32_t a = mapa_shared(smem_u32(sB) + (uint32_t)(i * BW + 32 * q + lane) * 4, c);
-            s0 += ld_shared_cluster_f32(a);
-            s1 += ld_shared_cluster_f32(a + BW * 4);
-          }
-          const bool second = i + 1 < tokens;
-          float a = out.value(s0, __ldg(p.a_scale + m0 + i));
-          const float b = out.value(s1, second ? __ldg(p.a_scale + m0 + i + 1) : 0.f);
-          if constexpr (GATED) {
-            a = out.gate(a, b);
-            const int odd = lane >> 4;
-            if (out.nvalid && (second || !odd)) out.put(m0 + i + odd, a);
-          } else if (out.nvalid) {
-            out.put(m0 + i, a);
-            if (second) out.put(m0 + i + 1, b);
+        // (four pairs at a time: their loads wait for each other's latency only once)
+        constexpr int U = 4;
+        for (int i0 = 2 * (rank + csize * w); i0 < tokens; i0 += 4 * csize * U) {
+          float sum[U][2] = {};
+          for (int c = 0; c < csize; ++c)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int i = min(i0 + 4 * csize * u, BT - 2);
+              const uint32_t a =
+                  mapa_shared(smem_u32(sB) + (uint32_t)(i * BW + 32 * q + lane) * 4, c);
+              sum[u][0] += ld_shared_cluster_f32(a);
+              sum[u][1] += ld_shared_cluster_f32(a + BW * 4);
+            }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int i = i0 + 4 * csize * u;
+            if (i >= tokens) break;
+            const bool second = i + 1 < tokens;
+            float a = out.value(sum[u][0], __ldg(p.a_scale + m0 + i));
+            const float b = out.value(sum[u][1], second ? __ldg(p.a_scale + m0 + i + 1) : 0.f);
+            if constexpr (GATED) {
+              a = out.gate(a, b);
+              const int odd = lane >> 4;
+              if (out.nvalid && (second || !odd)) out.put(m0 + i + odd, a);
+            } else if (out.nvalid) {
+              out.put(m0 + i, a);
+              if (second) out.put(m0 + i + 1, b);
+            }
           }
         }
       }
@@ -580,31 +597,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
+// CTAs that share a tile's K: as many as still fit the GPU at once and keep 1024 k each
+template <int BT>
+int split(int64_t tiles, int32_t K, int sms) {
+  int csize = 1;
+  if (BT < 256)
+    while (csize < 8 && tiles * csize * 2 <= sms && K / (csize * 2) >= 1024) csize *= 2;
+  return csize;
 }
 
-bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner,
-               uint64_t rows, uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_rows) {
-  auto enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dim[2] = {inner, rows};
-  cuuint64_t str[1] = {pitch_bytes};
-  cuuint32_t box[2] = {box_inner, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return enc(map, type, 2, const_cast<void*>(base), dim, str, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// What a product takes with tiles of BT tokens, in quarters of the time of one k at BT <= 128 (the
+// MMAs are then bound by the weight operand, whose 128 rows x 16 k take as long for 64 tokens as for
+// 128; 256 take 5/4 of it): each round of tiles over the SMs pays its k and its epilogue.
+template <int BT>
+int64_t cost(const Int8Problem& p, bool gated, int sms) {
+  const int64_t n_tiles = gated ? (p.N / 2 + BW / 2 - 1) / (BW / 2) : (p.N + BW - 1) / BW;
+  const int64_t tiles = n_tiles * ((p.M + BT - 1) / BT);
+  const int csize = split<BT>(tiles, p.K, sms);
+  const int64_t rounds = (tiles * csize + sms - 1) / sms;
+  return rounds * ((int64_t)(p.K / csize) * (BT == 256 ? 5 : 4) + (csize > 1 ? 24 : 8) * BT);
 }
 
 template <int BT, bool GATED>
@@ -615,9 +626,9 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   // ends in accumulator columns that nobody reads), zeros in the last of several token tiles.
   // (Copies of 64 rows, most of them outside the tensor, cost 5 us of 20 at M = 4 to 8.)
   const uint32_t box_rows = (uint32_t)min64(BT, (pr.M + 7) / 8 * 8);
-  if (!encode_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes16, pr.K, pr.M, (uint64_t)pr.K * 2, KA,
+  if (!encode_int8_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, codes16, pr.K, pr.M, (uint64_t)pr.K * 2, KA,
                  box_rows) ||
-      !encode_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, pr.W, pr.K, pr.N, pr.K, KW,
+      !encode_int8_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, pr.W, pr.K, pr.N, pr.K, KW,
                  GATED ? BW / 2 : BW))
     return QW_ERR_CUDA;
   Params p{};
@@ -628,6 +639,7 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   p.num_n_tiles = (p.cols + TILE_COLS - 1) / TILE_COLS;
   p.num_m_tiles = (int32_t)((pr.M + BT - 1) / BT);
   p.a_scale = pr.a_scale;
+  p.W = pr.W;
   p.w_scale = pr.w_scale;
   p.bias = pr.bias;
   p.C = pr.C;
@@ -647,10 +659,7 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   const int64_t tiles = (int64_t)p.num_n_tiles * p.num_m_tiles;
   const int sms = device_sm_count();
   if (tiles > 0x7FFFFFFF - sms) return QW_ERR_UNSUPPORTED;  // counted in 32 bits
-  // a tile's K is split while the CTAs still fit the GPU at once and keep 1024 k each
-  int csize = 1;
-  if (BT < 256)
-    while (csize < 8 && tiles * csize * 2 <= sms && pr.K / (csize * 2) >= 1024) csize *= 2;
+  const int csize = split<BT>(tiles, pr.K, sms);
   p.csize = csize;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(csize > 1 || tiles < sms ? tiles * csize : sms));
@@ -674,9 +683,15 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
 
 qw_status launch_gemm_int8_tc(const Int8Problem& p, const void* codes16, bool gated, int32_t* err,
                               cudaStream_t st) {
-  if (p.M <= 64)
+  // The cheapest tile (us with 64, 128 and 256 tokens a tile, those of the rule in brackets:
+  // 333 x 1000 x 1040 [9.0] 9.5 13.4, 512 x 4096 x 4096 26.9 [21.4] 26.8, 256 x 4096 x 14336 55 [39] 71,
+  // 4096 x 14336 x 4096 [260] with 256.)  FP32 results do not leave 256 tokens' sums the registers.
+  const int sms = device_sm_count();
+  const int64_t c64 = cost<64>(p, gated, sms), c128 = cost<128>(p, gated, sms),
+                c256 = p.c_f32 ? INT64_MAX : cost<256>(p, gated, sms);
+  if (c64 <= c128 && c64 <= c256)
     return gated ? launch<64, true>(p, codes16, err, st) : launch<64, false>(p, codes16, err, st);
-  if (p.M <= 128 || p.c_f32)
+  if (c128 <= c256)
     return gated ? launch<128, true>(p, codes16, err, st) : launch<128, false>(p, codes16, err, st);
   return gated ? launch<256, true>(p, codes16, err, st) : launch<256, false>(p, codes16, err, st);
 }

@@ -444,7 +444,7 @@ qw_status qw_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, 
 // The workspace of an INT8 product: the activations' codes as its kernel takes them (INT8 for
 // the GEMV, FP16 for the tensor cores), then the scales of rows quantised in the call.
 static uint64_t int8_code_bytes(int64_t M, int32_t K) {
-  return (uint64_t)round_up(M * (int64_t)K * (M > kInt8GemvRows ? 2 : 1), 256);
+  return (uint64_t)round_up(M * (int64_t)K * (M > kInt8MmaRows ? 2 : 1), 256);
 }
 
 qw_status qgemm_int8_workspace_size(int32_t afmt, int64_t max_rows, int32_t N, int32_t K,
@@ -456,7 +456,7 @@ qw_status qgemm_int8_workspace_size(int32_t afmt, int64_t max_rows, int32_t N, i
   if (afmt == QW_A_BF16)
     *bytes = int8_code_bytes(max_rows, K) + (uint64_t)max_rows * 4;
   else
-    *bytes = max_rows > kInt8GemvRows ? int8_code_bytes(max_rows, K) : 0;
+    *bytes = max_rows > kInt8MmaRows ? int8_code_bytes(max_rows, K) : 0;
   return QW_OK;
 }
 
@@ -493,19 +493,20 @@ static qw_status int8_product(int32_t afmt, const void* A, int64_t lda, const fl
   p.N = N;
   p.K = K;
   p.c_f32 = c_type == QW_T_F32;
-  const bool tensor = M > kInt8GemvRows;
+  const bool wide = M > kInt8MmaRows;  // operands in FP16
   if (quantise) {
     float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + int8_code_bytes(M, K));
-    s = launch_quantize_int8(A, lda, M, K, workspace, scales, tensor, d_err, st);
+    s = launch_quantize_int8(A, lda, M, K, workspace, scales, wide, d_err, st);
     p.A = static_cast<const int8_t*>(workspace);
     p.lda = K;
     p.a_scale = scales;
-  } else if (tensor) {
+  } else if (wide) {
     s = launch_widen_int8(A, lda, M, K, workspace, st);
   }
   if (s != QW_OK) return s;
-  return tensor ? launch_gemm_int8_tc(p, workspace, gated, d_err, st)
-                : launch_gemv_int8(p, gated, quantise, d_err, st);
+  if (wide) return launch_gemm_int8_tc(p, workspace, gated, d_err, st);
+  return M > kInt8GemvRows ? launch_gemm_int8_mma(p, gated, d_err, st)
+                           : launch_gemv_int8(p, gated, quantise, d_err, st);
 }
 
 qw_status qgemm_int8(int32_t afmt, const void* A, int64_t lda, const float* a_scale,

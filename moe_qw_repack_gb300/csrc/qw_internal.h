@@ -121,10 +121,10 @@ struct Int8Problem {
 };
 // largest K whose 32-bit integer sums cannot overflow (128 * 128 * K < 2^31), K % 16 == 0
 constexpr int32_t kInt8MaxK = 131056;
-// Products of more tokens than this run on the tensor cores.  Measured at N = 14336, K = 4096 with
-// the dp4a kernel for 1, 2, 4 and 8 tokens: 12.8, 13.8, 17.4 and 21.7 us; the tensor cores take
-// 18 us for any of 3 to 64.
-constexpr int64_t kInt8GemvRows = 2;
+// One or two tokens: dp4a.  Up to kInt8MmaRows: mma.sync.  More: tcgen05.  At N = 14336, K = 4096
+// (us): 2 tokens 13.4 with dp4a, 14.1 with mma.sync; 4 tokens 17.4 and 14.1; 16 tokens 15.2 with
+// mma.sync, 20.2 with tcgen05; 32 tokens 38 and 19.6.
+constexpr int64_t kInt8GemvRows = 2, kInt8MmaRows = 16;
 // f16: write the codes as FP16 integers (the tensor-core kernel's operand) instead of INT8
 qw_status launch_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, void* Q,
                                float* scale, bool f16, int32_t* err, cudaStream_t st);
@@ -133,6 +133,8 @@ qw_status launch_widen_int8(const void* A, int64_t lda, int64_t M, int32_t K, vo
 // early: the call's own quantiser was enqueued directly before
 qw_status launch_gemv_int8(const Int8Problem& p, bool gated, bool early, int32_t* err,
                            cudaStream_t st);
+// M <= kInt8MmaRows
+qw_status launch_gemm_int8_mma(const Int8Problem& p, bool gated, int32_t* err, cudaStream_t st);
 // codes16: the activations' codes as FP16 [M][K] (p.A is not read)
 qw_status launch_gemm_int8_tc(const Int8Problem& p, const void* codes16, bool gated, int32_t* err,
                               cudaStream_t st);
