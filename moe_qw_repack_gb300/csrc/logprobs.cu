@@ -37,6 +37,7 @@ constexpr int RV = 4;               // vectors of a thread per block
 constexpr int CAP = 512;            // candidate buffer
 constexpr int NOTES = 32;           // blocks (or runs of them) whose threads' maxima are noted
 constexpr int HITS = 512;           // of them that the bound lets through to the list
+constexpr int VHITS = 256;          // ... and of their vectors
 constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
 
@@ -279,13 +280,14 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   constexpr int VE = E::VE;
   constexpr int ES = 16 / VE;
   extern __shared__ __align__(128) uint4 ring[];  // [STAGES][BLOCK]
-  __shared__ uint64_t buf[CAP];
+  __shared__ __align__(16) uint64_t buf[CAP];
   __shared__ uint64_t sorted[kLogprobsMaxTop];
-  __shared__ int cnt;
-  __shared__ float sets[32];               // largest logits of 32 sets of threads
+  __shared__ int cnt, merged;
+  __shared__ __align__(16) uint32_t sets[32];  // largest logits of 32 sets of threads, by their order
   __shared__ uint16_t note[NOTES][THREADS];  // upper bounds (BF16 bits) of a thread's maxima
   __shared__ uint16_t list[HITS];            // note x THREADS + thread
-  __shared__ int hits;
+  __shared__ int32_t vlist[VHITS];           // vectors of the row
+  __shared__ int hits, vhits;
   __shared__ Part wpart[WARPS];
   __shared__ Part part;  // this CTA's result; on rank 0, at the end, the row's
   __shared__ uint64_t full[STAGES];
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    cnt = hits = 0;
+    cnt = merged = hits = vhits = 0;
     abort_flag = 0;
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
     fence_barrier_init();
@@ -331,10 +333,10 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   const bool tok_ok = tok >= 0 && tok < a.V;
   // a value above every logit counts nothing
   const bool want_rank = tok_ok && a.token_rank;
-  const float xt = want_rank ? E::load(base, tok) : INFINITY;
+  const float xtok = tok_ok && (a.token_rank || a.token_logprob) ? E::load(base, tok) : INFINITY;
+  const float xt = want_rank ? xtok : INFINITY;
   const float xt_up = want_rank ? E::next_up(xt) : INFINITY;
-  // vectors with a logit before the token: equal logits count in them (what is too much in the
-  // token's own vector is taken back at the end)
+  // vectors with a logit before the token: equal logits count in them
   const int vlim = tok > head ? min(nv, (tok - head + VE - 1) / VE) : 0;
 
   // M: the logit the reference r was made from (LOW: none yet)
@@ -342,6 +344,12 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   uint64_t s2 = 0, t2 = 0;
   int above = 0;
   bool bad = false;
+  // ... and those of the token's own vector, if it begins before the token, from the token on are
+  // taken back
+  if (want_rank && tid < VE && vlim > vbeg && vlim <= vend) {
+    const int i = head + (vlim - 1) * VE + tid;
+    above = i >= tok && E::load(base, i) == xt ? -1 : 0;
+  }
   auto rise = [&](float m) {  // a new reference
     const float rn = m * LOG2E, d = r - rn, f = ex2(d);
     const uint64_t f2 = pack2(f, f);
@@ -363,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
       s2 = pack2(1.f, 0.f);
       t2 = pack2(fmaf(side, LOG2E, -r), 0.f);
     }
-    above = side > xt || (side == xt && side_id < tok);
+    above += side > xt || (side == xt && side_id < tok);
   }
 
   float pmax = -INFINITY;  // of this thread's vectors since the last note
@@ -380,37 +388,36 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     // (a thread reads only vectors that it filled itself or that the copy brings)
     (void)warp_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err);
     typename E::Count count{};
-    // two vectors at a time, so that their maximum is looked at once for both
-#pragma unroll 1
-    for (int j = 0; j < RV; j += 2) {
-      const int v = v0 + j * THREADS;
-      const uint4 x4 = blk[j * THREADS], z4 = blk[(j + 1) * THREADS];
-      const float vm = E::vmax(x4, z4);
-      pmax = fmaxf(pmax, vm);
-      if (vm >= xt) {  // (masked vectors behind the row are not above anything)
-        E::count(x4, v < vlim ? xt : xt_up, count);
-        E::count(z4, v + THREADS < vlim ? xt : xt_up, count);
-      }
-      if (!(vm < (M == E::LOW ? E::LOW : M + HEADROOM))) {
-        bad = bad || !(vm < INFINITY);
-        if (vm > E::LOW) rise(vm);
-      }
-      if (vm > E::LOW) {
-        const uint64_t l2 = pack2(LOG2E, LOG2E), nr = pack2(-r, -r);
-        auto sum = [&](const uint4& q) {
-          float x[VE];
-          E::unpack_floored(q, x);
+    // all at once, so that one look at their maximum decides for all (two at a time: 4096 x 131072
+    // BF16 200 us for 191)
+    uint4 x4[RV];
 #pragma unroll
-          for (int i = 0; i < VE; i += 2) {
-            const uint64_t y = fma2(pack2(x[i], x[i + 1]), l2, nr);
-            const float2 yy = unpack2(y);
-            const uint64_t e = pack2(ex2(yy.x), ex2(yy.y));
-            s2 = add2(s2, e);
-            t2 = fma2(e, y, t2);
-          }
-        };
-        sum(x4);
-        sum(z4);
+    for (int j = 0; j < RV; ++j) x4[j] = blk[j * THREADS];
+    static_assert(RV == 4);
+    const float vm = El<QW_T_F32>::max_nan(E::vmax(x4[0], x4[1]), E::vmax(x4[2], x4[3]));
+    pmax = fmaxf(pmax, vm);
+    if (vm >= xt) {  // (masked vectors behind the row are not above anything)
+#pragma unroll
+      for (int j = 0; j < RV; ++j) E::count(x4[j], v0 + j * THREADS < vlim ? xt : xt_up, count);
+    }
+    if (!(vm < (M == E::LOW ? E::LOW : M + HEADROOM))) {
+      bad = bad || !(vm < INFINITY);
+      if (vm > E::LOW) rise(vm);
+    }
+    if (vm > E::LOW) {
+      const uint64_t l2 = pack2(LOG2E, LOG2E), nr = pack2(-r, -r);
+#pragma unroll
+      for (int j = 0; j < RV; ++j) {
+        float x[VE];
+        E::unpack_floored(x4[j], x);
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) {
+          const uint64_t y = fma2(pack2(x[i], x[i + 1]), l2, nr);
+          const float2 yy = unpack2(y);
+          const uint64_t e = pack2(ex2(yy.x), ex2(yy.y));
+          s2 = add2(s2, e);
+          t2 = fma2(e, y, t2);
+        }
       }
     }
     if (want_rank) above += E::total(count);
@@ -432,6 +439,21 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
 
   rmax = fmaxf(rmax, pmax);
 
+  // the k largest of the buffer's n keys to `sorted`, in order
+  auto rank_keys = [&](int n) {
+    const ulonglong2* two = reinterpret_cast<const ulonglong2*>(buf);
+    for (int i = tid; i < n; i += THREADS) {
+      const uint64_t key = buf[i];
+      int before = (n & 1) && buf[n - 1] > key;
+#pragma unroll 8
+      for (int j = 0; j < n / 2; ++j) {
+        const ulonglong2 q = two[j];
+        before += (q.x > key) + (q.y > key);
+      }
+      if (before < k) sorted[before] = key;
+    }
+  };
+
   int settled = 0;  // keys in `sorted`
   if (k > 0) {
     // lower bound of the k-th key, and its value; -inf is never offered (the masked ids that
@@ -445,14 +467,17 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
       float m = rmax;
 #pragma unroll
       for (int o = 1; o < THREADS / 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      if (tid % (THREADS / 32) == 0) sets[tid / (THREADS / 32)] = m;
+      if (tid % (THREADS / 32) == 0) sets[tid / (THREADS / 32)] = order_of(m);
       __syncthreads();
-      const uint32_t g = order_of(sets[lane]);
+      const uint32_t g = sets[lane];
       int before = 0;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t o = __shfl_sync(0xFFFFFFFFu, g, i);
-        before += o > g || (o == g && i < lane);
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(sets + i);
+        before += o.x > g || (o.x == g && i < lane);
+        before += o.y > g || (o.y == g && i + 1 < lane);
+        before += o.z > g || (o.z == g && i + 2 < lane);
+        before += o.w > g || (o.w == g && i + 3 < lane);
       }
       const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, before == k - 1)) - 1;
       const uint64_t key = (uint64_t)__shfl_sync(0xFFFFFFFFu, g, owner) << 32;
@@ -473,42 +498,46 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
       else
         lost = true;
     };
-    auto offer_vector = [&](int v) {
-      const uint4 q = v < vend ? __ldg(vec + v) : E::masked();
-      if (!(E::vmax(q) >= thr_x)) return;
-      float f[VE];
-      E::unpack(q, f);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) offer(f[e], head + v * VE + e);
-    };
+#pragma unroll 4
     for (int i = 0; i < notes; ++i)
       if (__uint_as_float((uint32_t)note[i][tid] << 16) >= thr_x) {
         const int pos = atomicAdd(&hits, 1);
         if (pos < HITS) list[pos] = (uint16_t)(i * THREADS + tid);
       }
     __syncthreads();
+    // the last blocks are still in the ring
+    auto place = [&](int gb, int v) {
+      return gb + STAGES >= nblk ? ring + gb % STAGES * BLOCK + (v - vbeg - gb * BLOCK) : vec + v;
+    };
     const int listed = hits;
+    if (listed <= HITS) {
+      for (int b = 0; b < run; ++b)
+        for (int i = tid; i < listed * RV; i += THREADS) {
+          const int e = list[i / RV], gb = e / THREADS * run + b;
+          const int v = vbeg + gb * BLOCK + i % RV * THREADS + e % THREADS;
+          if (gb >= nblk || v >= vend || !(E::vmax(*place(gb, v)) >= thr_x)) continue;
+          const int pos = atomicAdd(&vhits, 1);
+          if (pos < VHITS) vlist[pos] = v;
+        }
+    }
+    __syncthreads();
+    const bool few = listed <= HITS && vhits <= VHITS;
+    const int found = vhits;
     for (;;) {
       if (side > -INFINITY) offer(side, side_id);
-      if (listed <= HITS) {
-        for (int b = 0; b < run; ++b)
-          for (int i = tid; i < listed * RV; i += THREADS) {
-            const int e = list[i / RV], gb = e / THREADS * run + b;
-            if (gb < nblk) offer_vector(vbeg + gb * BLOCK + i % RV * THREADS + e % THREADS);
-          }
+      if (few) {
+        // a logit to a thread (a vector to a thread: few of them work, and long)
+        for (int i = tid; i < found * VE; i += THREADS) {
+          const int v = vlist[i / VE];
+          offer(E::load(place((v - vbeg) / BLOCK, v), i % VE), head + v * VE + i % VE);
+        }
       } else {
-        for (int i = vbeg + tid; i < vend; i += THREADS) offer_vector(i);
+        for (int i = head + vbeg * VE + tid; i < head + vend * VE; i += THREADS)
+          offer(E::load(base, i), i);
       }
       const bool again = __syncthreads_or(lost);
       const int n = min(cnt, CAP);
-      // the buffer's k largest keys, in order
-      for (int i = tid; i < n; i += THREADS) {
-        const uint64_t key = buf[i];
-        int before = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) before += buf[j] > key;
-        if (before < k) sorted[before] = key;
-      }
+      rank_keys(n);
       __syncthreads();
       settled = min(n, k);
       if (!again) break;
@@ -535,55 +564,62 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   bad = __any_sync(0xFFFFFFFFu, bad);
   if (lane == 0) wpart[warp] = Part{rmax, r, s, t, above, bad ? 1 : 0, 0};
   __syncthreads();
-  if (tid == 0) {
-    Part p = wpart[0];
-    for (int w = 1; w < WARPS; ++w) {
-      merge(p.r, p.s, p.t, wpart[w].r, wpart[w].s, wpart[w].t);
-      p.rmax = fmaxf(p.rmax, wpart[w].rmax);
-      p.above += wpart[w].above;
-      p.bad |= wpart[w].bad;
+  // lane w of a warp has part w (and every WARPS-th lane the same again)
+  auto merge_parts = [&](Part p, int n) {
+    for (int o = 1; o < n; o <<= 1) {
+      merge(p.r, p.s, p.t, __shfl_xor_sync(0xFFFFFFFFu, p.r, o),
+            __shfl_xor_sync(0xFFFFFFFFu, p.s, o), __shfl_xor_sync(0xFFFFFFFFu, p.t, o));
+      p.rmax = fmaxf(p.rmax, __shfl_xor_sync(0xFFFFFFFFu, p.rmax, o));
+      p.above += __shfl_xor_sync(0xFFFFFFFFu, p.above, o);
+      p.bad |= __shfl_xor_sync(0xFFFFFFFFu, p.bad, o);
     }
+    return p;
+  };
+  if (warp == 0) {
+    Part p = merge_parts(wpart[lane % WARPS], WARPS);
     p.n = settled;
-    // the vector that holds the token was counted as lying before it: take back the equal
-    // logits from the token on
-    const int vt = tok >= head ? (tok - head) / VE : -1;
-    if (want_rank && vt >= vbeg && vt < vend && head + vt * VE < tok)
-      for (int i = tok; i < head + (vt + 1) * VE; ++i) p.above -= E::load(base, i) == xt;
-    part = p;
+    if (lane == 0) part = p;
   }
   if (csize > 1) {
     cluster_sync();  // every CTA's part and list are written
-    if (rank == 0) {
-      if (tid == 0) {
-        Part p = part;
-        for (int c = 1; c < csize; ++c) {
-          const uint32_t q = mapa_shared(smem_u32(&part), (uint32_t)c);
-          merge(p.r, p.s, p.t, ld_shared_cluster_f32(q + 4), ld_shared_cluster_f32(q + 8),
-                ld_shared_cluster_f32(q + 12));
-          p.rmax = fmaxf(p.rmax, ld_shared_cluster_f32(q));
-          p.above += (int32_t)ld_cluster_u32(q + 16);
-          p.bad |= (int32_t)ld_cluster_u32(q + 20);
-        }
-        part = p;
-      }
-      if (tid == 0) cnt = 0;
-      __syncthreads();
-      for (int i = tid; i < csize * k; i += THREADS) {
-        const int c = i / k, j = i - c * k;
-        if (j < (int)ld_cluster_u32(mapa_shared(smem_u32(&part), (uint32_t)c) + 24))
-          buf[atomicAdd(&cnt, 1)] = ld_cluster_u64(mapa_shared(smem_u32(&sorted[j]), (uint32_t)c));
-      }
+    if (rank != 0) {
+      cluster_sync();  // rank 0 has read
+      return;
     }
-    cluster_sync();  // rank 0 has read; the others may leave
-    if (rank != 0) return;
-    const int n = cnt;
-    for (int i = tid; i < n; i += THREADS) {
-      const uint64_t key = buf[i];
-      int before = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) before += buf[j] > key;
-      if (before < k) sorted[before] = key;
+    // Everything of the others is asked for at once: lane c has CTA c's part, and (sorted lists) warp
+    // c CTA c's keys.  Two bounds leave few of them: a CTA's k-th key, and the least of the CTAs'
+    // m-th, m x csize >= k.
+    static_assert(kLogprobsMaxTop <= 32 && MAX_CLUSTER <= WARPS, "a warp per list");
+    const int c = lane & (csize - 1), m = (k + csize - 1) / csize;
+    const uint32_t q = mapa_shared(smem_u32(&part), (uint32_t)c);
+    const int n_c = (int)ld_cluster_u32(q + offsetof(Part, n));
+    Part p{ld_shared_cluster_f32(q + offsetof(Part, rmax)),
+           ld_shared_cluster_f32(q + offsetof(Part, r)),
+           ld_shared_cluster_f32(q + offsetof(Part, s)),
+           ld_shared_cluster_f32(q + offsetof(Part, t)),
+           (int32_t)ld_cluster_u32(q + offsetof(Part, above)),
+           (int32_t)ld_cluster_u32(q + offsetof(Part, bad)),
+           0};
+    if (k > 0) {
+      const uint32_t list = mapa_shared(smem_u32(sorted), (uint32_t)c);
+      uint64_t kth = ld_cluster_u64(list + 8 * (k - 1)), mth = ld_cluster_u64(list + 8 * (m - 1));
+      const uint64_t key = ld_cluster_u64(
+          mapa_shared(smem_u32(sorted), (uint32_t)min(warp, csize - 1)) + 8 * min(lane, k - 1));
+      kth = n_c >= k ? kth : 0;  // (what lies past a list's end is anything)
+      mth = n_c >= m ? mth : 0;
+      for (int o = 1; o < csize; o <<= 1) {
+        kth = max(kth, __shfl_xor_sync(0xFFFFFFFFu, kth, o));
+        mth = min(mth, __shfl_xor_sync(0xFFFFFFFFu, mth, o));
+      }
+      if (lane < __shfl_sync(0xFFFFFFFFu, n_c, warp) && warp < csize && key >= max(kth, mth))
+        buf[atomicAdd(&merged, 1)] = key;
     }
+    if (warp == 0) p = merge_parts(p, csize);
+    cluster_arrive();  // this thread has read (the wait is at the end)
+    __syncthreads();
+    if (tid == 0) part = p;
+    const int n = merged;
+    rank_keys(n);
     settled = min(n, k);
   }
   __syncthreads();
@@ -630,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   if (tid == 0) {
     if (p.bad) set_error(a.err, QW_ERR_VALUE);
     if (a.tokens && !tok_ok) set_error(a.err, QW_ERR_INVALID_ARG);
-    if (a.token_logprob) a.token_logprob[row] = tok_ok ? logp(E::load(base, tok)) : nan;
+    if (a.token_logprob) a.token_logprob[row] = tok_ok ? logp(xtok) : nan;
     if (a.token_rank) a.token_rank[row] = tok_ok ? 1 + p.above : 0;
     if (a.entropy) a.entropy[row] = p.bad ? nan : none ? 0.f : ent;
   }
@@ -652,6 +688,10 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     const uint64_t key = tid < (k > settled ? cnt : settled) ? sorted[tid] : 0xFFFFFFFFull;
     a.top_ids[row * k + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
     a.top_logprobs[row * k + tid] = logp(value_of(key));
+  }
+  if (csize > 1) {
+    __syncwarp();
+    cluster_wait();
   }
 }
 
