@@ -720,11 +720,12 @@ qw_status launch_type(const LogprobsArgs& a, int64_t T, int csize, cudaStream_t 
 }  // namespace
 
 qw_status launch_logprobs(const LogprobsArgs& a, int32_t type, int64_t T, cudaStream_t st) {
-  // CTAs to a row: as many as give every SM two while each keeps 2048 logits.  (Splitting further,
-  // towards even rounds of the four CTAs that fit an SM, costs more than it gives: 777 x 50021 FP16
-  // 28.6 us with one CTA a row, 40.9 with two.)
+  // CTAs to a row: while there are fewer than SMs and each keeps 8192 logits.  (What a CTA does besides
+  // reading costs more than splitting further gives: 64 x 32003 FP32 8.6 us, 11.3 with 4096 logits each;
+  // 64 x 131072 BF16 11.1 us, 13.7 with two CTAs per SM; 777 x 50021 FP16 28.6 us with one CTA a row,
+  // 40.9 with two towards even rounds of the four CTAs that fit an SM.)
   int csize = 1;
-  while (csize < MAX_CLUSTER && T * csize < 2 * device_sm_count() && a.V / csize > 4096) csize *= 2;
+  while (csize < MAX_CLUSTER && T * csize < device_sm_count() && a.V / csize > 8192) csize *= 2;
   if (type == QW_T_F32) return launch_type<QW_T_F32>(a, T, csize, st);
   if (type == QW_T_F16) return launch_type<QW_T_F16>(a, T, csize, st);
   return launch_type<QW_T_BF16>(a, T, csize, st);
