@@ -34,6 +34,8 @@
 // Every wait is bounded; on expiry the kernel reports QW_ERR_TIMEOUT and shuts down.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "int8_map.cuh"
 #include "qw_common.cuh"
 #include "qw_internal.h"
@@ -92,6 +94,8 @@ struct Params {
   int32_t cols;       // output columns: N, or I of the gated form
   int32_t K;
   int32_t num_n_tiles, num_m_tiles;
+  int32_t group;         // token tiles of a group
+  uint32_t group_tiles;  // group x num_n_tiles
   const float* a_scale;
   const int8_t* W;
   const float* w_scale;
@@ -264,21 +268,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int rank = (int)(blockIdx.x % (unsigned)csize);
   const uint32_t cluster = blockIdx.x / (unsigned)csize, clusters = gridDim.x / (unsigned)csize;
   const uint32_t num_n = (uint32_t)p.num_n_tiles, num_tiles = (uint32_t)p.num_m_tiles * num_n;
-  // tile t = mt num_n + nt: the first of this cluster, and the step to its next
+  // Tile t: groups of `group` token tiles, in each the weight tiles in turn, for each the group's token
+  // tiles.
   struct Tile {
     uint32_t t, mt, nt;
   };
-  const Tile first{cluster, cluster / num_n, cluster % num_n};
-  const uint32_t step_m = clusters / num_n, step_n = clusters % num_n;
+  auto locate = [&](Tile& x) {
+    const uint32_t m0 = x.t / p.group_tiles * (uint32_t)p.group;
+    const uint32_t r = x.t % p.group_tiles, gm = min((uint32_t)p.group, (uint32_t)p.num_m_tiles - m0);
+    x.nt = r / gm;
+    x.mt = m0 + r % gm;
+  };
   auto next = [&](Tile& x) {
     x.t += clusters;
-    x.mt += step_m;
-    x.nt += step_n;
-    if (x.nt >= num_n) {
-      x.nt -= num_n;
-      ++x.mt;
-    }
+    if (x.t < num_tiles) locate(x);
   };
+  Tile first{cluster, 0, 0};
+  locate(first);
   // this CTA's k stages of every tile, in weight stages of two
   const int KWB = (p.K + KW - 1) / KW, kw_per = (KWB + csize - 1) / csize;
   const int kw_beg = min(KWB, rank * kw_per), kw_end = min(KWB, kw_beg + kw_per);
@@ -638,6 +644,12 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   constexpr int TILE_COLS = GATED ? BW / 2 : BW;
   p.num_n_tiles = (p.cols + TILE_COLS - 1) / TILE_COLS;
   p.num_m_tiles = (int32_t)((pr.M + BT - 1) / BT);
+  // What the CTAs work on at a time is then a few weight tiles for a group's token tiles, and all
+  // weights pass by once per group.  (us with groups of one tile, 8, 16, 32 and 64 MB: gated
+  // 4096 x 2x14336 x 4096 587, 553, 530, 536, 543; 16384 x 4096 x 4096 347, 330, 331, 344, 394.)
+  constexpr int64_t kGroupBytes = 16 << 20;
+  p.group = (int32_t)std::max<int64_t>(1, min64(p.num_m_tiles, kGroupBytes / ((int64_t)BT * pr.K * 2)));
+  p.group_tiles = (uint32_t)min64((int64_t)p.group * p.num_n_tiles, 0x7FFFFFFF);
   p.a_scale = pr.a_scale;
   p.W = pr.W;
   p.w_scale = pr.w_scale;
@@ -685,7 +697,7 @@ qw_status launch_gemm_int8_tc(const Int8Problem& p, const void* codes16, bool ga
                               cudaStream_t st) {
   // The cheapest tile (us with 64, 128 and 256 tokens a tile, those of the rule in brackets:
   // 333 x 1000 x 1040 [9.0] 9.5 13.4, 512 x 4096 x 4096 26.9 [21.4] 26.8, 256 x 4096 x 14336 55 [39] 71,
-  // 4096 x 14336 x 4096 [260] with 256.)  FP32 results do not leave 256 tokens' sums the registers.
+  // 4096 x 14336 x 4096 [258] with 256.)  FP32 results do not leave 256 tokens' sums the registers.
   const int sms = device_sm_count();
   const int64_t c64 = cost<64>(p, gated, sms), c128 = cost<128>(p, gated, sms),
                 c256 = p.c_f32 ? INT64_MAX : cost<256>(p, gated, sms);
