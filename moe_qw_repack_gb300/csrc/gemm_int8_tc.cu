@@ -35,6 +35,8 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <array>
+#include <type_traits>
 
 #include "int8_map.cuh"
 #include "qw_common.cuh"
@@ -138,6 +140,17 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fdividef(g, 1.f + __expf(-g)) * u;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 // What a thread does with the finished sums of its weight row: scale, bias, gate, round, store.
 template <bool GATED>
 struct Out {
@@ -157,13 +170,7 @@ struct Out {
     const bool odd = lane >= 16;
     const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 16);
     const float g = odd ? other : a, u = odd ? b : other;
-    return __fdividef(g, 1.f + __expf(-g)) * u;
-  }
-  __device__ __forceinline__ void put(int64_t m, float v) const {
-    if (c_f32)
-      static_cast<float*>(C)[m * ldc + n] = v;
-    else
-      static_cast<__nv_bfloat16*>(C)[m * ldc + n] = __float2bfloat16_rn(v);
+    return silu_mul(g, u);
   }
   // FP32 results (BT <= 128: for 256 tokens a tile the registers do not reach): 128 contiguous
   // bytes a token as they are.
@@ -538,53 +545,60 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if constexpr (BT < 256) {
     if (csize > 1) {
-      // every CTA's sums are in its shared memory; this one finishes tokens rank, rank + csize, ..
-      // of the tile (in pairs), adding the slices in rank order
+      // Every CTA's sums are in its shared memory; this one finishes tokens rank, rank + csize, .. of
+      // the tile, adding the slices in rank order.  A lane has four weight rows of a token.
       __syncwarp();  // single-lane roles have left their warps apart
+      const int64_t m0 = (int64_t)first.mt * BT;
+      const bool up = GATED && (lane & 4);
+      const int32_t n = (int32_t)(first.nt * TILE_COLS) +
+                        (GATED ? 16 * (lane >> 3) + 4 * (lane & 3) : 4 * lane);
+      float sw[4] = {}, bias[4] = {};
+      if (warp >= EPI_WARP0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < p.cols) {
+            const int64_t wrow = (int64_t)(up ? p.cols : 0) + n + j;
+            sw[j] = __ldg(p.w_scale + wrow);
+            if (p.bias) bias[j] = __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16);
+          }
+      }
       cluster_sync();
       if (warp >= EPI_WARP0 && *abort_flag == 0) {
-        const int q = warp & 3, w = (warp - EPI_WARP0) >> 2;
-        const int64_t m0 = (int64_t)first.mt * BT;
-        Out<GATED> out{};
-        out.C = p.C;
-        out.ldc = p.ldc;
-        out.c_f32 = p.c_f32;
-        out.lane = lane;
-        out.n = (int32_t)(first.nt * TILE_COLS) +
-                (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
-        out.nvalid = out.n < p.cols;
-        const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + out.n : out.n;
-        out.sw = out.nvalid ? __ldg(p.w_scale + wrow) : 0.f;
-        out.bias =
-            p.bias && out.nvalid ? __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16) : 0.f;
-        const int tokens = (int)min64(BT, p.M - m0);
-        // (four pairs at a time: their loads wait for each other's latency only once)
-        constexpr int U = 4;
-        for (int i0 = 2 * (rank + csize * w); i0 < tokens; i0 += 4 * csize * U) {
-          float sum[U][2] = {};
-          for (int c = 0; c < csize; ++c)
+        const int tokens = (int)min64(BT, p.M - m0), step = csize * NUM_EPI_WARPS;
+        // Two tokens at a time: one waits for more latencies, four are more instructions, which a CTA
+        // has to fetch for the few times that it runs them (us with 1, 2 and 4 tokens:
+        // 256 x 4096 x 4096 17.4, 16.6, 17.9; 128 x 1024 x 4096 10.0, 11.1, 12.7).
+        constexpr int U = 2;
+        for (int i0 = rank + csize * (warp - EPI_WARP0); i0 < tokens; i0 += step * U) {
+          float sum[U][4] = {}, sa[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int i = min(i0 + 4 * csize * u, BT - 2);
-              const uint32_t a =
-                  mapa_shared(smem_u32(sB) + (uint32_t)(i * BW + 32 * q + lane) * 4, c);
-              sum[u][0] += ld_shared_cluster_f32(a);
-              sum[u][1] += ld_shared_cluster_f32(a + BW * 4);
-            }
+          for (int u = 0; u < U; ++u)
+            sa[u] = i0 + step * u < tokens ? __ldg(p.a_scale + m0 + i0 + step * u) : 0.f;
+          for (int c = 0; c < csize; ++c) {
+            const uint32_t from = mapa_shared(smem_u32(sB) + lane * 16, (uint32_t)c);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (i0 + step * u < tokens) {
+                const float4 v = ld_cluster_f32x4(from + (uint32_t)(i0 + step * u) * (BW * 4));
+                sum[u][0] += v.x;
+                sum[u][1] += v.y;
+                sum[u][2] += v.z;
+                sum[u][3] += v.w;
+              }
+          }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int i = i0 + 4 * csize * u;
-            if (i >= tokens) break;
-            const bool second = i + 1 < tokens;
-            float a = out.value(sum[u][0], __ldg(p.a_scale + m0 + i));
-            const float b = out.value(sum[u][1], second ? __ldg(p.a_scale + m0 + i + 1) : 0.f);
-            if constexpr (GATED) {
-              a = out.gate(a, b);
-              const int odd = lane >> 4;
-              if (out.nvalid && (second || !odd)) out.put(m0 + i + odd, a);
-            } else if (out.nvalid) {
-              out.put(m0 + i, a);
-              if (second) out.put(m0 + i + 1, b);
+            if (i0 + step * u >= tokens) break;
+            const int64_t at = (m0 + i0 + step * u) * p.ldc + n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float y = fmaf(sum[u][j], sa[u] * sw[j], bias[j]);
+              if constexpr (GATED) y = silu_mul(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
+              if (up || n + j >= p.cols) continue;
+              if (p.c_f32)
+                static_cast<float*>(p.C)[at + j] = y;
+              else
+                static_cast<__nv_bfloat16*>(p.C)[at + j] = __float2bfloat16_rn(y);
             }
           }
         }
@@ -603,29 +617,60 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// CTAs that share a tile's K: as many as still fit the GPU at once and keep 1024 k each
+// Clusters of csize CTAs that run at once (fewer than SMs / csize: a cluster lies within one GPC)
 template <int BT>
-int split(int64_t tiles, int32_t K, int sms) {
-  int csize = 1;
-  if (BT < 256)
-    while (csize < 8 && tiles * csize * 2 <= sms && K / (csize * 2) >= 1024) csize *= 2;
-  return csize;
+int max_clusters(int csize) {
+  static const std::array<int, 4> n = [] {
+    std::array<int, 4> n{};
+    for (int i = 0; i < 4; ++i) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(1u << i);
+      cfg.blockDim = dim3(NUM_THREADS);
+      cfg.dynamicSmemBytes = Geo<BT>::SMEM;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 1u << i;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      if (cudaFuncSetAttribute(gemm_int8_tc_kernel<BT, false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)Geo<BT>::SMEM) != cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&n[i], gemm_int8_tc_kernel<BT, false>, &cfg) != cudaSuccess)
+        n[i] = i ? 0 : device_sm_count();
+    }
+    return n;
+  }();
+  return n[csize == 8 ? 3 : csize >> 1];
 }
 
-// What a product takes with tiles of BT tokens, in quarters of the time of one k at BT <= 128 (the
-// MMAs are then bound by the weight operand, whose 128 rows x 16 k take as long for 64 tokens as for
-// 128; 256 take 5/4 of it): each round of tiles over the SMs pays its k and its epilogue.
+struct Plan {
+  int64_t cost;
+  int csize;  // CTAs that share a tile's K
+};
+// The cheapest split of K with tiles of BT tokens, and what the product then takes in quarters of the
+// time of one k at BT <= 128 (the MMAs are bound by the weight operand there, whose 128 rows x 16 k
+// take as long for 64 tokens as for 128; 256 take 5/4 of it): each round of tiles over the SMs pays its
+// k and its epilogue, a split also the joining.
 template <int BT>
-int64_t cost(const Int8Problem& p, bool gated, int sms) {
+Plan plan(const Int8Problem& p, bool gated) {
   const int64_t n_tiles = gated ? (p.N / 2 + BW / 2 - 1) / (BW / 2) : (p.N + BW - 1) / BW;
   const int64_t tiles = n_tiles * ((p.M + BT - 1) / BT);
-  const int csize = split<BT>(tiles, p.K, sms);
-  const int64_t rounds = (tiles * csize + sms - 1) / sms;
-  return rounds * ((int64_t)(p.K / csize) * (BT == 256 ? 5 : 4) + (csize > 1 ? 24 : 8) * BT);
+  const int64_t rounds = (tiles + max_clusters<BT>(1) - 1) / max_clusters<BT>(1);
+  Plan best{rounds * ((int64_t)p.K * (BT == 256 ? 5 : 4) + 8 * BT), 1};
+  for (int c = 2; BT < 256 && c <= 8; c *= 2) {
+    const int stages = (p.K + KW - 1) / KW, per = (stages + c - 1) / c;
+    if (tiles > max_clusters<BT>(c) || p.K / c < 512) break;
+    if ((c - 1) * per >= stages) continue;  // every CTA has a share (its accumulator holds sums)
+    const int64_t cost = (int64_t)per * KW * 4 + 8 * BT + 2048;
+    if (cost < best.cost) best = Plan{cost, c};
+  }
+  return best;
 }
 
 template <int BT, bool GATED>
-qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaStream_t st) {
+qw_status launch(const Int8Problem& pr, const void* codes16, int csize, int32_t* err,
+                 cudaStream_t st) {
   using GE = Geo<BT>;
   CUtensorMap tmA, tmW;
   // A tile's rows past M: none are copied where M is below BT (whatever the stage holds there
@@ -671,7 +716,6 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
   const int64_t tiles = (int64_t)p.num_n_tiles * p.num_m_tiles;
   const int sms = device_sm_count();
   if (tiles > 0x7FFFFFFF - sms) return QW_ERR_UNSUPPORTED;  // counted in 32 bits
-  const int csize = split<BT>(tiles, pr.K, sms);
   p.csize = csize;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(csize > 1 || tiles < sms ? tiles * csize : sms));
@@ -696,16 +740,18 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int32_t* err, cudaS
 qw_status launch_gemm_int8_tc(const Int8Problem& p, const void* codes16, bool gated, int32_t* err,
                               cudaStream_t st) {
   // The cheapest tile (us with 64, 128 and 256 tokens a tile, those of the rule in brackets:
-  // 333 x 1000 x 1040 [9.0] 9.5 13.4, 512 x 4096 x 4096 26.9 [21.4] 26.8, 256 x 4096 x 14336 55 [39] 71,
+  // 333 x 1000 x 1040 [9.0] 9.5 13.4, 512 x 4096 x 4096 26.9 [21.4] 26.8, 256 x 4096 x 14336 55 [36] 71,
   // 4096 x 14336 x 4096 [258] with 256.)  FP32 results do not leave 256 tokens' sums the registers.
-  const int sms = device_sm_count();
-  const int64_t c64 = cost<64>(p, gated, sms), c128 = cost<128>(p, gated, sms),
-                c256 = p.c_f32 ? INT64_MAX : cost<256>(p, gated, sms);
-  if (c64 <= c128 && c64 <= c256)
-    return gated ? launch<64, true>(p, codes16, err, st) : launch<64, false>(p, codes16, err, st);
-  if (c128 <= c256)
-    return gated ? launch<128, true>(p, codes16, err, st) : launch<128, false>(p, codes16, err, st);
-  return gated ? launch<256, true>(p, codes16, err, st) : launch<256, false>(p, codes16, err, st);
+  const Plan p64 = plan<64>(p, gated), p128 = plan<128>(p, gated), p256 = plan<256>(p, gated);
+  const bool use256 = !p.c_f32 && p256.cost < std::min(p64.cost, p128.cost);
+  auto go = [&](auto bt, const Plan& l) {
+    constexpr int BT = decltype(bt)::value;
+    return gated ? launch<BT, true>(p, codes16, l.csize, err, st)
+                 : launch<BT, false>(p, codes16, l.csize, err, st);
+  };
+  if (use256) return go(std::integral_constant<int, 256>{}, p256);
+  if (p128.cost < p64.cost) return go(std::integral_constant<int, 128>{}, p128);
+  return go(std::integral_constant<int, 64>{}, p64);
 }
 
 }  // namespace qw
