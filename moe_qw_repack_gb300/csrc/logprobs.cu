@@ -10,7 +10,7 @@
 // Alternatives: ids are ordered by a 64-bit key (the value's bits as an ordered integer above the
 // complement of the id), so ties need no second pass.  While the row streams by, a thread only notes
 // the largest logit of its vectors of each block (rounded up to 16 bits).  At the end the topk-th
-// largest of 32 sets of threads' maxima bounds the topk-th key from below (topk different logits are
+// largest of 64 sets of threads' maxima bounds the topk-th key from below (topk different logits are
 // at least that); what reaches it, about topk threads' vectors of some block, is listed and read
 // once more, from L2, a vector to a thread, and the logits at or above the bound are ranked.  Where
 // very many reach it (rows of ties), the bound rises to the topk-th key of a full buffer until what
@@ -35,6 +35,7 @@ namespace {
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int RV = 4;               // vectors of a thread per block
 constexpr int CAP = 512;            // candidate buffer
+constexpr int SETS = 64;            // sets of threads whose largest logits bound the k-th
 constexpr int NOTES = 32;           // blocks (or runs of them) whose threads' maxima are noted
 constexpr int HITS = 512;           // of them that the bound lets through to the list
 constexpr int VHITS = 256;          // ... and of their vectors
@@ -283,7 +284,8 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
   __shared__ __align__(16) uint64_t buf[CAP];
   __shared__ uint64_t sorted[kLogprobsMaxTop];
   __shared__ int cnt, merged;
-  __shared__ __align__(16) uint32_t sets[32];  // largest logits of 32 sets of threads, by their order
+  __shared__ uint32_t largest[THREADS];  // of each thread's logits, by their order
+  __shared__ uint32_t kth;
   __shared__ uint16_t note[NOTES][THREADS];  // upper bounds (BF16 bits) of a thread's maxima
   __shared__ uint16_t list[HITS];            // note x THREADS + thread
   __shared__ int32_t vlist[VHITS];           // vectors of the row
@@ -462,25 +464,30 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     uint64_t thr = (uint64_t)order_of(kLowest) << 32;
     float thr_x = kLowest;
     {
-      // the k-th largest of the maxima of 32 sets of threads, one a lane (the logits beside the
-      // vectors may be among them: they are offered too)
-      float m = rmax;
-#pragma unroll
-      for (int o = 1; o < THREADS / 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      if (tid % (THREADS / 32) == 0) sets[tid / (THREADS / 32)] = order_of(m);
+      // The k-th largest of the maxima of 64 sets of threads (the logits beside the vectors may be
+      // among them: they are offered too).  A warp has all of them, two a lane, and looks at eight.
+      // (32 sets leave k / 32 of them below the bound's set: with k = 32 the bound was the least of
+      // all and let 200 logits and more through.  Sets of threads that lie 64 apart have logits of
+      // their own even where a row has few vectors.)
+      largest[tid] = order_of(rmax);
       __syncthreads();
-      const uint32_t g = sets[lane];
-      int before = 0;
+      uint32_t lo = 0, hi = 0;
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const uint4 o = *reinterpret_cast<const uint4*>(sets + i);
-        before += o.x > g || (o.x == g && i < lane);
-        before += o.y > g || (o.y == g && i + 1 < lane);
-        before += o.z > g || (o.z == g && i + 2 < lane);
-        before += o.w > g || (o.w == g && i + 3 < lane);
+      for (int i = 0; i < THREADS; i += SETS) {
+        lo = max(lo, largest[i + lane]);
+        hi = max(hi, largest[i + 32 + lane]);
       }
-      const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, before == k - 1)) - 1;
-      const uint64_t key = (uint64_t)__shfl_sync(0xFFFFFFFFu, g, owner) << 32;
+      static_assert(SETS == 64 && SETS / WARPS * WARPS == SETS && kLogprobsMaxTop <= SETS);
+#pragma unroll
+      for (int i = 0; i < SETS / WARPS; ++i) {
+        const int at = warp * (SETS / WARPS) + i;  // a set; equal ones in this order
+        const uint32_t v = __shfl_sync(0xFFFFFFFFu, at < 32 ? lo : hi, at & 31);
+        const int before = __popc(__ballot_sync(0xFFFFFFFFu, lo > v || (lo == v && lane < at))) +
+                           __popc(__ballot_sync(0xFFFFFFFFu, hi > v || (hi == v && lane + 32 < at)));
+        if (before == k - 1 && lane == 0) kth = v;
+      }
+      __syncthreads();
+      const uint64_t key = (uint64_t)kth << 32;
       if (key > thr) {
         thr = key;
         thr_x = value_of(key);
