@@ -19,12 +19,16 @@
 // 20 alternatives at 264 us: the candidates' latency stood in the stream's way.  Reading again whole
 // quarters of a thread's blocks: 304 us.)
 //
-// Bound: the row is read once (HBM); the work per logit is one exponential and about seven
+// Bound: the row is read once (HBM); the work per logit is one exponential and about nine
 // instructions.  A CTA of 256 threads takes a row through a ring of bulk-copied blocks in shared
-// memory; few long rows are split over the CTAs of a cluster, whose rank 0 merges the partial
-// results through distributed shared memory in a fixed order.
+// memory.  Few long rows are split over the CTAs of a cluster, whose rank 0 merges the partial
+// results through distributed shared memory in a fixed order; many short ones go to CTAs of 128 or
+// 64 threads.  (4096 x 131072 BF16 with 20 alternatives: 188 us = 0.84 of the copy rate; without
+// alternatives 161 us.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "qw_common.cuh"
 #include "qw_internal.h"
@@ -32,11 +36,9 @@
 namespace qw {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int RV = 4;               // vectors of a thread per block
 constexpr int CAP = 512;            // candidate buffer
 constexpr int SETS = 64;            // sets of threads whose largest logits bound the k-th
-constexpr int NOTES = 32;           // blocks (or runs of them) whose threads' maxima are noted
 constexpr int HITS = 512;           // of them that the bound lets through to the list
 constexpr int VHITS = 256;          // ... and of their vectors
 constexpr int MAX_CLUSTER = 8;
@@ -261,10 +263,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-// One block of a CTA's vectors, in shared memory.
-constexpr int BLOCK = THREADS * RV;
-constexpr int STAGES = 2;
-constexpr size_t RING_BYTES = (size_t)STAGES * BLOCK * 16;
+constexpr int STAGES = 2;  // blocks of vectors in shared memory
+template <int THREADS>
+constexpr size_t ring_bytes() {
+  return (size_t)STAGES * THREADS * RV * 16;
+}
 // a reference is kept until a logit passes it by more than this (2^12 x 2^31 terms stay finite,
 // and the entropy, a difference of two numbers of that many bits, loses four of its own)
 constexpr float HEADROOM = 8.f;
@@ -275,9 +278,13 @@ __device__ __forceinline__ uint16_t bf16_above(float x) {
   return (uint16_t)(((b & 0x80000000u) ? b : b + 0xFFFFu) >> 16);
 }
 
-template <int TYPE>
-__global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs a, const int csize) {
+template <int TYPE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    logprobs_kernel(const LogprobsArgs a, const int csize) {
   using E = El<TYPE>;
+  constexpr int WARPS = THREADS / 32;
+  constexpr int BLOCK = THREADS * RV;               // vectors of a block
+  constexpr int NOTES = THREADS == 256 ? 32 : THREADS == 128 ? 16 : 4;  // blocks (or runs) noted
   constexpr int VE = E::VE;
   constexpr int ES = 16 / VE;
   extern __shared__ __align__(128) uint4 ring[];  // [STAGES][BLOCK]
@@ -587,7 +594,7 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     p.n = settled;
     if (lane == 0) part = p;
   }
-  if (csize > 1) {
+  if (THREADS == 256 && csize > 1) {
     cluster_sync();  // every CTA's part and list are written
     if (rank != 0) {
       cluster_sync();  // rank 0 has read
@@ -596,7 +603,8 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     // Everything of the others is asked for at once: lane c has CTA c's part, and (sorted lists) warp
     // c CTA c's keys.  Two bounds leave few of them: a CTA's k-th key, and the least of the CTAs'
     // m-th, m x csize >= k.
-    static_assert(kLogprobsMaxTop <= 32 && MAX_CLUSTER <= WARPS, "a warp per list");
+    static_assert(kLogprobsMaxTop <= 32 && (MAX_CLUSTER <= WARPS || THREADS < 256),
+                  "a warp per list");
     const int c = lane & (csize - 1), m = (k + csize - 1) / csize;
     const uint32_t q = mapa_shared(smem_u32(&part), (uint32_t)c);
     const int n_c = (int)ld_cluster_u32(q + offsetof(Part, n));
@@ -696,19 +704,20 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobsArgs
     a.top_ids[row * k + tid] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
     a.top_logprobs[row * k + tid] = logp(value_of(key));
   }
-  if (csize > 1) {
+  if (THREADS == 256 && csize > 1) {
     __syncwarp();
     cluster_wait();
   }
 }
 
-template <int TYPE>
+template <int TYPE, int THREADS>
 qw_status launch_type(const LogprobsArgs& a, int64_t T, int csize, cudaStream_t st) {
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      logprobs_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES);
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(logprobs_kernel<TYPE, THREADS>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring_bytes<THREADS>());
   if (attr != cudaSuccess) return QW_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.dynamicSmemBytes = RING_BYTES;
+  cfg.dynamicSmemBytes = ring_bytes<THREADS>();
   cfg.gridDim = dim3((unsigned)(T * csize));
   cfg.blockDim = dim3(THREADS);
   cfg.stream = st;
@@ -720,7 +729,7 @@ qw_status launch_type(const LogprobsArgs& a, int64_t T, int csize, cudaStream_t 
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = csize > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<TYPE>, a, csize) == cudaSuccess ? QW_OK
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<TYPE, THREADS>, a, csize) == cudaSuccess ? QW_OK
                                                                                    : QW_ERR_CUDA;
 }
 
@@ -733,9 +742,24 @@ qw_status launch_logprobs(const LogprobsArgs& a, int32_t type, int64_t T, cudaSt
   // 40.9 with two towards even rounds of the four CTAs that fit an SM.)
   int csize = 1;
   while (csize < MAX_CLUSTER && T * csize < device_sm_count() && a.V / csize > 8192) csize *= 2;
-  if (type == QW_T_F32) return launch_type<QW_T_F32>(a, T, csize, st);
-  if (type == QW_T_F16) return launch_type<QW_T_F16>(a, T, csize, st);
-  return launch_type<QW_T_BF16>(a, T, csize, st);
+  // Many rows: smaller CTAs, so that more rows are under way and one's ends hide under others' middles
+  // (us with 256, 128 and 64 threads: 4000 x 2000 BF16 42, 28, 24; 4000 x 8000 BF16 43, 35, 35;
+  // 4000 x 50021 FP16 98, 85; but 777 x 50021 27.0, 28.6; 1000 x 131072 BF16 54, 58; 2048 x 131072 FP32
+  // 174, 178).
+  const int64_t vectors = (int64_t)a.V * (type == QW_T_F32 ? 4 : 2) / 16, sms = device_sm_count();
+  const int threads = T <= 4 * sms                                             ? 256
+                      : vectors <= 256                                         ? 64
+                      : vectors <= 1024 || (vectors <= 6400 && T > 8 * sms) ? 128
+                                                                               : 256;
+  auto go = [&](auto t) {
+    constexpr int TYPE = decltype(t)::value;
+    return threads == 256   ? launch_type<TYPE, 256>(a, T, csize, st)
+           : threads == 128 ? launch_type<TYPE, 128>(a, T, 1, st)
+                            : launch_type<TYPE, 64>(a, T, 1, st);
+  };
+  if (type == QW_T_F32) return go(std::integral_constant<int, QW_T_F32>{});
+  if (type == QW_T_F16) return go(std::integral_constant<int, QW_T_F16>{});
+  return go(std::integral_constant<int, QW_T_BF16>{});
 }
 
 }  // namespace qw
