@@ -247,7 +247,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1 + NUM_CVT_WARPS / 2);  // the tokens' copy and a converter group
@@ -307,8 +306,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   // What is above overlaps the previous kernel's tail; everything else comes after this, the
   // first use of the tensor maps included: they lie in the launch's parameters, whose addresses
-  // are used again by later launches, and an SM may hold a map of an earlier one until here.
+  // are used again by later launches, and an SM may hold a map of an earlier one until here.  The next
+  // kernel may start now: whatever came before this call is complete.
   pdl_wait();
+  pdl_launch_dependents();
 
   if (warp < CVT_WARP0) {
     regs_dec<MISC_REGS>();

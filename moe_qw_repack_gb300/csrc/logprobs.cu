@@ -546,8 +546,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
           offer(E::load(place((v - vbeg) / BLOCK, v), i % VE), head + v * VE + i % VE);
         }
       } else {
-        for (int i = head + vbeg * VE + tid; i < head + vend * VE; i += THREADS)
-          offer(E::load(base, i), i);
+        for (int64_t i = head + vbeg * VE + tid; i < head + vend * VE; i += THREADS)
+          offer(E::load(base, i), (int32_t)i);
       }
       const bool again = __syncthreads_or(lost);
       const int n = min(cnt, CAP);
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   if (low) {
     // every logit is at or below LOW: sum against the maximum itself
     float sl = 0.f, tl = 0.f;
-    for (int32_t i = tid; i < a.V; i += THREADS) {
+    for (int64_t i = tid; i < a.V; i += THREADS) {
       const float y = fmaxf((E::load(base, i) - p.rmax) * LOG2E, -1e4f), e = ex2(y);
       sl += e;
       tl += e * y;
@@ -688,11 +688,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   if (tid == 0) cnt = settled;
   if (k > settled && warp == 0) {
     // fewer ids than asked for are left by the mask: the masked ones follow in id order
-    for (int32_t i0 = 0, n = settled; i0 < a.V && n < k; i0 += 32) {
+    int n = settled;
+    for (int64_t i0 = 0; i0 < a.V && n < k; i0 += 32) {
       const bool gone = i0 + lane < a.V && E::load(base, i0 + lane) == -INFINITY;
       const uint32_t set = __ballot_sync(0xFFFFFFFFu, gone);
       const int at = n + __popc(set & ((1u << lane) - 1u));
-      if (gone && at < k) sorted[at] = order_key(-INFINITY, i0 + lane);
+      if (gone && at < k) sorted[at] = order_key(-INFINITY, (int32_t)i0 + lane);
       n += __popc(set);
       if (lane == 0) cnt = min(n, k);
     }

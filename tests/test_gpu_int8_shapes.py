@@ -44,3 +44,14 @@ def test_drawn_shapes(seed):
     afmt = qw().QW_A_INT8_TOKEN if seed % 2 else None
     check(p, call(p, afmt=afmt, ldc_pad=seed % 5))
     check_gated(p, call(p, afmt=afmt, gated=True))
+
+
+@pytest.mark.parametrize("M,N", [(1, 20), (2, 34), (9, 20), (40, 36), (130, 30)])
+def test_longest_k(M, N):
+    """K = 131056: the largest 32-bit sum (every code -128) among them."""
+    K = 131056
+    p = problem(M, N, K, M, a="int8", extreme=True)
+    check(p, call(p, c_type=qw().QW_T_F32), f32=True)
+    check_gated(p, call(p, gated=True))
+    p = problem(M, N, K, M + 1, bias=True)
+    check(p, call(p))
