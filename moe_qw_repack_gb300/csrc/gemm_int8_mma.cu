@@ -5,9 +5,9 @@
 // conversion, eight tokens more cost 8.5 us where these cost 2 at 14336 x 4096.)
 //
 // Bound: the weights' bytes, as long as the MMAs (weights as the 16-row operand, eight tokens a
-// column group) hide under them.  tcgen05 takes as long for 8 tokens as for 64 - its weight operand
-// passes through tensor memory at the same rate - and that is more than the bytes take: 14336 x 4096
-// with 16 tokens 20.2 us there, 15.2 here; with 32 tokens 19.6 there, 38 here.
+// column group) hide under them.  Small blocks of rows keep every SM reading, where tcgen05's tiles
+// of 128 rows leave a part of the SMs idle and each CTA a longer pipeline to fill: 14336 x 4096 with 16
+// tokens 20.2 us there, 15.2 here; with 32 tokens 19.6 there, 38 here.
 //
 // A CTA of eight computing warps and one that copies has BR weight rows (gated: BR / 2 gate rows,
 // then the up rows of the same outputs) and all of K, or a cluster's share of it.  Weights and tokens
