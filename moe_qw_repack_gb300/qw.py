@@ -146,7 +146,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:  # the current stream's handle without building a Stream object (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
