@@ -225,10 +225,17 @@ qw_status launch(const Int8Problem& p, int32_t* err, cudaStream_t st) {
   constexpr int OUTS = GATED ? BR / 2 : BR;
   const int32_t cols = GATED ? p.N / 2 : p.N;
   const int64_t blocks = ((int64_t)cols + OUTS - 1) / OUTS;
-  // few blocks share K out over clusters while each CTA keeps a chunk of it
+  // Few blocks share K out over clusters while each CTA keeps a chunk of it; with a little more than one
+  // block per SM that evens the SMs' loads out, and pays where much K is left (us without and with:
+  // 16 x 5120 x 8192 17.0, 15.6; 16 x 6144 x 16384 28.9, 24.1; but 16 x 6144 x 2048 7.1, 7.6 and
+  // 16 x 7168 x 8192 17.5, 17.7).
   const int sms = device_sm_count();
+  auto split = [&](int c) {
+    return p.K / (2 * c) >= CK &&
+           (blocks * c <= sms || (10 * blocks * c <= 13 * sms && p.K / (2 * c) >= 5 * CK));
+  };
   int csize = 1;
-  while (csize < 8 && blocks * csize <= sms && p.K / (2 * csize) >= CK) csize *= 2;
+  while (csize < 8 && split(csize)) csize *= 2;
   const int32_t k_len = ((p.K + csize - 1) / csize + CK - 1) / CK * CK;
   csize = (p.K + k_len - 1) / k_len;
   CUtensorMap tmA, tmW;
