@@ -377,8 +377,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     rmax = side;
     if (side > E::LOW) {
       rise(side);
-      s2 = pack2(1.f, 0.f);
-      t2 = pack2(fmaf(side, LOG2E, -r), 0.f);
+      const float y = fmaf(side, LOG2E, -r), e = ex2(y);  // (y: what r lost in rounding)
+      s2 = pack2(e, 0.f);
+      t2 = pack2(e * y, 0.f);
     }
     above += side > xt || (side == xt && side_id < tok);
   }
