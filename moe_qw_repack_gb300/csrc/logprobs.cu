@@ -5,7 +5,10 @@
 // times log2(e), rounded): s = sum 2^y and t = sum 2^y y.  A new reference r' rescales
 // t <- 2^(r-r') (t + s (r - r')), s <- 2^(r-r') s, which also merges the partial sums of threads,
 // warps and CTAs.  Then log p(x) = ln2 (x log2(e) - r - log2 s) and the entropy is
-// ln2 (log2 s - t / s): r's own rounding cancels, so rows of large logits lose nothing.
+// ln2 (log2 s - t / s).  r's own rounding cancels there, but it is part of every y: half a unit of r,
+// which is 2 at |x| = 2^25 and would leave 2^y nothing (or infinity) from about 2^31 on.  So sums leave
+// out what is below LOW, and a row whose largest logit is far from 0 (2^24 and more) is summed once
+// more, against that logit itself.
 //
 // Alternatives: ids are ordered by a 64-bit key (the value's bits as an ordered integer above the
 // complement of the id), so ties need no second pass.  While the row streams by, a thread only notes
@@ -44,16 +47,16 @@ constexpr int VHITS = 256;          // ... and of their vectors
 constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
 
-// Per element type: values per 16-byte vector; `LOW`: sums skip vectors whose maximum is not
-// above it (next to anything larger they are zero; rows that have nothing larger are summed
-// by slow_row); `FLOOR`: what -inf is replaced with inside a vector, far enough below LOW to
-// stay zero and finite, so that 0 * y never is 0 * inf.
+// Per element type: VE, values per 16-byte vector; LOW: sums skip vectors whose maximum is not above it,
+// and unpack_floored raises smaller values to it (FP16: to the lowest finite one), so that 0 * y never is
+// 0 * inf; ROW_LOW, ROW_HIGH: the sums stand if the row's maximum is above the one and not above the other
+// (next to such a maximum everything at or below LOW is zero), else the row is summed against its maximum.
 template <int TYPE>
 struct El;
 template <>
 struct El<QW_T_F32> {
   static constexpr int VE = 4;
-  static constexpr float LOW = -1e30f;
+  static constexpr float LOW = -0x1p25f, ROW_LOW = -0x1p24f, ROW_HIGH = 0x1p24f;
   static __device__ __forceinline__ float load(const void* p, int64_t i) {
     return static_cast<const float*>(p)[i];
   }
@@ -178,7 +181,7 @@ struct El16 {
 };
 template <>
 struct El<QW_T_BF16> : El16<__nv_bfloat162> {
-  static constexpr float LOW = -1e30f;
+  static constexpr float LOW = -0x1p25f, ROW_LOW = -0x1p24f, ROW_HIGH = 0x1p24f;
   static __device__ __forceinline__ float load(const void* p, int64_t i) {
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
   }
@@ -188,7 +191,8 @@ struct El<QW_T_BF16> : El16<__nv_bfloat162> {
 };
 template <>
 struct El<QW_T_F16> : El16<__half2> {
-  static constexpr float LOW = -60000.f;  // FP16 values next to it are 32 apart
+  // FP16 values next to it are 32 apart
+  static constexpr float LOW = -60000.f, ROW_LOW = LOW, ROW_HIGH = 65504.f;
   static __device__ __forceinline__ float load(const void* p, int64_t i) {
     return __half2float(static_cast<const __half*>(p)[i]);
   }
@@ -268,8 +272,9 @@ template <int THREADS>
 constexpr size_t ring_bytes() {
   return (size_t)STAGES * THREADS * RV * 16;
 }
-// a reference is kept until a logit passes it by more than this (2^12 x 2^31 terms stay finite,
-// and the entropy, a difference of two numbers of that many bits, loses four of its own)
+// a reference is kept until a logit passes it by more than this (2^12 x 2^31 terms stay finite, 2^14 x 2^31
+// with the rounding of a reference of 2^25; and the entropy, a difference of two numbers of that many
+// bits, loses four of its own)
 constexpr float HEADROOM = 8.f;
 
 // BF16 bits of a number that is x or above it
@@ -642,11 +647,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 
   const Part p = part;
   const bool none = p.rmax == -INFINITY;
-  const bool low = !none && !p.bad && p.rmax <= E::LOW;
+  const bool far = !none && !p.bad && (p.rmax <= E::ROW_LOW || p.rmax > E::ROW_HIGH);
   const float ref = p.r;
   float l2s = log2f(p.s), ent = (l2s - p.t / p.s) * LN2;
-  if (low) {
-    // every logit is at or below LOW: sum against the maximum itself
+  if (far) {
+    // (in slow motion: rows like this are masked ones, or broken)
     float sl = 0.f, tl = 0.f;
     for (int64_t i = tid; i < a.V; i += THREADS) {
       const float y = fmaxf((E::load(base, i) - p.rmax) * LOG2E, -1e4f), e = ex2(y);
@@ -675,7 +680,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   auto logp = [&](float x) {
     if (p.bad) return nan;
     if (none) return -INFINITY;
-    if (low) return (x - p.rmax) - l2s * LN2;
+    if (far) return (x - p.rmax) - l2s * LN2;
     if (x < -1e30f) return x - p.rmax;  // x log2(e) may overflow; log s is lost beside it
     return (fmaf(x, LOG2E, -ref) - l2s) * LN2;
   };
