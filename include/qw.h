@@ -406,9 +406,10 @@ qw_status qgemm_moe_grouped_indexed(const qw_packed_desc* desc, const void* w_pa
  * [N][K], contiguous, any value -128 .. 127, and FP32 scales [N]; nothing is repacked.
  *
  * qw_quantize_int8 - BF16 rows -> INT8 codes and a scale per row:
- *   A_scale[r] = amax_r / 127,  A_q[r][k] = rint(A[r][k] * min(127 / amax_r, FLT_MAX))
- *   with amax_r the row's largest magnitude; FP32 arithmetic, ties to even (a row of zeros
- *   has scale 0).  A: BF16, row pitch lda >= K elements; A_q: INT8 [rows][K]; A_scale: FP32
+ *   A_scale[r] = amax_r / 127,  A_q[r][k] = rint(A[r][k] * (127 / amax_r))
+ *   with amax_r the row's largest magnitude; FP32 roundings (of the quotient as if FP32's range
+ *   had no end), ties to even.  A row without a normal number (amax_r < 2^-126) has codes 0, a
+ *   row of zeros also the scale 0.  A: BF16, row pitch lda >= K elements; A_q: INT8 [rows][K]; A_scale: FP32
  *   [rows].  1 <= K, K % 16 == 0 (else QW_ERR_UNSUPPORTED); A and A_q 16-byte aligned, lda a
  *   multiple of 8.  A row with a non-finite value sets QW_ERR_VALUE in d_err, gets the scale
  *   NaN and codes 0 (a product with it is NaN, not a plausible number).

@@ -1,7 +1,7 @@
 // int8.cu - the INT8 product with a scale per token and per output channel, its gated form,
 // and the per-token quantiser in front of them.
 //
-//   q[m][k] = rint(a[m][k] * min(127 / amax_m, FLT_MAX)),  sa_m = amax_m / 127
+//   q[m][k] = rint(a[m][k] * (127 / amax_m)),  sa_m = amax_m / 127
 //   C[m][n] = sa_m * sw_n * sum_k q[m][k] w[n][k] + bias[n]
 //   Y[m][i] = silu(C[m][i]) * C[m][I + i]                               (gated)
 #include <cuda_bf16.h>
@@ -26,18 +26,21 @@ __device__ __forceinline__ uint32_t bf16x8_absmax(const uint4& v) {
 }
 
 // A row's scale and codes from its largest magnitude (BF16 bits).  A row with a non-finite value has
-// the scale NaN and codes 0.
+// the scale NaN and codes 0.  Below 2^-121 the quotient 127 / amax may pass FP32's range: such a row is
+// multiplied by 2^64 first, which is exact.  A row without a normal number has codes 0: its scale would
+// keep too few bits.
 struct RowScale {
   // adding 1.5 * 2^23 rounds |x| < 2^22 to an integer (ties to even), which the sum's low bits hold
   // in two's complement
   static constexpr float kRound = 12582912.f;
   bool finite;
-  float scale, inv;
+  float scale, up, inv;
   __device__ __forceinline__ explicit RowScale(uint32_t amax) {
     const float top = __uint_as_float(amax << 16);
     finite = amax < 0x7F80u;
     scale = finite ? top / 127.0f : __uint_as_float(0x7FC00000u);
-    inv = fminf(127.0f / top, 3.4028234663852886e38f);
+    up = amax < 0x0300u ? 0x1p64f : 1.f;  // (0x0300: 2^-121)
+    inv = amax < 0x0080u ? 0.f : 127.0f / (top * up);
   }
   // eight values' codes plus kRound; the product is rounded to FP32 before the code is (no fused
   // multiply-add)
@@ -45,8 +48,8 @@ struct RowScale {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      q[2 * j] = finite ? __fadd_rn(__fmul_rn(bf16_lo(w[j]), inv), kRound) : kRound;
-      q[2 * j + 1] = finite ? __fadd_rn(__fmul_rn(bf16_hi(w[j]), inv), kRound) : kRound;
+      q[2 * j] = finite ? __fadd_rn(__fmul_rn(bf16_lo(w[j]) * up, inv), kRound) : kRound;
+      q[2 * j + 1] = finite ? __fadd_rn(__fmul_rn(bf16_hi(w[j]) * up, inv), kRound) : kRound;
     }
   }
   __device__ __forceinline__ uint2 codes(const uint4& v) const {
