@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(NUM_THREADS, CTAS_PER_SM)
         v[h] = sum * (sa * __ldg(p.w_scale + wr));
         if (p.bias) v[h] += __uint_as_float((uint32_t)__ldg(p.bias + wr) << 16);
       }
-      const float y = GATED ? v[0] / (1.f + expf(-v[0])) * v[GATED ? 1 : 0] : v[0];
+      const float y = GATED ? gate_up(v[0], v[GATED ? 1 : 0]) : v[0];
       if (p.c_f32)
         static_cast<float*>(p.C)[m * p.ldc + n] = y;
       else

@@ -140,9 +140,6 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  return __fdividef(g, 1.f + __expf(-g)) * u;
-}
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -170,7 +167,7 @@ struct Out {
     const bool odd = lane >= 16;
     const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 16);
     const float g = odd ? other : a, u = odd ? b : other;
-    return silu_mul(g, u);
+    return gate_up(g, u);
   }
   // FP32 results (BT <= 128: for 256 tokens a tile the registers do not reach): 128 contiguous
   // bytes a token as they are.
@@ -594,7 +591,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float y = fmaf(sum[u][j], sa[u] * sw[j], bias[j]);
-              if constexpr (GATED) y = silu_mul(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
+              if constexpr (GATED) y = gate_up(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
               if (up || n + j >= p.cols) continue;
               if (p.c_f32)
                 static_cast<float*>(p.C)[at + j] = y;

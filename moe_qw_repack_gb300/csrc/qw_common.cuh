@@ -361,6 +361,13 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
   return *reinterpret_cast<uint32_t*>(&b);
 }
 
+// silu(g) u = g / (1 + e^-g) u, from e^-|g|: it does not overflow, and the divisor stays between 1 and 2,
+// where the fast division is good to 2 units (above 2^126 it returns 0).
+__device__ __forceinline__ float gate_up(float g, float u) {
+  const float e = expf(-fabsf(g));
+  return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
+}
+
 // Four INT8 codes -> two FP16 pairs, exactly: byte b of code + 128 dropped into the mantissa of
 // 1024 is the FP16 number 1024 + b.
 __device__ __forceinline__ void int8x4_to_f16x2(uint32_t x, uint32_t& lo, uint32_t& hi) {
