@@ -120,6 +120,9 @@ __global__ void __launch_bounds__(NUM_THREADS, CTAS_PER_SM)
       if (n < cols)
         prefetch_l2(p.W + ((int64_t)(r / OUTS ? cols : 0) + n) * p.K + k_beg + (i - r * lines) * KB);
     }
+    // The copies begin when the previous kernel has ended, and waits for them are limited: they must
+    // not count that kernel's time.
+    pdl_wait();
     const uint32_t row = mma_row(lane), chunk = (uint32_t)(warp & 1) * 4 + (lane & 3);
     const uint32_t off = row * KB + ((chunk ^ row) << 4);
     for (int c = 0; c < chunks; ++c) {
@@ -160,7 +163,6 @@ __global__ void __launch_bounds__(NUM_THREADS, CTAS_PER_SM)
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
-    pdl_wait();  // (scales and results below)
   }
   pdl_launch_dependents();
   __syncthreads();  // the ring has been read
