@@ -424,7 +424,8 @@ qw_status qw_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, 
  *        call exactly as qw_quantize_int8 does; a_scale must be NULL.
  *   bias: BF16 [N] or NULL.  c_type QW_T_BF16 or QW_T_F32 (logits); C: row pitch ldc >= N
  *   elements.  Sums of products are exact below 2^24 and rounded to FP32 above.
- * K % 16 == 0 and K <= 131056 (else QW_ERR_UNSUPPORTED); M >= 0 (0 is a no-op), M < 2^31.
+ * K % 16 == 0, K <= 131056 and N <= 2^31 - 256 (else QW_ERR_UNSUPPORTED); M >= 0 (0 is a
+ * no-op), M < 2^31.
  * Alignment: A and W 16 bytes, the pitch of A a multiple of 16 bytes, scales 4, bias 2, C its
  * element size, workspace 256.  Workspace: qgemm_int8_workspace_size bytes for up to max_rows
  * rows (any content; the quantised activations live there during the call; calls that share
@@ -442,7 +443,7 @@ qw_status qgemm_int8(int32_t afmt, const void* A, int64_t lda, const float* a_sc
  *     g = product with rows 0 .. I-1 of W, u = product with rows I .. 2I-1 (bias included),
  *     Y[m][i] = bf16( g / (1 + e^-g) * u ), FP32 until that rounding.
  *   W: INT8 [2I][K], w_scale FP32 [2I], bias BF16 [2I] or NULL; Y: BF16, row pitch ldy >= I;
- *   the rest as qgemm_int8 (workspace: qgemm_int8_workspace_size with N = 2I).  I < 2^30.
+ *   the rest as qgemm_int8 (workspace: qgemm_int8_workspace_size with N = 2I).  I <= 2^30 - 128.
  */
 qw_status qgemm_int8_gated(int32_t afmt, const void* A, int64_t lda, const float* a_scale,
                            const void* W, const float* w_scale, const void* bias, void* Y,

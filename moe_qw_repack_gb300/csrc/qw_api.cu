@@ -452,7 +452,7 @@ qw_status qgemm_int8_workspace_size(int32_t afmt, int64_t max_rows, int32_t N, i
   if (!bytes || max_rows < 0 || max_rows > 0x7FFFFFFFLL || N < 1 || K < 1)
     return QW_ERR_INVALID_ARG;
   if (afmt != QW_A_BF16 && afmt != QW_A_INT8_TOKEN) return QW_ERR_UNSUPPORTED;
-  if (K % 16 || K > kInt8MaxK) return QW_ERR_UNSUPPORTED;
+  if (K % 16 || K > kInt8MaxK || N > kInt8MaxN) return QW_ERR_UNSUPPORTED;
   if (afmt == QW_A_BF16)
     *bytes = int8_code_bytes(max_rows, K) + (uint64_t)max_rows * 4;
   else

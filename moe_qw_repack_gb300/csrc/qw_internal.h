@@ -121,6 +121,8 @@ struct Int8Problem {
 };
 // largest K whose 32-bit integer sums cannot overflow (128 * 128 * K < 2^31), K % 16 == 0
 constexpr int32_t kInt8MaxK = 131056;
+// largest N: columns are counted in 32 bits, rounded up to whole tiles (of at most 128)
+constexpr int32_t kInt8MaxN = 0x7FFFFFFF - 255;
 // One or two tokens: dp4a.  Up to kInt8MmaRows: mma.sync.  More: tcgen05.  At N = 14336, K = 4096
 // (us): 2 tokens 13.4 with dp4a, 14.1 with mma.sync; 4 tokens 17.4 and 14.1; 16 tokens 15.2 with
 // mma.sync, 20.2 with tcgen05; 32 tokens 38 and 19.6.
