@@ -545,7 +545,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (csize > 1) {
       // Every CTA's sums are in its shared memory; this one finishes tokens rank, rank + csize, .. of
       // the tile, adding the slices in rank order.  A lane has four weight rows of a token.
-      __syncwarp();  // single-lane roles have left their warps apart
       const int64_t m0 = (int64_t)first.mt * BT;
       const bool up = GATED && (lane & 4);
       const int32_t n = (int32_t)(first.nt * TILE_COLS) +
@@ -601,7 +600,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      __syncwarp();
       cluster_sync();  // nobody leaves while its sums are read
     }
   }

@@ -126,8 +126,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 // Executed by every thread of every CTA of the cluster (CTAs of a cluster are co-scheduled);
-// orders shared-memory writes before it with reads after it across the cluster.
+// orders shared-memory writes before it with reads after it across the cluster.  A warp's lanes may
+// come from a loop that they left one by one; .aligned wants them together.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
