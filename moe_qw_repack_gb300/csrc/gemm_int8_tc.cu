@@ -57,7 +57,9 @@ constexpr int A_SLOT_COLS = KA / 2;  // 32-bit columns of one operand slot
 constexpr int A_COL0 = 256;          // the accumulator uses columns [0, BT)
 
 // Registers: launched with 96 a thread, then shared out by warpgroup (the sum below is not above what
-// the launch holds; launch() checks that the kernel was compiled to LAUNCH_REGS).  No role calls a
+// the launch holds; launch() checks that the kernel was compiled to LAUNCH_REGS), and given back when a
+// role ends: what comes after all roles is compiled once for every warp, to the launch's share.  The
+// others' increase waits until the epilogue, which ends whatever happens, has decreased.  No role calls a
 // subroutine, whose registers would not follow the share: a 64-bit division is one, so tiles are
 // counted in 32 bits and stepped by additions.
 constexpr int LAUNCH_REGS = 96, MISC_REGS = 56, CVT_REGS = 72, EPI_REGS = 136;
@@ -71,6 +73,13 @@ __device__ __forceinline__ void regs_dec() {
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// the end of a role: its warps together (between two setmaxnreg a warpgroup has to be)
+template <int ROLE, int WARPS>
+__device__ __forceinline__ void role_end() {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"n"(ROLE), "n"(WARPS * 32) : "memory");
 }
 
 template <int BT>
@@ -405,6 +414,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         wait_landed(final_bar, 0);
       }
     }
+    role_end<1, CVT_WARP0>();
+    regs_inc<LAUNCH_REGS>();
   } else if (warp < EPI_WARP0) {
     // ------------------------------------------------------------ converters
     regs_dec<CVT_REGS>();
@@ -464,6 +475,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
     }
+    role_end<2, NUM_CVT_WARPS>();
+    regs_inc<LAUNCH_REGS>();
   } else {
     // ------------------------------------------------------------ epilogue
     regs_inc<EPI_REGS>();
@@ -539,6 +552,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         out.template store<STEP>(packed, m, left);
       }
     }
+    role_end<3, NUM_EPI_WARPS>();
+    regs_dec<LAUNCH_REGS>();
   }
 
   if constexpr (BT < 256) {
