@@ -244,10 +244,13 @@ qw_status launch(const Int8Problem& p, int32_t* err, cudaStream_t st) {
   if (!encode_int8_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.A, p.K, p.M, p.lda, KB, GE::TOKENS) ||
       !encode_int8_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.W, p.K, p.N, p.K, KB, OUTS))
     return QW_ERR_CUDA;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(gemm_int8_mma_kernel<NT, GATED>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, GE::SMEM);
-  if (attr != cudaSuccess) return QW_ERR_CUDA;
+  static std::atomic<int> ready[64];
+  if (once_per_device(ready, [] {
+        return cudaFuncSetAttribute(gemm_int8_mma_kernel<NT, GATED>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    GE::SMEM) == cudaSuccess;
+      }) <= 0)
+    return QW_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(blocks * csize));
   cfg.blockDim = dim3(NUM_THREADS);

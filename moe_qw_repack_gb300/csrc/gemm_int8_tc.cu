@@ -35,7 +35,6 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <array>
 #include <type_traits>
 
 #include "int8_map.cuh"
@@ -631,28 +630,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // Clusters of csize CTAs that run at once (fewer than SMs / csize: a cluster lies within one GPC)
 template <int BT>
 int max_clusters(int csize) {
-  static const std::array<int, 4> n = [] {
-    std::array<int, 4> n{};
-    for (int i = 0; i < 4; ++i) {
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(1u << i);
-      cfg.blockDim = dim3(NUM_THREADS);
-      cfg.dynamicSmemBytes = Geo<BT>::SMEM;
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = 1u << i;
-      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      if (cudaFuncSetAttribute(gemm_int8_tc_kernel<BT, false>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)Geo<BT>::SMEM) != cudaSuccess ||
-          cudaOccupancyMaxActiveClusters(&n[i], gemm_int8_tc_kernel<BT, false>, &cfg) != cudaSuccess)
-        n[i] = i ? 0 : device_sm_count();
-    }
-    return n;
-  }();
-  return n[csize == 8 ? 3 : csize >> 1];
+  static std::atomic<int> cache[4][64];
+  const int found = once_per_device(cache[csize == 8 ? 3 : csize >> 1], [=] {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)csize);
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = Geo<BT>::SMEM;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)csize;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(gemm_int8_tc_kernel<BT, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Geo<BT>::SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gemm_int8_tc_kernel<BT, false>, &cfg) != cudaSuccess)
+      return 0;
+    return n + 1;  // (none is an answer too)
+  });
+  // without an answer (or an SM free of others) tiles are counted in rounds over all SMs, none split
+  return found > 1 ? found - 1 : csize > 1 ? 0 : device_sm_count();
 }
 
 struct Plan {
@@ -715,15 +714,16 @@ qw_status launch(const Int8Problem& pr, const void* codes16, int csize, int32_t*
   p.c_f32 = pr.c_f32;
   p.b_bytes = box_rows * KA * 2;
   p.err = err;
-  static const bool ready = [] {
-    cudaFuncAttributes fa{};
-    return cudaFuncSetAttribute(gemm_int8_tc_kernel<BT, GATED>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)GE::SMEM) == cudaSuccess &&
-           cudaFuncGetAttributes(&fa, gemm_int8_tc_kernel<BT, GATED>) == cudaSuccess &&
-           fa.numRegs == LAUNCH_REGS;  // the register split depends on it
-  }();
-  if (!ready) return QW_ERR_CUDA;
+  static std::atomic<int> ready[64];
+  if (once_per_device(ready, [] {
+        cudaFuncAttributes fa{};
+        return cudaFuncSetAttribute(gemm_int8_tc_kernel<BT, GATED>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)GE::SMEM) == cudaSuccess &&
+               cudaFuncGetAttributes(&fa, gemm_int8_tc_kernel<BT, GATED>) == cudaSuccess &&
+               fa.numRegs == LAUNCH_REGS;  // the register split depends on it
+      }) <= 0)
+    return QW_ERR_CUDA;
   const int64_t tiles = (int64_t)p.num_n_tiles * p.num_m_tiles;
   const int sms = device_sm_count();
   if (tiles > 0x7FFFFFFF - sms) return QW_ERR_UNSUPPORTED;  // counted in 32 bits

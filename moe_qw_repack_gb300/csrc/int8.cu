@@ -332,10 +332,13 @@ qw_status launch_gemv(const Int8Problem& p, bool early, int32_t* err, cudaStream
   const int buffers = g.slices > g.csize ? 2 : 1;
   const int pitch = (g.len + 511) / 512 * 512;
   constexpr int kMaxSmem = 2 * R * SLICE;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(gemv_int8_kernel<MT, RW, GATED>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  if (attr != cudaSuccess) return QW_ERR_CUDA;
+  static std::atomic<int> ready[64];
+  if (once_per_device(ready, [] {
+        return cudaFuncSetAttribute(gemv_int8_kernel<MT, RW, GATED>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kMaxSmem) == cudaSuccess;
+      }) <= 0)
+    return QW_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(blocks * g.csize));
   cfg.blockDim = dim3(GTHREADS);

@@ -719,10 +719,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 
 template <int TYPE, int THREADS>
 qw_status launch_type(const LogprobsArgs& a, int64_t T, int csize, cudaStream_t st) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(logprobs_kernel<TYPE, THREADS>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring_bytes<THREADS>());
-  if (attr != cudaSuccess) return QW_ERR_CUDA;
+  static std::atomic<int> ready[64];
+  if (once_per_device(ready, [] {
+        return cudaFuncSetAttribute(logprobs_kernel<TYPE, THREADS>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)ring_bytes<THREADS>()) == cudaSuccess;
+      }) <= 0)
+    return QW_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.dynamicSmemBytes = ring_bytes<THREADS>();
   cfg.gridDim = dim3((unsigned)(T * csize));

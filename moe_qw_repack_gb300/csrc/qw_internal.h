@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/qw.h"
@@ -10,6 +11,18 @@ namespace qw {
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
+// What `find` says (a positive number; anything else is a failure, which is not kept) of the current
+// device, found once for each.
+template <class F>
+int once_per_device(std::atomic<int> (&cache)[64], F&& find) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  int v = dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+  if (v > 0) return v;
+  v = find();
+  if (v > 0 && dev < 64) cache[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
 
 // Packed-layout geometry shared by repack and the GEMM kernels.
 constexpr int kIntGroup = 128;       // K elements per BF16 scale (INT formats)
