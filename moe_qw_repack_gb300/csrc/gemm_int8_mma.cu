@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(NUM_THREADS, CTAS_PER_SM)
         else
           sum = *o;
         const int64_t wr = (int64_t)(h ? cols : 0) + n;
-        v[h] = sum * (sa * __ldg(p.w_scale + wr));
-        if (p.bias) v[h] += __uint_as_float((uint32_t)__ldg(p.bias + wr) << 16);
+        v[h] = sum * (sa * p.w_scale[wr]);
+        if (p.bias) v[h] += __uint_as_float((uint32_t)p.bias[wr] << 16);
       }
       const float y = GATED ? gate_up(v[0], v[GATED ? 1 : 0]) : v[0];
       if (p.c_f32)

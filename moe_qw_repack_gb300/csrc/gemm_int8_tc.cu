@@ -496,12 +496,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       out.n = (int32_t)(x.nt * TILE_COLS) + (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
       out.nvalid = out.n < p.cols;
       const int64_t wrow = (GATED && lane >= 16) ? (int64_t)p.cols + out.n : out.n;
-      out.sw = out.nvalid ? __ldg(p.w_scale + wrow) : 0.f;
-      out.bias = p.bias && out.nvalid ? __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16) : 0.f;
+      out.sw = out.nvalid ? p.w_scale[wrow] : 0.f;
+      out.bias = p.bias && out.nvalid ? __uint_as_float((uint32_t)p.bias[wrow] << 16) : 0.f;
       __syncwarp();  // the previous tile's scales have been read
       const int64_t mw = m0 + part * (BT / 2);  // first token of this warp
 #pragma unroll
-      for (int i = lane; i < BT / 2; i += 32) sc[i] = mw + i < p.M ? __ldg(p.a_scale + mw + i) : 0.f;
+      for (int i = lane; i < BT / 2; i += 32) sc[i] = mw + i < p.M ? p.a_scale[mw + i] : 0.f;
       __syncwarp();
       if (!warp_wait(acc_full, acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
@@ -569,8 +569,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int j = 0; j < 4; ++j)
           if (n + j < p.cols) {
             const int64_t wrow = (int64_t)(up ? p.cols : 0) + n + j;
-            sw[j] = __ldg(p.w_scale + wrow);
-            if (p.bias) bias[j] = __uint_as_float((uint32_t)__ldg(p.bias + wrow) << 16);
+            sw[j] = p.w_scale[wrow];
+            if (p.bias) bias[j] = __uint_as_float((uint32_t)p.bias[wrow] << 16);
           }
       }
       cluster_sync();
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           float sum[U][4] = {}, sa[U];
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            sa[u] = i0 + step * u < tokens ? __ldg(p.a_scale + m0 + i0 + step * u) : 0.f;
+            sa[u] = i0 + step * u < tokens ? p.a_scale[m0 + i0 + step * u] : 0.f;
           for (int c = 0; c < csize; ++c) {
             const uint32_t from = mapa_shared(smem_u32(sB) + lane * 16, (uint32_t)c);
 #pragma unroll

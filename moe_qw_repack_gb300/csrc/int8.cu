@@ -83,7 +83,7 @@ struct RowScale {
 constexpr int QTHREADS = 256;
 template <bool F16, int VEC>
 __global__ void __launch_bounds__(QTHREADS)
-    quantize_int8_kernel(const uint16_t* __restrict__ A, int64_t lda, int32_t K,
+    quantize_int8_kernel(const uint16_t* A, int64_t lda, int32_t K,
                          void* __restrict__ Q, float* __restrict__ S, int32_t* err) {
   // FP16 codes are only written in front of the tensor-core kernel, which reads nothing before its own
   // wait and lets the next kernel start only after it: it may be set up while this one still waits
@@ -100,12 +100,12 @@ __global__ void __launch_bounds__(QTHREADS)
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
     const int i = threadIdx.x + j * QTHREADS;
-    keep[j] = i < n8 ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    keep[j] = i < n8 ? src[i] : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int j = 0; j < VEC; ++j) amax = max(amax, bf16x8_absmax(keep[j]));
   for (int i = threadIdx.x + VEC * QTHREADS; i < n8; i += QTHREADS)
-    amax = max(amax, bf16x8_absmax(__ldg(src + i)));
+    amax = max(amax, bf16x8_absmax(src[i]));
   __shared__ uint32_t part[QTHREADS / 32];
   amax = __reduce_max_sync(0xFFFFFFFFu, amax);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(QTHREADS)
     const int i = threadIdx.x + j * QTHREADS;
     if (i < n8) put(i, keep[j]);
   }
-  for (int i = threadIdx.x + VEC * QTHREADS; i < n8; i += QTHREADS) put(i, __ldg(src + i));
+  for (int i = threadIdx.x + VEC * QTHREADS; i < n8; i += QTHREADS) put(i, src[i]);
 }
 
 // INT8 codes [M][lda] -> the same integers as FP16 [M][K]; a thread takes eight times eight codes at a
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(QTHREADS)
 // and a 64-bit division for them took 12.6 us for 4096 x 4096, 8.5 now).
 template <typename I>
 __global__ void __launch_bounds__(256)
-    widen_int8_kernel(const int8_t* __restrict__ A, int64_t lda, I total, I per_row,
+    widen_int8_kernel(const int8_t* A, int64_t lda, I total, I per_row,
                       uint4* __restrict__ Q) {
   pdl_launch_dependents();  // (as the quantiser above)
   pdl_wait();
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const I at = i + u * step, r = at / per_row;
-      v[u] = at < total ? __ldg(reinterpret_cast<const uint2*>(A + (int64_t)r * lda) + (at - r * per_row))
+      v[u] = at < total ? reinterpret_cast<const uint2*>(A + (int64_t)r * lda)[at - r * per_row]
                         : make_uint2(0, 0);
     }
 #pragma unroll
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(GTHREADS)
       for (int m = 0; m < MT; ++m) {
         const int k = j * 512 + lane * 16;
         x[j][m] = k < len && m < p.M
-                      ? __ldg(reinterpret_cast<const uint4*>(p.A + m * p.lda + k0 + k))
+                      ? *reinterpret_cast<const uint4*>(p.A + m * p.lda + k0 + k)
                       : make_uint4(0, 0, 0, 0);
       }
     if (!warp_wait(&full[buffer], phase, &abort_flag, err)) wait_landed(&full[buffer], phase);
@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(GTHREADS)
           sum += __float_as_int(
               ld_shared_cluster_f32(mapa_shared(smem_u32(&part[row * MT + m]), (uint32_t)c)));
         const int64_t wr = (int64_t)(h ? cols : 0) + n;
-        v[h] = (float)sum * (p.a_scale[m] * __ldg(p.w_scale + wr));
-        if (p.bias) v[h] += __uint_as_float((uint32_t)__ldg(p.bias + wr) << 16);
+        v[h] = (float)sum * (p.a_scale[m] * p.w_scale[wr]);
+        if (p.bias) v[h] += __uint_as_float((uint32_t)p.bias[wr] << 16);
       }
       const float y = GATED ? gate_up(v[0], v[GATED ? 1 : 0]) : v[0];
       if (p.c_f32)

@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   if (tid == 0)
     for (int b = 0; b < min(STAGES, nblk); ++b) fetch(b);
 
-  const int32_t tok = a.tokens ? __ldg(a.tokens + row) : -1;
+  const int32_t tok = a.tokens ? a.tokens[row] : -1;
   const bool tok_ok = tok >= 0 && tok < a.V;
   // a value above every logit counts nothing
   const bool want_rank = tok_ok && a.token_rank;

@@ -158,7 +158,9 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 // ... and waits here until the previous kernel has finished and its writes are visible (a
-// no-op when the kernel was launched without the attribute).
+// no-op when the kernel was launched without the attribute).  What that kernel writes is read with
+// plain loads: the read-only path (__ldg, const __restrict__) is for memory that nothing writes while
+// this kernel runs, and the compiler may move such loads above the wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Launch as a programmatic dependent of the previous kernel on the stream: its launch and
