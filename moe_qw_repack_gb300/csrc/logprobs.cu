@@ -305,12 +305,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   __shared__ Part wpart[WARPS];
   __shared__ Part part;  // this CTA's result; on rank 0, at the end, the row's
   __shared__ uint64_t full[STAGES];
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, failed;  // failed: the block whose wait gave up
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     cnt = merged = hits = vhits = 0;
     abort_flag = 0;
+    failed = 0x7FFFFFFF;
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
     fence_barrier_init();
   }
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         if (v0 + j * THREADS >= vend) blk[j * THREADS] = E::masked();
     }
     // (a thread reads only vectors that it filled itself or that the copy brings)
-    (void)warp_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err);
+    if (!warp_wait(&full[b % STAGES], (uint32_t)(b / STAGES) & 1u, &abort_flag, a.err)) failed = b;
     typename E::Count count{};
     // all at once, so that one look at their maximum decides for all (two at a time: 4096 x 131072
     // BF16 200 us for 191)
@@ -443,7 +444,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       in_run = 0;
     }
     __syncthreads();  // every thread is done with the block
-    if (abort_flag) {
+    // (not abort_flag: a warp ahead may raise it for the next block before all have looked here, and
+    // the barriers that follow want all threads)
+    if (failed <= b) {
       // a wait gave up: let the copies in flight land before shared memory goes away
       for (int i = b; tid == 0 && i < min(nblk, b + STAGES); ++i)
         wait_landed(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u);
