@@ -423,7 +423,11 @@ qw_status qw_quantize_int8(const void* A, int64_t lda, int64_t rows, int32_t K, 
  *   afmt QW_A_BF16: A is BF16 (row pitch lda >= K elements), quantised per token inside the
  *        call exactly as qw_quantize_int8 does; a_scale must be NULL.
  *   bias: BF16 [N] or NULL.  c_type QW_T_BF16 or QW_T_F32 (logits); C: row pitch ldc >= N
- *   elements.  Sums of products are exact below 2^24 and rounded to FP32 above.
+ *   elements.  The scales' product is formed first, in FP32.  Sums of products: one or two tokens
+ *   are summed in 32-bit integers and rounded to FP32 once; more on the tensor cores in FP32, exact
+ *   while the sum of |A_q W| stays below 2^24, and above it each 16 k may lose 2^-23 of the partial
+ *   sum.  So the last bits of a token's FP32 results may depend on how many tokens share its call;
+ *   the same call gives the same bits.
  * K % 16 == 0, K <= 131056 and N <= 2^31 - 256 (else QW_ERR_UNSUPPORTED); M >= 0 (0 is a
  * no-op), M < 2^31.
  * Alignment: A and W 16 bytes, the pitch of A a multiple of 16 bytes, scales 4, bias 2, C its

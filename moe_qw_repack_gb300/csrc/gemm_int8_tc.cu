@@ -3,8 +3,8 @@
 //
 // Mathematics: C[m][n] = a_scale[m] w_scale[n] sum_k q[m][k] w[n][k] + bias[n].  Every INT8 code
 // is an FP16 number and every product of two an FP32 integer, so kind::f16 MMAs with FP32
-// accumulation give the integer sum exactly while partial sums stay below 2^24 (sm_103a's own
-// integer tensor rate is far below its 16-bit one).
+// accumulation give the integer sum exactly while partial sums stay below 2^24, and lose up to 2^-23
+// of one a step above (sm_103a's own integer tensor rate is far below its 16-bit one).
 //
 // Structure (persistent, one CTA per SM; a tile is 128 weight rows x BT tokens):
 //   warp 0      TMA producer of the tokens' tile: FP16 codes [M][K] of the workspace, 64 k
