@@ -106,6 +106,21 @@ typedef enum qw_dtype {
   QW_T_F16 = 2
 } qw_dtype;
 
+/* Which values of a head's turned part make a pair (qw_rope). */
+typedef enum qw_rope_layout {
+  QW_ROPE_HALF = 0,        /* (j, j + rot_dim / 2)                                         */
+  QW_ROPE_INTERLEAVED = 1  /* (2 j, 2 j + 1)                                               */
+} qw_rope_layout;
+
+/* How rotary frequencies are made for contexts beyond the trained one (qw_rope_frequencies). */
+typedef enum qw_rope_method {
+  QW_ROPE_NONE = 0,
+  QW_ROPE_LINEAR = 1,      /* every frequency / factor (position interpolation)            */
+  QW_ROPE_NTK = 2,         /* base * factor^(rot_dim / (rot_dim - 2))                      */
+  QW_ROPE_YARN = 3,        /* by bands, and attention 0.1 ln(factor) + 1                   */
+  QW_ROPE_BANDS = 4        /* slow frequencies / factor, fast ones kept, between them mixed */
+} qw_rope_method;
+
 /* Description of one repacked weight set (E experts; E = 1 for a dense layer).
  * Filled by qw_repack_query; treat as read-only. */
 typedef struct qw_packed_desc {
@@ -474,6 +489,79 @@ qw_status qw_logprobs(int32_t l_type, const void* logits, int64_t ld, int64_t T,
                       const int32_t* tokens, int32_t topk, float* token_logprobs,
                       int32_t* token_ranks, float* entropy, int32_t* top_ids,
                       float* top_logprobs, int32_t* d_err, void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * Around a projection: the norm in front of it, the low-rank adapters beside it, the rotary
+ * positions behind it.  Inputs and outputs may be the same buffer with the same pitch where the
+ * comment says so, and must not overlap otherwise.
+ *
+ * qw_rmsnorm - residual addition, root-mean-square norm and the next product's operand:
+ *     h = X + R, rounded to R's type and written to R_out        (R NULL: h = X)
+ *     y[r][k] = h[r][k] * (w_offset + W[k]) / sqrt(mean_k h[r][k]^2 + eps)
+ *   X: x_type QW_T_BF16 or QW_T_F32 [rows][K], row pitch ldx >= K elements.  R, R_out: r_type
+ *   QW_T_BF16 or QW_T_F32 (R_out may be NULL, be R, or be X where the types agree).  W: BF16 [K].
+ *   Y: the rows y in BF16, pitch ldy, or NULL (may be X where X is BF16).
+ *   q_fmt: what else is made of y, from its FP32 values:
+ *     QW_A_BF16        nothing (Q and Q_sf NULL);
+ *     QW_A_INT8_TOKEN  Q INT8 [rows][K], Q_sf FP32 [rows]: scale max|y| / 127, codes
+ *                      rint(y * (127 / max|y|)), ties to even (max|y| below 2^-119: codes 0);
+ *     QW_A_MXFP8_G32   Q E4M3 [rows][K], Q_sf E8M0 [rows][K/32], as qw_quantize_mxfp8.
+ *   FP32 arithmetic; |w_offset + W| below 2^64.  A row with a non-finite h sets QW_ERR_VALUE in
+ *   d_err; its y is NaN, its INT8 scale NaN with codes 0, its E8M0 scales 0xFF with codes 0.
+ *   K % 8 == 0 (INT8: 16, MXFP8: 32; else QW_ERR_UNSUPPORTED).  2^-126 <= eps <= 2^100,
+ *   |w_offset| <= 2^60.  X, R, R_out, W, Y, Q and all pitches 16-byte aligned, FP32 Q_sf 4.
+ */
+qw_status qw_rmsnorm(int32_t x_type, const void* X, int64_t ldx, int32_t r_type, const void* R,
+                     int64_t ldr, void* R_out, int64_t ldro, const void* W, float w_offset, float eps,
+                     int64_t rows, int32_t K, void* Y, int64_t ldy, int32_t q_fmt, void* Q,
+                     void* Q_sf, int32_t* d_err, void* stream);
+
+/* qgemm_lora - the low-rank adapters of many requests beside a shared projection:
+ *     C[m][n] = base[m][n] + scales[a] * sum_{r < ranks[a]} B[a][n][r] * (sum_k A[a][r][k] X[m][k])
+ *   with a = ids[m], the token's adapter (device int32 [M], any order; tokens of the same adapter
+ *   that stand together share its weights).  ids[m] = -1: C's row is base's, bit for bit.
+ *   X: BF16 [M][K], row pitch ldx.  A: BF16 [L][R][K], B: BF16 [L][N][R], contiguous: adapters of up
+ *   to R rows and columns, of which ranks[a] (device int32 [L], 0 .. R; NULL: R) are read.  scales:
+ *   FP32 [L] or NULL (1).  base: c_type, row pitch ld_base, or NULL (0); may be C with the same
+ *   pitch, which adds to a projection's output in place (rows without adapter are then not
+ *   touched).  C: c_type QW_T_BF16 or QW_T_F32, row pitch ldc >= N, rounded once.  Products and sums
+ *   in FP32.
+ *   An id outside [-1, L) or a rank outside [0, R] sets QW_ERR_INVALID_ARG in d_err; the token is
+ *   then taken as one without adapter.
+ *   K % 8 == 0, R % 8 == 0, R <= 256, M <= 2^26, N and K <= 2^31 - 256 (else QW_ERR_UNSUPPORTED).  X, A, B
+ *   and the pitch of X 16-byte aligned, base and C their element size.  L * R * K and L * N * R may
+ *   pass 2^31.  No workspace.
+ */
+qw_status qgemm_lora(const void* X, int64_t ldx, const void* A, const void* B, const float* scales,
+                     const int32_t* ranks, int32_t L, int32_t R, const int32_t* ids,
+                     const void* base, int64_t ld_base, int32_t c_type, void* C, int64_t ldc,
+                     int64_t M, int32_t N, int32_t K, int32_t* d_err, void* stream);
+
+/* qw_rope - rotary positions: in each of a token's heads the first rot_dim values are turned in
+ *   pairs (layout) by the angle positions[t] * freqs[j], j the pair, times `scale`:
+ *     (a, b) -> scale * (a cos - b sin, b cos + a sin)
+ *   and the rest of the head is copied.  X, Y: type QW_T_BF16, QW_T_F16 or QW_T_F32, heads of
+ *   head_dim values side by side from the row's start (the query and key heads of a fused
+ *   projection are one call), row pitches ldx, ldy >= heads * head_dim; Y may be X with the same
+ *   pitch.  positions: device int32 [T], any value (a negative one turns back).  freqs: device FP64
+ *   [rot_dim / 2], radians per position, |freq| <= 2^32 (else QW_ERR_VALUE in d_err and NaN).
+ *   Angles are held to 2^-32 of a turn at any position, the rest is FP32, rounded once.
+ *   rot_dim even, 2 <= rot_dim <= head_dim <= 1024, heads * head_dim <= 2^24.  X and Y aligned to their element
+ *   size (16 bytes with pitch, head_dim and rot_dim / 2 of whole 16-byte vectors run faster).
+ *
+ * qw_rope_frequencies - the freqs of qw_rope, on the host (freqs: host double [rot_dim / 2]; attention:
+ *   host float, the `scale` of qw_rope): base^(-2 j / rot_dim), for longer contexts changed by `method`
+ *   with factor >= 1.  The two by bands take f * (k + (1 - k) / factor) with
+ *   k = clamp((original f / 2 pi - low) / (high - low), 0, 1): frequencies of over `high` turns in
+ *   the `original` length are kept, those of under `low` are stretched.
+ */
+qw_status qw_rope(int32_t type, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t T,
+                  int32_t heads, int32_t head_dim, int32_t rot_dim, int32_t layout,
+                  const int32_t* positions, const double* freqs, float scale, int32_t* d_err,
+                  void* stream);
+qw_status qw_rope_frequencies(int32_t method, double base, int32_t rot_dim, double factor,
+                              double original, double low, double high, double* freqs,
+                              float* attention);
 
 /* --------------------------------------------------------------------------------------
  * qw_read_error - synchronise `stream`, copy *d_err to the host (`host_code`, host

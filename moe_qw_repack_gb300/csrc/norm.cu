@@ -1,0 +1,340 @@
+// norm.cu - residual addition, root-mean-square norm and the operand of the product behind it, in one
+// pass over the row.
+//
+//   h = x + r (as stored: rounded to r's type; without r: x)
+//   y[k] = h[k] w[k] / sqrt(mean h^2 + eps)
+// y leaves as BF16, as MXFP8 (qw_quantize_mxfp8's conversion) or as INT8 codes with a scale per row
+// (qw_quantize_int8's), both from the FP32 y: rounded to BF16 on the way, a code would be off by up to
+// 1/4 of a step more.
+//
+// Arithmetic: sums of squares in FP32.  h w is formed first: of BF16 values it is exact, and an FP32
+// h costs one rounding; 1 / rms is held as a sum of two FP32 numbers, so y has one more rounding.
+// Squares that pass FP32 (|h| above 2^63 or so) take a second reduction on h scaled by a power of two.
+#include <cuda_bf16.h>
+
+#include <cfloat>
+
+#include "qw_common.cuh"
+#include "qw_internal.h"
+
+namespace qw {
+namespace {
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(w[j]);
+    f[2 * j + 1] = bf16_hi(w[j]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+
+// Eight values of a row from element 8 i.  Plain loads: the previous kernel may have written them, and
+// this one may write h or y to the same place.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* row, int i, float (&f)[8]) {
+  if constexpr (F32) {
+    const float4* p = static_cast<const float4*>(row) + 2 * i;
+    const float4 a = p[0], b = p[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    unpack8(static_cast<const uint4*>(row)[i], f);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ const void* row_of(const void* p, int64_t r, int64_t ld) {
+  return static_cast<const uint8_t*>(p) + r * ld * (F32 ? 4 : 2);
+}
+
+// What a row is held as: nothing beside x, or a residual in BF16 or FP32.
+enum { R_NONE = 0, R_BF16 = 1, R_F32 = 2 };
+enum { Q_NONE = 0, Q_INT8 = 1, Q_MXFP8 = 2 };
+
+constexpr int NORM_WARPS = 4;  // rows of a CTA where a warp takes a row
+
+template <bool ONE_WARP>
+struct Reduce {
+  float* part;  // [32]
+  // Sums or maxima over the row's threads; every thread gets the result.
+  template <class F>
+  __device__ __forceinline__ float operator()(float v, F&& join) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    if constexpr (!ONE_WARP) {
+      const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+      __syncthreads();  // (the last result has been read)
+      if (lane == 0) part[threadIdx.x >> 5] = v;
+      __syncthreads();
+      v = part[lane < warps ? lane : 0];
+      if (lane >= warps) v = 0.f;  // (sums, and maxima of magnitudes)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    }
+    return v;
+  }
+  __device__ __forceinline__ float sum(float v) const {
+    return (*this)(v, [](float a, float b) { return a + b; });
+  }
+  // of magnitudes, NaN above all: they order like their bits
+  __device__ __forceinline__ float top(float v) const {
+    return (*this)(v, [](float a, float b) {
+      return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+    });
+  }
+};
+
+// two FP32 values -> two E4M3 codes, x0 in the low byte (round to nearest even, saturate)
+__device__ __forceinline__ uint32_t e4m3x2(float x0, float x1) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(x1), "f"(x0));
+  return d;
+}
+
+template <bool X32, int RK, int QF, int VEC, bool ONE_WARP>
+__global__ void __launch_bounds__(ONE_WARP ? NORM_WARPS * 32 : 1024)
+    rmsnorm_kernel(const NormArgs a) {
+  __shared__ float part[32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lanes = ONE_WARP ? 32 : blockDim.x;
+  const int me = ONE_WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = ONE_WARP ? (int64_t)blockIdx.x * NORM_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+  if (ONE_WARP && row >= a.rows) return;
+  const Reduce<ONE_WARP> reduce{part};
+  const int n8 = a.K / 8;
+  const void* xr = row_of<X32>(a.X, row, a.ldx);
+  const void* rr = row_of<RK == R_F32>(a.R, row, a.ldr);
+  void* ro = RK == R_NONE ? nullptr : const_cast<void*>(row_of<RK == R_F32>(a.R_out, row, a.ldro));
+  const bool keep_h = RK != R_NONE && a.R_out != nullptr;
+  // h, from x and r, rounded as r is
+  auto sum8 = [&](int i, float (&h)[8]) {
+    load8<X32>(xr, i, h);
+    if constexpr (RK != R_NONE) {
+      float r[8];
+      load8<RK == R_F32>(rr, i, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] += r[j];
+      if constexpr (RK == R_BF16) {
+        const uint4 v = pack8(h);
+        unpack8(v, h);
+        if (keep_h) static_cast<uint4*>(ro)[i] = v;
+      } else if (keep_h) {
+        float4* o = static_cast<float4*>(ro) + 2 * i;
+        o[0] = make_float4(h[0], h[1], h[2], h[3]);
+        o[1] = make_float4(h[4], h[5], h[6], h[7]);
+      }
+    }
+  };
+  // ... again, for what the registers do not hold: h as it was stored (r may be gone by now)
+  auto again8 = [&](int i, float (&h)[8]) {
+    if (keep_h)
+      load8<RK == R_F32>(ro, i, h);
+    else
+      sum8(i, h);
+  };
+  float h[VEC][8], ss = 0.f;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const int i = me + v * lanes;
+    if (i < n8) {
+      sum8(i, h[v]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < VEC; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(h[v][j], h[v][j], ss);
+  for (int i = me + VEC * lanes; i < n8; i += lanes) {
+    float t[8];
+    sum8(i, t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(t[j], t[j], ss);
+  }
+  ss = reduce.sum(ss);
+  float pre = 1.f;  // h is taken times this power of two
+  if (!(ss < 0x1p126f)) {  // (the same in all of the row's threads)
+    float top = 0.f;
+    auto more = [&](const float (&t)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(fabsf(t[j]))));
+    };
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) more(h[v]);
+    for (int i = me + VEC * lanes; i < n8; i += lanes) {
+      float t[8];
+      again8(i, t);
+      more(t);
+    }
+    top = reduce.top(top);
+    pre = top < INFINITY ? 0x1p-96f : __uint_as_float(0x7FC00000u);
+    ss = 0.f;
+    auto squares = [&](const float (&t)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(t[j] * pre, t[j] * pre, ss);
+    };
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) squares(h[v]);
+    for (int i = me + VEC * lanes; i < n8; i += lanes) {
+      float t[8];
+      again8(i, t);
+      squares(t);
+    }
+    ss = reduce.sum(ss);
+  }
+  // 1 / sqrt(m) and what its rounding left: one Newton step from the exact residual 1 - m r^2
+  const float m = ss / (float)a.K + a.eps * pre * pre;
+  const float r_hi = rsqrtf(m), mr = m * r_hi;
+  const float r_lo = 0.5f * r_hi * fmaf(-fmaf(m, r_hi, -mr), r_hi, fmaf(-mr, r_hi, 1.f));
+  const uint4* w = static_cast<const uint4*>(a.W);
+  auto out8 = [&](int i, const float (&h8)[8], float (&y)[8]) {
+    float w8[8];
+    unpack8(w[i], w8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float p = h8[j] * pre * (w8[j] + a.offset);
+      y[j] = fmaf(p, r_hi, p * r_lo);
+    }
+  };
+  uint16_t* yr = a.Y ? static_cast<uint16_t*>(a.Y) + row * a.ldy : nullptr;
+  float inv = 0.f, scale = 0.f;
+  bool bad = pre != pre;
+  if constexpr (QF == Q_INT8) {
+    float top = 0.f;
+    auto more = [&](const float (&y)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(fabsf(y[j]))));
+    };
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const int i = me + v * lanes;
+      if (i < n8) {
+        out8(i, h[v], h[v]);
+        more(h[v]);
+      }
+    }
+    for (int i = me + VEC * lanes; i < n8; i += lanes) {
+      float t[8];
+      again8(i, t);
+      out8(i, t, t);
+      more(t);
+    }
+    top = reduce.top(top);
+    bad = bad || !(top < INFINITY);
+    scale = bad ? __uint_as_float(0x7FC00000u) : top / 127.f;
+    inv = bad || top < FLT_MIN * 128.f ? 0.f : 127.f / top;
+  }
+  auto put8 = [&](int i, const float (&y)[8]) {
+    if (yr) reinterpret_cast<uint4*>(yr)[i] = pack8(y);
+    if constexpr (QF == Q_INT8) {
+      // adding 1.5 * 2^23 rounds to an integer, ties to even, in the sum's low bits
+      uint32_t q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        q[j] = bad ? 0u : __float_as_uint(__fadd_rn(__fmul_rn(y[j], inv), 12582912.f));
+      uint2 o;
+      o.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+      o.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+      reinterpret_cast<uint2*>(a.Q)[row * n8 + i] = o;
+    }
+  };
+  // (MXFP8: all lanes of a warp together; K % 32 == 0, so that a group's four threads are there or not)
+  auto put8_mx = [&](int i, const float (&y)[8], bool live) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const bool sick = top >= 0x7F800000u;
+    bad = bad || sick;
+    int X = -127;
+    if (top != 0) {
+      const int ef = (int)(top >> 23);
+      const int fl = ef > 0 ? ef - 127 : -149 + (31 - __clz(top));  // floor(log2 max |y|)
+      X = max(-127, min(127, fl - 8));
+    }
+    const float to = __uint_as_float((uint32_t)(127 - X) << 23);  // 2^-X, X in [-127, 119]
+    uint2 q;
+    q.x = e4m3x2(y[0] * to, y[1] * to) | (e4m3x2(y[2] * to, y[3] * to) << 16);
+    q.y = e4m3x2(y[4] * to, y[5] * to) | (e4m3x2(y[6] * to, y[7] * to) << 16);
+    if (live) {
+      if (yr) reinterpret_cast<uint4*>(yr)[i] = pack8(y);
+      reinterpret_cast<uint2*>(a.Q)[row * n8 + i] = sick ? make_uint2(0, 0) : q;
+      if ((i & 3) == 0)
+        static_cast<uint8_t*>(a.Q_sf)[row * (n8 / 4) + (i >> 2)] = sick ? 0xFF : (uint8_t)(X + 127);
+    }
+  };
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const int i = me + v * lanes;
+    if constexpr (QF == Q_MXFP8) {
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (i < n8) out8(i, h[v], y);
+      put8_mx(i, y, i < n8);
+    } else if (i < n8) {
+      if constexpr (QF == Q_NONE) out8(i, h[v], h[v]);  // (INT8: already y)
+      put8(i, h[v]);
+    }
+  }
+  for (int i0 = VEC * lanes; i0 < n8; i0 += lanes) {
+    const int i = i0 + me;
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (i < n8) {
+      again8(i, y);
+      out8(i, y, y);
+    }
+    if constexpr (QF == Q_MXFP8)
+      put8_mx(i, y, i < n8);
+    else if (i < n8)
+      put8(i, y);
+  }
+  if constexpr (QF == Q_INT8) {
+    if (me == 0) static_cast<float*>(a.Q_sf)[row] = scale;
+  }
+  if (bad) set_error(a.err, QW_ERR_VALUE);
+}
+
+template <bool X32, int RK, int QF>
+qw_status launch(const NormArgs& a, cudaStream_t st) {
+  const int n8 = a.K / 8;
+  if (n8 <= 128) {
+    const unsigned grid = (unsigned)((a.rows + NORM_WARPS - 1) / NORM_WARPS);
+    return launch_pdl(rmsnorm_kernel<X32, RK, QF, 4, true>, dim3(grid), dim3(NORM_WARPS * 32), 0, st, a);
+  }
+  int threads = ((n8 + 1) / 2 + 31) / 32 * 32;
+  if (threads > 1024) threads = 1024;
+  return launch_pdl(rmsnorm_kernel<X32, RK, QF, 2, false>, dim3((unsigned)a.rows), dim3(threads), 0,
+                    st, a);
+}
+
+template <bool X32, int RK>
+qw_status launch_q(const NormArgs& a, int q_fmt, cudaStream_t st) {
+  if (q_fmt == QW_A_INT8_TOKEN) return launch<X32, RK, Q_INT8>(a, st);
+  if (q_fmt == QW_A_MXFP8_G32) return launch<X32, RK, Q_MXFP8>(a, st);
+  return launch<X32, RK, Q_NONE>(a, st);
+}
+template <bool X32>
+qw_status launch_r(const NormArgs& a, int r_type, int q_fmt, cudaStream_t st) {
+  if (!a.R) return launch_q<X32, R_NONE>(a, q_fmt, st);
+  return r_type == QW_T_F32 ? launch_q<X32, R_F32>(a, q_fmt, st) : launch_q<X32, R_BF16>(a, q_fmt, st);
+}
+
+}  // namespace
+
+qw_status launch_rmsnorm(const NormArgs& a, int32_t x_type, int32_t r_type, int32_t q_fmt,
+                         cudaStream_t st) {
+  return x_type == QW_T_F32 ? launch_r<true>(a, r_type, q_fmt, st)
+                            : launch_r<false>(a, r_type, q_fmt, st);
+}
+
+}  // namespace qw

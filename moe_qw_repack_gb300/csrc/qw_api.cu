@@ -545,6 +545,93 @@ qw_status qw_logprobs(int32_t l_type, const void* logits, int64_t ld, int64_t T,
   return launch_logprobs(a, l_type, T, static_cast<cudaStream_t>(stream));
 }
 
+qw_status qw_rmsnorm(int32_t x_type, const void* X, int64_t ldx, int32_t r_type, const void* R,
+                     int64_t ldr, void* R_out, int64_t ldro, const void* W, float w_offset, float eps,
+                     int64_t rows, int32_t K, void* Y, int64_t ldy, int32_t q_fmt, void* Q,
+                     void* Q_sf, int32_t* d_err, void* stream) {
+  if (x_type != QW_T_BF16 && x_type != QW_T_F32) return QW_ERR_UNSUPPORTED;
+  if (R && r_type != QW_T_BF16 && r_type != QW_T_F32) return QW_ERR_UNSUPPORTED;
+  if (q_fmt != QW_A_BF16 && q_fmt != QW_A_INT8_TOKEN && q_fmt != QW_A_MXFP8_G32)
+    return QW_ERR_UNSUPPORTED;
+  if (rows < 0 || K < 1 || ldx < K || (R && ldr < K) || (R_out && ldro < K) || (Y && ldy < K))
+    return QW_ERR_INVALID_ARG;
+  // (a normal number, far from FP32's largest; NaN fails both)
+  if (!(eps >= 0x1p-126f && eps <= 0x1p100f) || !(w_offset >= -0x1p60f && w_offset <= 0x1p60f))
+    return QW_ERR_INVALID_ARG;
+  if (K % (q_fmt == QW_A_BF16 ? 8 : q_fmt == QW_A_INT8_TOKEN ? 16 : 32) || rows > 0x7FFFFFFFLL)
+    return QW_ERR_UNSUPPORTED;
+  if (rows == 0) return QW_OK;
+  const bool quantise = q_fmt != QW_A_BF16;
+  if (!X || !W || (R_out && !R) || quantise != (Q != nullptr) || quantise != (Q_sf != nullptr) ||
+      (!Y && !Q))
+    return QW_ERR_INVALID_ARG;
+  const int x_vec = x_type == QW_T_F32 ? 4 : 8, r_vec = R && r_type == QW_T_F32 ? 4 : 8;
+  if (!aligned(X, 16) || ldx % x_vec || (R && (!aligned(R, 16) || ldr % r_vec)) ||
+      (R_out && (!aligned(R_out, 16) || ldro % r_vec)) || !aligned(W, 16) ||
+      (Y && (!aligned(Y, 16) || ldy % 8)) || !aligned(Q, 16) ||
+      (q_fmt == QW_A_INT8_TOKEN && !aligned(Q_sf, 4)))
+    return QW_ERR_ALIGNMENT;
+  const NormArgs a{X, ldx, R, ldr, R_out, ldro, W, w_offset, eps, rows, K, Y, ldy, Q, Q_sf, d_err};
+  return launch_rmsnorm(a, x_type, r_type, q_fmt, static_cast<cudaStream_t>(stream));
+}
+
+qw_status qgemm_lora(const void* X, int64_t ldx, const void* A, const void* B, const float* scales,
+                     const int32_t* ranks, int32_t L, int32_t R, const int32_t* ids,
+                     const void* base, int64_t ld_base, int32_t c_type, void* C, int64_t ldc,
+                     int64_t M, int32_t N, int32_t K, int32_t* d_err, void* stream) {
+  if (c_type != QW_T_BF16 && c_type != QW_T_F32) return QW_ERR_UNSUPPORTED;
+  if (M < 0 || N < 1 || K < 1 || L < 1 || R < 1 || ldx < K || ldc < N || (base && ld_base < N))
+    return QW_ERR_INVALID_ARG;
+  if (K % 8 || R % 8 || R > kLoraMaxRank || M > kLoraMaxRows || N > kInt8MaxN || K > kInt8MaxN)
+    return QW_ERR_UNSUPPORTED;
+  if (M == 0) return QW_OK;
+  if (!X || !A || !B || !ids || !C || (base == C && ld_base != ldc)) return QW_ERR_INVALID_ARG;
+  const int size = c_type == QW_T_F32 ? 4 : 2;
+  if (!aligned(X, 16) || ldx % 8 || !aligned(A, 16) || !aligned(B, 16) || !aligned(scales, 4) ||
+      !aligned(ranks, 4) || !aligned(ids, 4) || !aligned(base, size) || !aligned(C, size))
+    return QW_ERR_ALIGNMENT;
+  const LoraArgs a{static_cast<const uint16_t*>(X), ldx, static_cast<const uint16_t*>(A),
+                   static_cast<const uint16_t*>(B), scales, ranks, L, R, ids, base, ld_base, C, ldc,
+                   M, N, K, d_err};
+  return launch_lora(a, c_type == QW_T_F32, static_cast<cudaStream_t>(stream));
+}
+
+qw_status qw_rope_frequencies(int32_t method, double base, int32_t rot_dim, double factor,
+                              double original, double low, double high, double* freqs,
+                              float* attention) {
+  if (method < QW_ROPE_NONE || method > QW_ROPE_BANDS) return QW_ERR_UNSUPPORTED;
+  if (!freqs || !attention || rot_dim < 2 || rot_dim % 2 || rot_dim > kRopeMaxDim)
+    return QW_ERR_INVALID_ARG;
+  if (!(base > 1.0 && base <= 1e30)) return QW_ERR_INVALID_ARG;
+  if (method != QW_ROPE_NONE && !(factor >= 1.0 && factor <= 1e9)) return QW_ERR_INVALID_ARG;
+  if ((method == QW_ROPE_YARN || method == QW_ROPE_BANDS) &&
+      !(original > 0.0 && original <= 1e18 && low >= 0.0 && high > low && high <= 1e18))
+    return QW_ERR_INVALID_ARG;
+  return rope_frequencies(method, base, rot_dim, factor, original, low, high, freqs, attention);
+}
+
+qw_status qw_rope(int32_t type, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t T,
+                  int32_t heads, int32_t head_dim, int32_t rot_dim, int32_t layout,
+                  const int32_t* positions, const double* freqs, float scale, int32_t* d_err,
+                  void* stream) {
+  if (type != QW_T_BF16 && type != QW_T_F16 && type != QW_T_F32) return QW_ERR_UNSUPPORTED;
+  if (layout != QW_ROPE_HALF && layout != QW_ROPE_INTERLEAVED) return QW_ERR_UNSUPPORTED;
+  if (T < 0 || heads < 1 || head_dim < 1 || rot_dim < 2 || rot_dim % 2 || rot_dim > head_dim)
+    return QW_ERR_INVALID_ARG;
+  if (T > 0x7FFFFFFFLL || head_dim > kRopeMaxDim || heads > kRopeMaxWidth / head_dim)
+    return QW_ERR_UNSUPPORTED;
+  const int64_t width = (int64_t)heads * head_dim;
+  if (ldx < width || ldy < width || !(scale >= -3.4e38f && scale <= 3.4e38f))
+    return QW_ERR_INVALID_ARG;
+  if (T == 0) return QW_OK;
+  if (!X || !Y || !positions || !freqs || (X == Y && ldx != ldy)) return QW_ERR_INVALID_ARG;
+  const int size = type == QW_T_F32 ? 4 : 2;
+  if (!aligned(X, size) || !aligned(Y, size) || !aligned(positions, 4) || !aligned(freqs, 8))
+    return QW_ERR_ALIGNMENT;
+  const RopeArgs a{X, ldx, Y, ldy, T, heads, head_dim, rot_dim, positions, freqs, scale, d_err};
+  return launch_rope(a, type, layout, static_cast<cudaStream_t>(stream));
+}
+
 qw_status qw_read_error(const int32_t* d_err, void* stream, int32_t* host_code) {
   if (!d_err || !host_code) return QW_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return QW_ERR_CUDA;

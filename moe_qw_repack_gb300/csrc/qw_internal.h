@@ -172,6 +172,68 @@ constexpr int32_t kLogprobsMaxTop = 32;
 constexpr int64_t kLogprobsMaxRows = (int64_t)1 << 26;  // rows of one call (grid size)
 qw_status launch_logprobs(const LogprobsArgs& a, int32_t type, int64_t T, cudaStream_t st);
 
+// Residual addition, norm and 8-bit operand (norm.cu); R, R_out, Y and Q may be null.
+struct NormArgs {
+  const void* X;   // BF16 or FP32
+  int64_t ldx;
+  const void* R;   // BF16 or FP32
+  int64_t ldr;
+  void* R_out;     // R's type
+  int64_t ldro;
+  const void* W;   // BF16 [K]
+  float offset, eps;
+  int64_t rows;
+  int32_t K;
+  void* Y;         // BF16
+  int64_t ldy;
+  void* Q;         // codes [rows][K]
+  void* Q_sf;
+  int32_t* err;
+};
+qw_status launch_rmsnorm(const NormArgs& a, int32_t x_type, int32_t r_type, int32_t q_fmt,
+                         cudaStream_t st);
+
+// Low-rank adapters (lora.cu); scales, ranks and base may be null.
+struct LoraArgs {
+  const uint16_t* X;      // BF16 [M][ldx]
+  int64_t ldx;
+  const uint16_t* A;      // BF16 [L][R][K]
+  const uint16_t* B;      // BF16 [L][N][R]
+  const float* scales;    // [L]
+  const int32_t* ranks;   // [L]
+  int32_t L, R;
+  const int32_t* ids;     // [M]
+  const void* base;       // C's type
+  int64_t ld_base;
+  void* C;
+  int64_t ldc;
+  int64_t M;
+  int32_t N, K;
+  int32_t* err;
+};
+constexpr int32_t kLoraMaxRank = 256;
+constexpr int64_t kLoraMaxRows = (int64_t)1 << 26;  // tokens of one call (grid size)
+qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st);
+
+// Rotary positions (rope.cu).
+struct RopeArgs {
+  const void* X;
+  int64_t ldx;
+  void* Y;
+  int64_t ldy;
+  int64_t T;
+  int32_t heads, head_dim, rot;
+  const int32_t* positions;  // [T]
+  const double* freqs;       // [rot / 2]
+  float scale;
+  int32_t* err;
+};
+constexpr int32_t kRopeMaxDim = 1024;       // of a head
+constexpr int32_t kRopeMaxWidth = 1 << 24;  // of a token's heads together
+qw_status launch_rope(const RopeArgs& a, int32_t type, int32_t layout, cudaStream_t st);
+qw_status rope_frequencies(int32_t method, double base, int32_t rot, double factor, double original,
+                           double low, double high, double* freqs, float* attention);
+
 // MoE scheduling.
 qw_status launch_moe_route(const float* logits, int32_t T, int32_t E, int32_t topk,
                            int32_t* topk_ids, int32_t* sorted_pairs, int32_t* offsets, void* ws,

@@ -42,6 +42,13 @@ QW_A_INT8_TOKEN = 3
 QW_T_BF16 = 0
 QW_T_F32 = 1
 QW_T_F16 = 2
+QW_ROPE_HALF = 0
+QW_ROPE_INTERLEAVED = 1
+QW_ROPE_NONE = 0
+QW_ROPE_LINEAR = 1
+QW_ROPE_NTK = 2
+QW_ROPE_YARN = 3
+QW_ROPE_BANDS = 4
 
 EXPORTS = (
     "qw_status_str", "qw_version", "qw_repack_query", "qw_repack", "qw_unpack",
@@ -54,6 +61,7 @@ EXPORTS = (
     "qw_mma_rate_probe",
     "qw_quantize_int8", "qgemm_int8_workspace_size", "qgemm_int8", "qgemm_int8_gated",
     "qw_logprobs",
+    "qw_rmsnorm", "qgemm_lora", "qw_rope", "qw_rope_frequencies",
 )
 
 
@@ -77,6 +85,8 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _U64 = ctypes.c_uint64
+_F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _DESC = ctypes.POINTER(PackedDesc)
 
 _SIGS = {
@@ -111,6 +121,14 @@ _SIGS = {
     "qgemm_int8_gated": (_I32, [_I32, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _P,
                                 _U64, _P, _P]),
     "qw_logprobs": (_I32, [_I32, _P, _I64, _I64, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "qw_rmsnorm": (_I32, [_I32, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _F32, _F32, _I64, _I32, _P,
+                          _I64, _I32, _P, _P, _P, _P]),
+    "qgemm_lora": (_I32, [_P, _I64, _P, _P, _P, _P, _I32, _I32, _P, _P, _I64, _I32, _P, _I64, _I64,
+                          _I32, _I32, _P, _P]),
+    "qw_rope": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _F32, _P,
+                       _P]),
+    "qw_rope_frequencies": (_I32, [_I32, _F64, _I32, _F64, _F64, _F64, _F64, ctypes.POINTER(_F64),
+                                   ctypes.POINTER(_F32)]),
 }
 
 
@@ -318,6 +336,42 @@ def qw_logprobs(l_type, logits, ld, T, V, tokens, topk, token_logprobs, token_ra
         l_type, _ptr(logits), ld, T, V, _ptr(tokens), topk, _ptr(token_logprobs),
         _ptr(token_ranks), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), _ptr(d_err),
         _stream(stream)))
+
+
+def qw_rmsnorm(x_type, X, ldx, r_type, R, ldr, R_out, ldro, W, w_offset, eps, rows, K, Y, ldy,
+               q_fmt=QW_A_BF16, Q=None, Q_sf=None, d_err=None, stream=None):
+    """h = X + R (written to R_out), y = h * (w_offset + W) / rms(h): BF16 rows Y and / or the codes
+    and scales of ``q_fmt``."""
+    _check("qw_rmsnorm", LIB.qw_rmsnorm(
+        x_type, _ptr(X), ldx, r_type, _ptr(R), ldr, _ptr(R_out), ldro, _ptr(W), w_offset, eps, rows,
+        K, _ptr(Y), ldy, q_fmt, _ptr(Q), _ptr(Q_sf), _ptr(d_err), _stream(stream)))
+
+
+def qgemm_lora(X, ldx, A, B, scales, ranks, L, R, ids, base, ld_base, c_type, C, ldc, M, N, K,
+               d_err=None, stream=None):
+    """C = base + scales[a] * B[a] (A[a] x) with each token's adapter a = ids[m] (-1: none);
+    A [L][R][K], B [L][N][R]."""
+    _check("qgemm_lora", LIB.qgemm_lora(
+        _ptr(X), ldx, _ptr(A), _ptr(B), _ptr(scales), _ptr(ranks), L, R, _ptr(ids), _ptr(base),
+        ld_base, c_type, _ptr(C), ldc, M, N, K, _ptr(d_err), _stream(stream)))
+
+
+def qw_rope(type, X, ldx, Y, ldy, T, heads, head_dim, rot_dim, layout, positions, freqs, scale=1.0,
+            d_err=None, stream=None):
+    """The heads of X's rows turned by positions * freqs (device FP64) into Y (may be X)."""
+    _check("qw_rope", LIB.qw_rope(
+        type, _ptr(X), ldx, _ptr(Y), ldy, T, heads, head_dim, rot_dim, layout, _ptr(positions),
+        _ptr(freqs), scale, _ptr(d_err), _stream(stream)))
+
+
+def qw_rope_frequencies(method, base, rot_dim, factor=1.0, original=0.0, low=1.0, high=32.0):
+    """(frequencies, attention): FP64 tensor [rot_dim / 2] on the host, and qw_rope's ``scale``."""
+    freqs = torch.empty(max(rot_dim, 2) // 2, dtype=torch.float64)
+    attention = _F32(1.0)
+    _check("qw_rope_frequencies", LIB.qw_rope_frequencies(
+        method, base, rot_dim, factor, original, low, high,
+        ctypes.cast(freqs.data_ptr(), ctypes.POINTER(_F64)), ctypes.byref(attention)))
+    return freqs, attention.value
 
 
 def qw_read_error(d_err, stream=None) -> int:
