@@ -528,7 +528,7 @@ qw_status qw_rmsnorm(int32_t x_type, const void* X, int64_t ldx, int32_t r_type,
  *   in FP32.
  *   An id outside [-1, L) or a rank outside [0, R] sets QW_ERR_INVALID_ARG in d_err; the token is
  *   then taken as one without adapter.
- *   K % 8 == 0, R % 8 == 0, R <= 256, M <= 2^26, N and K <= 2^31 - 256 (else QW_ERR_UNSUPPORTED).  X, A, B
+ *   K % 8 == 0, R % 8 == 0, R <= 256, M <= 2^26, N and K <= 2^30 (else QW_ERR_UNSUPPORTED).  X, A, B
  *   and the pitch of X 16-byte aligned, base and C their element size.  L * R * K and L * N * R may
  *   pass 2^31.  No workspace.
  */

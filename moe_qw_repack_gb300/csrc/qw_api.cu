@@ -582,7 +582,7 @@ qw_status qgemm_lora(const void* X, int64_t ldx, const void* A, const void* B, c
   if (c_type != QW_T_BF16 && c_type != QW_T_F32) return QW_ERR_UNSUPPORTED;
   if (M < 0 || N < 1 || K < 1 || L < 1 || R < 1 || ldx < K || ldc < N || (base && ld_base < N))
     return QW_ERR_INVALID_ARG;
-  if (K % 8 || R % 8 || R > kLoraMaxRank || M > kLoraMaxRows || N > kInt8MaxN || K > kInt8MaxN)
+  if (K % 8 || R % 8 || R > kLoraMaxRank || M > kLoraMaxRows || N > kLoraMaxDim || K > kLoraMaxDim)
     return QW_ERR_UNSUPPORTED;
   if (M == 0) return QW_OK;
   if (!X || !A || !B || !ids || !C || (base == C && ld_base != ldc)) return QW_ERR_INVALID_ARG;
