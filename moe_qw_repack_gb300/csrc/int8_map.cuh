@@ -1,4 +1,4 @@
-// int8_map.cuh - tensor maps of the INT8 products: two dimensions, 128-byte swizzle, zeros outside.
+// int8_map.cuh - tensor maps of the INT8 products and the adapters: two dimensions, zeros outside.
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -21,7 +21,8 @@ inline PFN_cuTensorMapEncodeTiled_v12000 int8_encode_fn() {
 
 inline bool encode_int8_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base,
                            uint64_t inner, uint64_t rows, uint64_t pitch_bytes, uint32_t box_inner,
-                           uint32_t box_rows) {
+                           uint32_t box_rows,
+                           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto enc = int8_encode_fn();
   if (!enc) return false;
   cuuint64_t dim[2] = {inner, rows};
@@ -29,7 +30,7 @@ inline bool encode_int8_2d(CUtensorMap* map, CUtensorMapDataType type, const voi
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t es[2] = {1, 1};
   return enc(map, type, 2, const_cast<void*>(base), dim, str, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -13,12 +13,9 @@
 // The order of k and r within an MMA is free as long as both operands have the same: a lane reads 16
 // bytes of a row at once, two MMAs' share.  In the second product row 8 g + i of 64 belongs to the lanes
 // of group g, so that a lane ends with eight neighbouring columns of a token, one 16-byte access of C.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 
-#include "qw_common.cuh"
-#include "qw_internal.h"
+#include "lora_common.cuh"
 
 namespace qw {
 namespace {
@@ -42,18 +39,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ float bf16_of(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
-// the first `n` of eight BF16 values, zeros behind them (what lies there may be anything)
-__device__ __forceinline__ uint4 first_of(uint4 v, int n) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w[j] = n >= 2 * j + 2 ? w[j] : n == 2 * j + 1 ? w[j] & 0xFFFFu : 0u;
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // t of one 16-row block of A for 8 NT tokens over 32-k chunks [c0, c1) from k0, below k1.
 template <int NT>
 __device__ __forceinline__ void shrink_block(const uint16_t* a_lo, const uint16_t* a_hi, bool lo, bool hi,
@@ -120,23 +105,6 @@ __device__ __forceinline__ void put8(const LoraArgs& p, bool wide, int64_t m, in
           c[i] = __bfloat16_as_ushort(__float2bfloat16_rn((b ? bf16_of(b[i]) : 0.f) + s[i]));
     }
   }
-}
-
-// Rows without adapter: base's bits.
-template <bool C32>
-__device__ __forceinline__ void copy_row(const LoraArgs& p, bool wide, int64_t m, int32_t n0, int32_t n1) {
-  using T = std::conditional_t<C32, uint32_t, uint16_t>;
-  constexpr int V = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31;
-  const T* b = p.base ? static_cast<const T*>(p.base) + m * p.ld_base : nullptr;
-  T* c = static_cast<T*>(p.C) + m * p.ldc;
-  int32_t n = n0;
-  if (wide) {
-    for (n += lane * V; n + V <= n1; n += 32 * V)
-      *reinterpret_cast<uint4*>(c + n) = b ? *reinterpret_cast<const uint4*>(b + n) : zero4();
-    n = n0 + (n1 - n0) / V * V;
-  }
-  for (n += lane; n < n1; n += 32) c[n] = b ? b[n] : (T)0;
 }
 
 struct Smem {
@@ -275,7 +243,7 @@ struct Pass {
 };
 
 template <bool C32, int NTM>
-__global__ void __launch_bounds__(THREADS) lora_mma_kernel(const LoraArgs p, const Cut cut) {
+__global__ void __launch_bounds__(THREADS, NTM == 1 ? 3 : 2) lora_mma_kernel(const LoraArgs p, const Cut cut) {
   using P = Pass<C32, NTM>;
   constexpr int T = 8 * NTM;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -299,13 +267,8 @@ __global__ void __launch_bounds__(THREADS) lora_mma_kernel(const LoraArgs p, con
     const int64_t m = m0 + threadIdx.x;
     int id = -2;
     if (m < p.M) {
-      id = p.ids[m];
-      const int rank = id >= 0 && id < p.L ? (p.ranks ? p.ranks[id] : p.R) : 0;
-      if (id < -1 || id >= p.L || rank < 0 || rank > p.R) {
-        set_error(p.err, QW_ERR_INVALID_ARG);
-        id = -1;
-      }
-      if (rank == 0) id = -1;
+      int rank;
+      id = adapter_of(p, m, rank);
     }
     ids[threadIdx.x] = id;
   }
@@ -336,6 +299,12 @@ __global__ void __launch_bounds__(THREADS) lora_mma_kernel(const LoraArgs p, con
     const uint32_t lo = __ballot_sync(0xFFFFFFFFu, ids[lane] == id);
     const uint32_t hi = __ballot_sync(0xFFFFFFFFu, ids[lane + 32] == id);
     const int cnt_lo = __popc(lo), cnt = cnt_lo + __popc(hi);
+    {  // the second product's weights on their way to L2
+      const int lines = (rank * 2 + 127) / 128;
+      const uint16_t* b = p.B + ((int64_t)id * p.N + n0) * p.R;
+      for (int i = threadIdx.x; i < (n1 - n0) * lines; i += THREADS)
+        prefetch_l2(b + (int64_t)(i / lines) * p.R + i % lines * 64);
+    }
     __syncthreads();  // (the last group's list has been read)
     if (warp == 0) {
       const uint32_t below = (1u << lane) - 1u;
@@ -415,6 +384,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
 }  // namespace
 
 qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st) {
+  if (a.M > 16 && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
   if (a.M <= 8) return c_f32 ? launch<true, 1>(a, st) : launch<false, 1>(a, st);
   return c_f32 ? launch<true, 4>(a, st) : launch<false, 4>(a, st);
 }

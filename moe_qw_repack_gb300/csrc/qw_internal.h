@@ -215,6 +215,9 @@ constexpr int32_t kLoraMaxRank = 256;
 constexpr int32_t kLoraMaxDim = 1 << 30;  // N and K: counted in 32 bits, rounded up to whole blocks
 constexpr int64_t kLoraMaxRows = (int64_t)1 << 26;  // tokens of one call (grid size)
 qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st);
+// on tcgen05, for more tokens
+bool lora_tc_takes(const LoraArgs& a, bool c_f32);
+qw_status launch_lora_tc(const LoraArgs& a, bool c_f32, cudaStream_t st);
 
 // Rotary positions (rope.cu).
 struct RopeArgs {
