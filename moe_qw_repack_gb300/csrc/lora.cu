@@ -12,12 +12,15 @@
 // t is held as a sum of BF16 numbers for the second product: two for BF16 results (2^-17 t is lost
 // of what the result rounds to 2^-9), three for FP32 ones (all 24 bits).
 // The order of k and r within an MMA is free as long as both operands have the same: a lane reads 16
-// bytes of a row at once, two MMAs' share.  In the second product row 8 g + i of 64 belongs to the lanes
-// of group g, so that a lane ends with eight neighbouring columns of a token, one 16-byte access of C.
-// Bound: latencies, one after the other (ids, ranks, A and X, the cluster's sums, B and base).  B's lines
-// are fetched to L2 from the start, and a block's weights and base before the sums are there.
+// bytes of a row at once, two MMAs' share.  In the second product row 4 g + i of 32 belongs to the lanes
+// of group g, so that a lane ends with four neighbouring columns of a token.
+// Bound: latencies, one after the other (ids, ranks, A and X, the cluster's sums, B).  So B comes through a
+// ring of TMA boxes of each warp's own (32 rows x 64 r, or 32 r where the rank is no more), filled from the
+// moment the adapter is known, and base two blocks ahead.  (Through registers alone 25.3 us for 64 tokens of
+// 32 adapters, 14336 x 4096; 16 warps a CTA 26.5; the rest of B prefetched to L2 26.3; now 23.3.)
 #include <algorithm>
 
+#include "int8_map.cuh"
 #include "lora_common.cuh"
 
 namespace qw {
@@ -25,7 +28,9 @@ namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int TM = 64;  // tokens of a tile
-constexpr int BN = 64;  // columns of a warp's block in the second product
+constexpr int BN = 32;  // columns of a warp's block in the second product
+constexpr int BR = 64;  // r of a box
+constexpr int SLOT = BN * BR * 2, SLOTS = 3;
 
 // How a call is cut up: a cluster of csize CTAs takes K in slices of k_len and, of the columns of its
 // part (nsplit of them), slices of n_len.
@@ -42,6 +47,11 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// `bytes` (a multiple of 16) from a 16-byte boundary on their way to L2
+__device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // t of one 16-row block of A for eight tokens over 32-k chunks [c0, c1) from k0, below k1.
 __device__ __forceinline__ void shrink_block(const uint16_t* a_lo, const uint16_t* a_hi, bool lo, bool hi,
                                              const uint16_t* x, bool live, int32_t k0, int32_t k1, int c0,
@@ -66,68 +76,51 @@ __device__ __forceinline__ void shrink_block(const uint16_t* a_lo, const uint16_
   }
 }
 
-// base of a lane's eight columns of a token, as it lies in memory
+// base of a lane's four columns of a token, as it lies in memory; `left`: columns from there to the end
 template <bool C32>
-struct Piece {
-  uint4 v[C32 ? 2 : 1];
-};
+using Piece = std::conditional_t<C32, uint4, uint2>;
 template <bool C32>
-__device__ __forceinline__ Piece<C32> get8(const LoraArgs& p, bool wide, int64_t m, int32_t n) {
-  Piece<C32> x;
-  constexpr int SIZE = C32 ? 4 : 2;
+__device__ __forceinline__ Piece<C32> get4(const uint8_t* b, bool wide, int32_t left) {
+  if (wide && left >= 4) return *reinterpret_cast<const Piece<C32>*>(b);
+  uint32_t w[4] = {};
 #pragma unroll
-  for (int i = 0; i < (C32 ? 2 : 1); ++i) x.v[i] = zero4();
-  if (!p.base) return x;
-  const uint8_t* b = static_cast<const uint8_t*>(p.base) + (m * p.ld_base + n) * SIZE;
-  if (wide && n + 8 <= p.N) {
-#pragma unroll
-    for (int i = 0; i < (C32 ? 2 : 1); ++i) x.v[i] = reinterpret_cast<const uint4*>(b)[i];
-  } else {
-    uint32_t w[C32 ? 8 : 4] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (n + i >= p.N) continue;
-      if constexpr (C32)
-        w[i] = reinterpret_cast<const uint32_t*>(b)[i];
-      else
-        w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(b)[i] << (16 * (i % 2));
-    }
-#pragma unroll
-    for (int i = 0; i < (C32 ? 2 : 1); ++i)
-      x.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  for (int i = 0; i < 4; ++i) {
+    if (i >= left) continue;
+    if constexpr (C32)
+      w[i] = reinterpret_cast<const uint32_t*>(b)[i];
+    else
+      w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(b)[i] << (16 * (i % 2));
   }
-  return x;
+  if constexpr (C32)
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    return make_uint2(w[0], w[1]);
 }
 // ... plus sums, to C
 template <bool C32>
-__device__ __forceinline__ void put8(const LoraArgs& p, bool wide, int64_t m, int32_t n,
-                                     const Piece<C32>& x, const float (&s)[8]) {
-  constexpr int SIZE = C32 ? 4 : 2;
-  uint8_t* c = static_cast<uint8_t*>(p.C) + (m * p.ldc + n) * SIZE;
-  uint32_t o[C32 ? 8 : 4];
+__device__ __forceinline__ void put4(uint8_t* c, bool wide, int32_t left, const Piece<C32>& x, float s0, float s1,
+                                     float s2, float s3) {
+  Piece<C32> o;
+  uint32_t w[4];
   if constexpr (C32) {
-    const uint32_t w[8] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w, x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(w[j]) + s[j]);
+    w[0] = __float_as_uint(__uint_as_float(x.x) + s0), w[1] = __float_as_uint(__uint_as_float(x.y) + s1);
+    w[2] = __float_as_uint(__uint_as_float(x.z) + s2), w[3] = __float_as_uint(__uint_as_float(x.w) + s3);
+    o = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
-    const uint32_t w[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = pack_bf16x2(__uint_as_float(w[j] << 16) + s[2 * j],
-                         __uint_as_float(w[j] & 0xFFFF0000u) + s[2 * j + 1]);
+    w[0] = pack_bf16x2(__uint_as_float(x.x << 16) + s0, __uint_as_float(x.x & 0xFFFF0000u) + s1);
+    w[1] = pack_bf16x2(__uint_as_float(x.y << 16) + s2, __uint_as_float(x.y & 0xFFFF0000u) + s3);
+    o = make_uint2(w[0], w[1]);
   }
-  if (wide && n + 8 <= p.N) {
-#pragma unroll
-    for (int i = 0; i < (C32 ? 2 : 1); ++i)
-      reinterpret_cast<uint4*>(c)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  if (wide && left >= 4) {
+    *reinterpret_cast<Piece<C32>*>(c) = o;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (n + i >= p.N) continue;
+    for (int i = 0; i < 4; ++i) {
+      if (i >= left) continue;
       if constexpr (C32)
-        reinterpret_cast<uint32_t*>(c)[i] = o[i];
+        reinterpret_cast<uint32_t*>(c)[i] = w[i];
       else
-        reinterpret_cast<uint16_t*>(c)[i] = (uint16_t)(o[i / 2] >> (16 * (i % 2)));
+        reinterpret_cast<uint16_t*>(c)[i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
     }
   }
 }
@@ -211,70 +204,47 @@ struct Pass {
     }
   }
 
-  // of a block of 64 columns: the weights of 32 r of a lane's eight rows
-  struct Weights {
-    uint4 w[8];
-  };
-  __device__ __forceinline__ void load(int32_t nb, int32_t n1, int r0, Weights& x) const {
-    const int32_t n = nb + 8 * g;
-    const int left = rank - r0 - 8 * t;  // of this lane's eight r, how many count
-    const uint16_t* b = p.B + ((int64_t)id * p.N + n) * p.R + r0 + 8 * t;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x.w[i] = left > 0 && n + i < n1 ? *reinterpret_cast<const uint4*>(b + (int64_t)i * p.R) : zero4();
+};
+
+// A warp's ring of B's boxes: those of its blocks (every eighth of the CTA's), r after r.
+struct Ring {
+  uint8_t* slots;
+  uint64_t* full;
+  int32_t n0, end;        // the warp's first column, where the CTA's end
+  int id, rank;
+  // what is asked for next (one lane), and the next slots to fill and to read
+  int32_t n, r;
+  uint32_t ask, take, phase;
+
+  __device__ __forceinline__ void start() { n = n0, r = 0; }
+  __device__ __forceinline__ void request(const CUtensorMap& wide, const CUtensorMap& narrow) {
+    if (n >= end) return;
+    const bool half = rank <= 32;
+    mbar_arrive_expect_tx(&full[ask], half ? SLOT / 2 : SLOT);
+    tma_load_3d(slots + ask * SLOT, half ? &narrow : &wide, &full[ask], r, n, id);
+    r += BR;
+    if (r >= rank) r = 0, n += WARPS * BN;
+    ask = ask + 1 == SLOTS ? 0 : ask + 1;
   }
-  // base + B t for this CTA's columns; `next`: the first block's weights
-  __device__ __forceinline__ void expand(int32_t n0, int32_t n1, const uint16_t* ts, int pitch,
-                                         Weights& next) const {
-    for (int32_t nb = n0 + warp * BN; nb < n1; nb += WARPS * BN) {
-      const int32_t n = nb + 8 * g;
-      Piece<C32> was[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (2 * t + e < cnt && n < n1) was[e] = get8<C32>(p, cut.wide, m0 + list[2 * t + e], n);
-      float acc[4][4] = {};
-      for (int r0 = 0; r0 < rank; r0 += 32) {
-        Weights x = next;
-        const bool more = r0 + 32 < rank;
-        load(more ? nb : nb + WARPS * BN, n1, more ? r0 + 32 : 0, next);
-        const int left = rank - r0 - 8 * t;
-        if (left < 8) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x.w[i] = first_of(x.w[i], left);
-        }
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const uint4 v = *reinterpret_cast<const uint4*>(ts + (s * T + g) * pitch + r0 + 8 * t);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mma_bf16(acc[i], x.w[2 * i].x, x.w[2 * i + 1].x, x.w[2 * i].y, x.w[2 * i + 1].y, v.x, v.y);
-            mma_bf16(acc[i], x.w[2 * i].z, x.w[2 * i + 1].z, x.w[2 * i].w, x.w[2 * i + 1].w, v.z, v.w);
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (2 * t + e >= cnt || n >= n1) continue;
-        float s[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[2 * i] = acc[i][e];
-          s[2 * i + 1] = acc[i][2 + e];
-        }
-        put8<C32>(p, cut.wide, m0 + list[2 * t + e], n, was[e], s);
-      }
-    }
+  __device__ __forceinline__ void next() {
+    if (++take == SLOTS) take = 0, phase ^= 1u;
   }
 };
 
 template <bool C32>
-__global__ void __launch_bounds__(THREADS, 2) lora_mma_kernel(const __grid_constant__ LoraArgs p,
-                                                              const __grid_constant__ Cut cut) {
-  extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(THREADS, 2)
+    lora_mma_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB32,
+                    const __grid_constant__ LoraArgs p, const __grid_constant__ Cut cut) {
+  constexpr int NS = C32 ? 3 : 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (0u - smem_u32(smem_raw) & 1023u);  // (stays a shared address)
   __shared__ uint8_t lists[WARPS][TM];
-  const Smem lay{(p.R + 31) / 32 * 32, C32 ? 3 : 2};
-  float* sums = reinterpret_cast<float*>(smem);
-  float* part = reinterpret_cast<float*>(smem + lay.sum_bytes());
+  __shared__ uint64_t full[WARPS][SLOTS];
+  __shared__ int abort_shared;
+  volatile int* abort_flag = &abort_shared;
+  const Smem lay{(p.R + 31) / 32 * 32, NS};
+  float* sums = reinterpret_cast<float*>(smem + WARPS * SLOTS * SLOT);
+  float* part = reinterpret_cast<float*>(smem + WARPS * SLOTS * SLOT + lay.sum_bytes());
   uint16_t* ts = reinterpret_cast<uint16_t*>(part);
   const int crank = (int)(blockIdx.x & (unsigned)(cut.csize - 1));
   const unsigned cluster = blockIdx.x >> cut.csize_log;
@@ -283,7 +253,11 @@ __global__ void __launch_bounds__(THREADS, 2) lora_mma_kernel(const __grid_const
   const int64_t at = (int64_t)((cluster - tile * (unsigned)cut.nsplit) * cut.csize + crank) * cut.n_len;
   const int32_t n0 = (int32_t)min64(p.N, at), n1 = (int32_t)min64(p.N, at + cut.n_len);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
+  if (threadIdx.x < WARPS * SLOTS) mbar_init(&full[0][0] + threadIdx.x, 1);
+  if (threadIdx.x == 0) abort_shared = 0;
+  fence_barrier_init();
+  __syncthreads();
+  pdl_wait();  // (before the first use of the tensor maps too: their addresses are used again by later launches)
   pdl_launch_dependents();
 
   // The tokens' adapters, two a lane, each warp for itself: -1 none (or none that works), -2 behind the
@@ -303,52 +277,128 @@ __global__ void __launch_bounds__(THREADS, 2) lora_mma_kernel(const __grid_const
       first_hi = first_hi && other != id_hi;
     }
   }
-  uint64_t leaders = __ballot_sync(0xFFFFFFFFu, first_lo) |
-                     (uint64_t)__ballot_sync(0xFFFFFFFFu, first_hi) << 32;
+  const uint32_t below = (1u << lane) - 1u;
+  const uint32_t firsts_lo = __ballot_sync(0xFFFFFFFFu, first_lo), firsts_hi = __ballot_sync(0xFFFFFFFFu, first_hi);
+  const int groups = __popc(firsts_lo) + __popc(firsts_hi);
+  const int my_lo = __popc(firsts_lo & below), my_hi = __popc(firsts_lo) + __popc(firsts_hi & below);
 
   bool reading = false;  // others may still read this CTA's sums
-  for (int group = 0, mine = (int)blockIdx.y; leaders; ++group) {
-    const int leader = __ffsll((long long)leaders) - 1;
-    leaders &= leaders - 1;
-    if (group != mine) continue;
-    mine += (int)gridDim.y;
-    const int id = __shfl_sync(0xFFFFFFFFu, leader < 32 ? id_lo : id_hi, leader & 31);
-    const int rank = __shfl_sync(0xFFFFFFFFu, leader < 32 ? rank_lo : rank_hi, leader & 31);
+  bool ok = true;
+  Ring ring{smem + warp * (SLOTS * SLOT), full[warp], n0 + warp * BN, n1};
+  const int g = lane >> 2, t = lane & 3;
+  for (int group = (int)blockIdx.y; group < groups; group += (int)gridDim.y) {
+    const uint32_t in_lo = __ballot_sync(0xFFFFFFFFu, first_lo && my_lo == group);
+    const uint32_t in_hi = __ballot_sync(0xFFFFFFFFu, first_hi && my_hi == group);
+    const int leader = __ffs((int)(in_lo | in_hi)) - 1;
+    const int id = __shfl_sync(0xFFFFFFFFu, in_lo ? id_lo : id_hi, leader);
+    const int rank = __shfl_sync(0xFFFFFFFFu, in_lo ? rank_lo : rank_hi, leader);
     const float scale = p.scales ? p.scales[id] : 1.f;
-    {  // the second product's weights on their way to L2
-      const uint16_t* b = p.B + (int64_t)id * p.N * p.R;
-      for (int32_t n = n0 + (int32_t)threadIdx.x; n < n1; n += THREADS)
-        for (int r = 0; r < rank; r += 64) prefetch_l2(b + (int64_t)n * p.R + r);
-    }
+    ring.id = id, ring.rank = rank;
     const uint32_t lo = __ballot_sync(0xFFFFFFFFu, id_lo == id), hi = __ballot_sync(0xFFFFFFFFu, id_hi == id);
     const int cnt_lo = __popc(lo), cnt = cnt_lo + __popc(hi);
-    const uint32_t below = (1u << lane) - 1u;
     __syncwarp();  // (the last group's list has been read)
     if (lo >> lane & 1) lists[warp][__popc(lo & below)] = (uint8_t)lane;
     if (hi >> lane & 1) lists[warp][cnt_lo + __popc(hi & below)] = (uint8_t)(lane + 32);
     __syncwarp();
     for (int done = 0; done < cnt; done += T) {
       const int now = min(T, cnt - done);
-      const Pass<C32> pass{p, cut, m0, id, rank, now, lists[warp] + done, lane, warp, lane >> 2, lane & 3};
-      // base, too
-      for (int i = warp; i < now && p.base; i += WARPS) {
-        const uint8_t* b = static_cast<const uint8_t*>(p.base) + (m0 + pass.list[i]) * p.ld_base * (C32 ? 4 : 2);
-        for (int32_t n = n0 + lane * 64; n < n1; n += 32 * 64)
-          for (int h = 0; h < (C32 ? 2 : 1); ++h) prefetch_l2(b + (int64_t)n * (C32 ? 4 : 2) + 128 * h);
+      const uint8_t* list = lists[warp] + done;
+      ring.start();
+      if (lane == 0 && ok)
+        for (int i = 0; i < SLOTS; ++i) ring.request(tmB, tmB32);
+      if (lane == 0 && warp < now && p.base && cut.wide && n1 - n0 >= 8) {  // base on its way to L2
+        constexpr int SIZE = C32 ? 4 : 2;
+        bulk_prefetch_l2(static_cast<const uint8_t*>(p.base) + ((m0 + list[warp]) * p.ld_base + n0) * SIZE,
+                         (uint32_t)(n1 - n0) / 8u * 8u * SIZE);
       }
-      typename Pass<C32>::Weights w;
+      __syncwarp();
+      const Pass<C32> pass{p, cut, m0, id, rank, now, list, lane, warp, g, t};
       if (reading) cluster_wait();
       pass.shrink(crank, sums, part);
-      pass.load(n0 + warp * BN, n1, 0, w);
       cluster_sync();
       pass.gather(scale, sums, ts, lay.pitch());
       cluster_arrive();
       reading = true;
       __syncthreads();
-      pass.expand(n0, n1, ts, lay.pitch(), w);
+      // base + B t for this warp's blocks: a lane's rows of a box, its tokens' rows of base and C
+      constexpr int SIZE = C32 ? 4 : 2;
+      const int shift = rank <= 32 ? 6 : 7;
+      int at[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * g + i;
+        at[i] = (row << shift) + ((t ^ (shift == 7 ? row & 7 : row >> 1 & 3)) << 4);
+      }
+      const uint16_t* my_t = ts + g * lay.pitch() + 8 * t;
+      const uint8_t* b[2] = {};
+      uint8_t* c[2];
+      int32_t n = ring.n0 + 4 * g;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t m = m0 + (2 * t + e < now ? list[2 * t + e] : 0);
+        if (p.base) b[e] = static_cast<const uint8_t*>(p.base) + (m * p.ld_base + n) * SIZE;
+        c[e] = static_cast<uint8_t*>(p.C) + (m * p.ldc + n) * SIZE;
+      }
+      const bool mine0 = 2 * t < now, mine1 = 2 * t + 1 < now;
+      Piece<C32> one[2] = {}, two[2] = {};  // base of the next two blocks
+      auto ahead = [&](int32_t to, Piece<C32>(&x)[2]) {
+        const int32_t left = n1 - n - to;
+        if (left <= 0 || !p.base) return;
+        if (mine0) x[0] = get4<C32>(b[0] + (int64_t)to * SIZE, cut.wide, left);
+        if (mine1) x[1] = get4<C32>(b[1] + (int64_t)to * SIZE, cut.wide, left);
+      };
+      ahead(0, one);
+      ahead(WARPS * BN, two);
+      for (int32_t nb = ring.n0; nb < n1; nb += WARPS * BN) {
+        const Piece<C32> was[2] = {one[0], one[1]};
+        one[0] = two[0], one[1] = two[1];
+        ahead(2 * WARPS * BN, two);
+        float acc[2][4] = {};
+#pragma unroll 1
+        for (int r = 0; r < rank; r += BR) {
+          if (ok) ok = warp_wait(&full[warp][ring.take], ring.phase, abort_flag, p.err);
+          const uint8_t* box = ring.slots + ring.take * SLOT;
+#pragma unroll
+          for (int r0 = 0; r0 < BR; r0 += 32) {
+            const int left = rank - r - r0;
+            if (left <= 0) break;
+            uint4 w[4];
+            const bool some = left > 8 * t;  // (what lies past the rank may be anything)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = some ? *reinterpret_cast<const uint4*>(box + (at[i] ^ 2 * r0)) : zero4();
+            if (rank & 7 && left < 32) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = first_of(w[i], left - 8 * t);
+            }
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+              const uint4 v = *reinterpret_cast<const uint4*>(my_t + s * T * lay.pitch() + r + r0);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                mma_bf16(acc[i], w[2 * i].x, w[2 * i + 1].x, w[2 * i].y, w[2 * i + 1].y, v.x, v.y);
+                mma_bf16(acc[i], w[2 * i].z, w[2 * i + 1].z, w[2 * i].w, w[2 * i + 1].w, v.z, v.w);
+              }
+            }
+          }
+          __syncwarp();  // the box has been read
+          ring.next();
+          if (lane == 0 && ok) ring.request(tmB, tmB32);
+        }
+        const int32_t left = n1 - n;
+        if (left > 0) {
+          if (mine0) put4<C32>(c[0], cut.wide, left, was[0], acc[0][0], acc[0][2], acc[1][0], acc[1][2]);
+          if (mine1) put4<C32>(c[1], cut.wide, left, was[1], acc[0][1], acc[0][3], acc[1][1], acc[1][3]);
+        }
+        n += WARPS * BN;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) b[e] += WARPS * BN * SIZE, c[e] += WARPS * BN * SIZE;
+      }
       __syncthreads();  // (ts and part share their place)
     }
   }
+  if (!ok && lane == 0)  // after a wait that gave up: let the copies land
+    for (int i = 0; i < SLOTS; ++i) wait_landed(&full[warp][i], i < (int)ring.take ? ring.phase ^ 1u : ring.phase);
   if (p.C != p.base)
     for (int i = warp + WARPS * (int)blockIdx.y; i < TM; i += WARPS * (int)gridDim.y) {
       const int id = __shfl_sync(0xFFFFFFFFu, i < 32 ? id_lo : id_hi, i & 31);
@@ -364,14 +414,14 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   const int64_t groups = std::min<int64_t>(std::min<int64_t>(TM, a.M), a.L);  // of a tile, at most
   Cut cut{};
   cut.csize = 1;
-  while (cut.csize < 8 && (a.K >= 256 * cut.csize || a.N >= 2 * BN * cut.csize)) cut.csize *= 2, ++cut.csize_log;
+  while (cut.csize < 8 && (a.K >= 256 * cut.csize || a.N >= 128 * cut.csize)) cut.csize *= 2, ++cut.csize_log;
   cut.nsplit = 1;
   while (tiles * groups * cut.csize * cut.nsplit * 2 <= 2 * sms &&
          (int64_t)a.N * a.R * 2 / (cut.csize * cut.nsplit) > 32768)
     cut.nsplit *= 2;
   const int parts = cut.csize * cut.nsplit;
   cut.k_len = ((a.K + cut.csize - 1) / cut.csize + 63) / 64 * 64;
-  cut.n_len = (int32_t)(((int64_t)a.N + parts - 1) / parts + BN - 1) / BN * BN;
+  cut.n_len = (int32_t)((((int64_t)a.N + parts - 1) / parts + 63) / 64 * 64);
   const int vec = C32 ? 4 : 8;
   cut.wide = ((uintptr_t)a.C | (uintptr_t)a.base) % 16 == 0 && a.ldc % vec == 0 &&
              (!a.base || a.ld_base % vec == 0);
@@ -380,17 +430,22 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   if (x > 0x7FFFFFFF) return QW_ERR_UNSUPPORTED;
   const Smem lay{(a.R + 31) / 32 * 32, C32 ? 3 : 2};
   constexpr Smem most{kLoraMaxRank, C32 ? 3 : 2};
+  constexpr int RING = 1024 + WARPS * SLOTS * SLOT;
+  CUtensorMap tmB, tmB32;
+  if (!encode_bf16_3d(&tmB, a.B, a.R, a.N, a.L, BR, BN) ||
+      !encode_bf16_3d(&tmB32, a.B, a.R, a.N, a.L, 32, BN, CU_TENSOR_MAP_SWIZZLE_64B))
+    return QW_ERR_CUDA;
   static std::atomic<int> ready[64];
   if (once_per_device(ready, [&] {
         return cudaFuncSetAttribute(lora_mma_kernel<C32>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    most.bytes()) == cudaSuccess;
+                                    RING + most.bytes()) == cudaSuccess;
       }) <= 0)
     return QW_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)x, (unsigned)y);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = (size_t)lay.bytes();
+  cfg.dynamicSmemBytes = (size_t)(RING + lay.bytes());
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -400,14 +455,16 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cut.csize > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, lora_mma_kernel<C32>, a, cut) == cudaSuccess ? QW_OK : QW_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, lora_mma_kernel<C32>, tmB, tmB32, a, cut) == cudaSuccess ? QW_OK : QW_ERR_CUDA;
 }
 
 }  // namespace
 
 qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st) {
-  // Tokens of an adapter that are more than a few go through the tensor cores together.
-  if (a.M > 16 && a.M > 8 * (int64_t)a.L && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
+  // Many tokens of an adapter go through the tensor cores together (us here and there, 4096 x 4096: 64 tokens of
+  // 64 adapters rank 64 26, 35; 64 of 8 rank 16 11, 17; 128 of 64 rank 16 23, 31; 192 of 64 rank 64 46, 36;
+  // 4096 x 14336 x 4096 rank 64 216, 87).
+  if (a.M > 16 && (a.M > 128 || a.M > T * (int64_t)a.L) && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
   return c_f32 ? launch<true>(a, st) : launch<false>(a, st);
 }
 

@@ -32,6 +32,15 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& p, int64_t m, int& ran
   return rank > 0 ? id : -1;
 }
 
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // Rows without adapter: base's bits.
 template <bool C32>
 __device__ __forceinline__ void copy_row(const LoraArgs& p, bool wide, int64_t m, int32_t n0, int32_t n1) {

@@ -932,14 +932,17 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   if (p.all_bytes / stage1 < 2 || p.s2 < 2) return QW_ERR_UNSUPPORTED;
   // The cheapest cluster, in rounds of what runs at once (about 90 % of it: a cluster lies within one GPC) of
   // what an item takes: to find and, shared, to join (cycles 8000 and 15000), and each CTA's share of the
-  // stages (1000 each) and tiles (2200).  About a fifth of the items are parts of 128 tokens.
-  const int64_t items = (a.M + TT - 1) / TT * 5 / 4 + 1, at_once = sms * (two ? 2 : 1) * 9 / 10;
-  int64_t least = INT64_MAX;
+  // stages (1000 each) and tiles (4400).  About a fifth of the items are parts of 128 tokens; in small calls
+  // each adapter has one of its own.  (us with clusters of 2, 4 and 8: 4096 x 14336 x 4096 rank 64 185, 103,
+  // [87]; 8192 x 4096 x 4096 rank 128 [84], 92, 135; 256 tokens of 64 adapters, 4096 x 4096 rank 32 50, [34], 43.)
+  const double items = (double)((a.M + TT - 1) / TT) * 1.25 + 1 + (a.M <= WINDOW ? std::min<int64_t>(a.L, a.M) : 0);
+  const double at_once = sms * (two ? 2 : 1) * 0.9;
+  double least = 1e30;
   for (int log = 0; log <= 3; ++log) {
     const int64_t c = (int64_t)1 << log;
     if ((c > 1 && c > all_k && c > all_tiles) || (c == 2 && a.R > 128)) continue;
-    const int64_t rounds = (items * c + at_once - 1) / at_once;
-    const int64_t cost = rounds * (8000 + (c > 1 ? 15000 : 0) + (all_k + c - 1) / c * 1000 + (all_tiles + c - 1) / c * 2200);
+    const double cost = std::max(1.0, items * c / at_once) *
+                        (8000.0 + (c > 1 ? 15000 : 0) + (all_k + c - 1) / c * 1000.0 + (all_tiles + c - 1) / c * 4400.0);
     if (cost < least) least = cost, p.csize_log = log;
   }
   const int csize = 1 << p.csize_log;
