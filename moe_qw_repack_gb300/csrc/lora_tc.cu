@@ -823,41 +823,41 @@ __global__ void __launch_bounds__(THREADS, 2)
         tma_store_done();
         __syncwarp();
       } else {
-      for (int d = 0; d < depth; ++d) load(d);
-      for (int i = 0; i < tiles; ++i) {
-        const uint32_t v = ua + (uint32_t)i, buf = v & 1u;
-        prefetch_base(i + 2, e);
-        if (ok) ok = warp_wait(&acc_full[buf], v >> 1 & 1u, abort_flag, a.err);
-        tc_fence_after();
-        for (int unit = i << per_log; unit < min(units, (i + 1) << per_log); ++unit) {
-          cp_async_wait_upto(depth - 1);
-          __syncwarp();  // the unit's base is there
-          uint8_t* at = place(unit);
-          const uint32_t d2 = tbase + lanes + buf * BN + col0 + ((unit & last) << cols_log);
-          for (int c = 0; c < cols; c += 16) {
-            float d[16];
-            uint4 was[16 / EACH];
-            tc_ld<16>(d2 + c, d);
+        for (int d = 0; d < depth; ++d) load(d);
+        for (int i = 0; i < tiles; ++i) {
+          const uint32_t v = ua + (uint32_t)i, buf = v & 1u;
+          prefetch_base(i + 2, e);
+          if (ok) ok = warp_wait(&acc_full[buf], v >> 1 & 1u, abort_flag, a.err);
+          tc_fence_after();
+          for (int unit = i << per_log; unit < min(units, (i + 1) << per_log); ++unit) {
+            cp_async_wait_upto(depth - 1);
+            __syncwarp();  // the unit's base is there
+            uint8_t* at = place(unit);
+            const uint32_t d2 = tbase + lanes + buf * BN + col0 + ((unit & last) << cols_log);
+            for (int c = 0; c < cols; c += 16) {
+              float d[16];
+              uint4 was[16 / EACH];
+              tc_ld<16>(d2 + c, d);
 #pragma unroll
-            for (int j = 0; j < 16 / EACH; ++j)
-              was[j] = a.base ? *reinterpret_cast<const uint4*>(at + piece(my_row, c / EACH + j)) : zero4();
-            tc_landed(d);
+              for (int j = 0; j < 16 / EACH; ++j)
+                was[j] = a.base ? *reinterpret_cast<const uint4*>(at + piece(my_row, c / EACH + j)) : zero4();
+              tc_landed(d);
 #pragma unroll
-            for (int j = 0; j < 16 / EACH; ++j) {
-              const uint4 o = add_piece<C32>(was[j], d + j * EACH);
-              if (lane < count) *reinterpret_cast<uint4*>(at + piece(my_row, c / EACH + j)) = o;
+              for (int j = 0; j < 16 / EACH; ++j) {
+                const uint4 o = add_piece<C32>(was[j], d + j * EACH);
+                if (lane < count) *reinterpret_cast<uint4*>(at + piece(my_row, c / EACH + j)) = o;
+              }
             }
+            __syncwarp();  // its results are
+            store(unit);
+            __syncwarp();
+            load(unit + depth);
           }
-          __syncwarp();  // its results are
-          store(unit);
+          tc_fence_before();
           __syncwarp();
-          load(unit + depth);
+          if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
-      }
-      cp_async_wait<0>();
+        cp_async_wait<0>();
       }
     }
     u1 += (uint32_t)nk;
