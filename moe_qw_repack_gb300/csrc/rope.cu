@@ -19,12 +19,19 @@
 namespace qw {
 namespace {
 
-// Turns per position of a frequency in radians, as a 64-bit fraction (whole turns dropped).
-// 1/(2 pi) in two FP64 parts: 0.15915494309189535 - 9.8393383375... e-18.
-__device__ __forceinline__ uint64_t turns(double f) {
-  const double c_hi = 0.15915494309189535, c_lo = -9.839338337591243e-18;
-  const double hi = f * c_hi, lo = fma(f, c_hi, -hi) + f * c_lo;
-  return __double2ull_rn((hi - floor(hi)) * 0x1p64) + (uint64_t)__double2ll_rn(lo * 0x1p64);
+// Turns per position of a frequency in radians (|f| <= 2^32), as a 64-bit fraction (whole turns dropped): the
+// 53 bits of f times 1 / (2 pi) in 128 bits, cut off where the fraction ends.  (FP64 arithmetic for this took
+// 0.6 us more of a small call: an SM has little of it.)
+__device__ __forceinline__ uint64_t turns(uint64_t f) {  // f: the FP64 number's bits
+  const uint64_t c_hi = 0x28BE60DB9391054AULL, c_lo = 0x7F09D5F47D4D3770ULL;
+  const uint32_t exponent = (uint32_t)(f >> 52) & 0x7FFu;
+  const uint64_t m = (f & 0xFFFFFFFFFFFFFull) | (exponent ? 1ull << 52 : 0ull);  // f = m 2^(exponent - 1075)
+  const uint64_t mid = m * c_hi, carry = __umul64hi(m, c_lo);
+  const uint64_t p1 = mid + carry, p2 = __umul64hi(m, c_hi) + (p1 < mid ? 1u : 0u);  // above the low 64 bits
+  const uint32_t shift = 64u + 1075u - max(exponent, 1u);  // at least 84
+  const uint64_t r = shift < 128 ? p1 >> (shift - 64) | p2 << (128 - shift)
+                                 : shift < 192 ? p2 >> (shift - 128) : 0ull;
+  return f >> 63 ? 0ull - r : r;
 }
 
 // cosine and sine of a 64-bit fraction of a turn
@@ -59,101 +66,177 @@ struct Elem<QW_T_F32> {
 };
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_TOKENS = 4;
+constexpr int ROPE_ITEMS = 5 * ROPE_THREADS;    // that a CTA takes tokens for
+constexpr int ROPE_TABLE = 2048;                // cosines and sines of a CTA, unless one token has more
 
-// V: elements of a thread's vector (16 bytes), or 1 where pitch, alignment or sizes do not allow it.
+struct Shape {
+  RopeArgs a;
+  int32_t tokens;    // of a CTA
+  int32_t turn;      // items of a head that are turned
+  int32_t per_head;  // ... and copied
+  // a step of all threads, in heads and items of a head
+  int32_t step_heads, step_items;
+  int32_t groups;    // threads that share a frequency
+  uint32_t by_half, by_head, by_heads;  // ceil(2^32 / d) for rot / 2, per_head and heads (0: d is 1)
+};
+// n / d; where n d passes 2^32 it may be one more
+__device__ __forceinline__ int divide(int n, uint32_t by) { return by ? (int)__umulhi((uint32_t)n, by) : n; }
+inline uint32_t divisor(int64_t d) { return d == 1 ? 0u : (uint32_t)(((1ull << 32) + (uint64_t)d - 1) / (uint64_t)d); }
+
+// A CTA makes its tokens' cosines and sines once for all heads, then each thread takes an item of V values of
+// a head at a time (half layout: two vectors of V, rot / 2 apart; interleaved: one): 16 bytes where pitch,
+// alignment and sizes allow, else 8, 4 or a value.  Items are counted on without divisions, which took most of
+// the narrow forms' time (16384 tokens, 20 heads of 256, 126 turned: interleaved FP16 202 -> 109 us, half BF16
+// 208 -> 148).
 template <int TYPE, int LAYOUT, int V>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ Shape s) {
   using E = Elem<TYPE>;
   using T = typename E::T;
   struct alignas(V * sizeof(T)) Vec {
     T v[V];
   };
+  const RopeArgs& a = s.a;
   extern __shared__ float2 table[];  // [tokens][rot / 2]
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t t0 = (int64_t)blockIdx.x * ROPE_TOKENS;
-  const int tokens = (int)min64(ROPE_TOKENS, a.T - t0), half = a.rot / 2;
-  for (int j = threadIdx.x; j < half; j += ROPE_THREADS) {
-    const double f = a.freqs[j];
-    const bool ok = fabs(f) <= 0x1p32;
-    if (!ok) set_error(a.err, QW_ERR_VALUE);
-    const uint64_t per = ok ? turns(f) : 0;
-    for (int t = 0; t < tokens; ++t) {
-      float2 cs = cos_sin(per * (uint64_t)(int64_t)a.positions[t0 + t]);
-      cs.x *= a.scale, cs.y *= a.scale;
-      table[t * half + j] = ok ? cs : make_float2(NAN, NAN);
+  const int64_t t0 = (int64_t)blockIdx.x * s.tokens;
+  const int tokens = (int)min64(s.tokens, a.T - t0), half = a.rot / 2;
+  {
+    const int groups = s.groups, group = groups > 1 ? divide((int)threadIdx.x, s.by_half) : 0;
+    for (int j = (int)threadIdx.x - group * half; j < half && group < groups; j += ROPE_THREADS) {
+      const uint64_t f = reinterpret_cast<const uint64_t*>(a.freqs)[j];
+      const bool ok = (f & ~(1ull << 63)) <= 0x41F0000000000000ull;  // |f| <= 2^32 (NaN and infinity are above)
+      if (!ok) set_error(a.err, QW_ERR_VALUE);
+      const uint64_t per = ok ? turns(f) : 0;
+      for (int t = group; t < tokens; t += groups) {
+        float2 cs = cos_sin(per * (uint64_t)(int64_t)a.positions[t0 + t]);
+        cs.x *= a.scale, cs.y *= a.scale;
+        table[t * half + j] = ok ? cs : make_float2(NAN, NAN);
+      }
+      if (groups > 1) break;
     }
   }
   __syncthreads();
-  const T* X = static_cast<const T*>(a.X);
-  T* Y = static_cast<T*>(a.Y);
-  // A head's items: vectors of pairs (half layout: two vectors, rot / 2 apart), then (unless in place)
-  // vectors to copy.
   constexpr int PAIRS = LAYOUT == QW_ROPE_HALF ? V : (V == 1 ? 1 : V / 2);  // of an item
-  const int turn = half / PAIRS, keep = a.X == a.Y ? 0 : (a.head_dim - a.rot) / V;
-  const int per_head = turn + keep, per_token = per_head * a.heads;
-  for (int i = threadIdx.x + blockIdx.y * ROPE_THREADS; i < per_token * tokens;
-       i += ROPE_THREADS * gridDim.y) {
-    const int t = i / per_token, rest = i - t * per_token, head = rest / per_head;
-    const int k = rest - head * per_head;
-    const T* x = X + (t0 + t) * a.ldx + (int64_t)head * a.head_dim;
-    T* y = Y + (t0 + t) * a.ldy + (int64_t)head * a.head_dim;
-    if (k >= turn) {
-      const int c = a.rot + (k - turn) * V;
-      *reinterpret_cast<Vec*>(y + c) = *reinterpret_cast<const Vec*>(x + c);
-    } else if constexpr (LAYOUT == QW_ROPE_HALF) {
-      const int c = k * V;
-      Vec p = *reinterpret_cast<const Vec*>(x + c), q = *reinterpret_cast<const Vec*>(x + half + c);
+  const int first = (int)(threadIdx.x + blockIdx.y * ROPE_THREADS);
+  int head = divide(first, s.by_head), k = first - head * s.per_head, t = divide(head, s.by_heads);
+  head -= t * a.heads;
+  if (head < 0) head += a.heads, --t;  // (over 2^15 heads: one too many)
+  auto advance = [&] {
+    k += s.step_items;
+    head += s.step_heads;
+    if (k >= s.per_head) k -= s.per_head, ++head;
+    while (head >= a.heads) head -= a.heads, ++t;
+  };
+  constexpr bool TWO = LAYOUT == QW_ROPE_HALF || V == 1;  // a pair's values lie in two vectors
+  const int apart = LAYOUT == QW_ROPE_HALF ? half : 1;
+  // (p, q) or p turned by the V / 2 or V angles from cs on
+  auto turn = [](Vec& p, Vec& q, const float2* cs) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 cs = table[t * half + c + j];
-        const float u = E::get(p.v[j]), w = E::get(q.v[j]);
-        p.v[j] = E::put(u * cs.x - w * cs.y);
-        q.v[j] = E::put(w * cs.x + u * cs.y);
+    for (int j = 0; j < PAIRS; ++j) {
+      const float2 r = cs[j];
+      T& lo = TWO ? p.v[j % V] : p.v[2 * j % V];
+      T& hi = TWO ? q.v[j % V] : p.v[(2 * j + 1) % V];
+      const float u = E::get(lo), w = E::get(hi);
+      lo = E::put(u * r.x - w * r.y);
+      hi = E::put(w * r.x + u * r.y);
+    }
+  };
+  // Narrow items go several at a time, so that enough is on its way.
+  constexpr int BYTES = V * (int)sizeof(T), U = BYTES >= 8 ? 1 : BYTES == 4 && LAYOUT == QW_ROPE_HALF ? 2 : 4;
+  while (t < tokens) {
+    if constexpr (U == 1) {
+      const T* x = static_cast<const T*>(a.X) + (t0 + t) * a.ldx + (int64_t)head * a.head_dim;
+      T* y = static_cast<T*>(a.Y) + (t0 + t) * a.ldy + (int64_t)head * a.head_dim;
+      if (k >= s.turn) {
+        const int c = a.rot + (k - s.turn) * V;
+        *reinterpret_cast<Vec*>(y + c) = *reinterpret_cast<const Vec*>(x + c);
+      } else {
+        const int c = LAYOUT == QW_ROPE_HALF ? k * V : 2 * k * PAIRS;
+        Vec p = *reinterpret_cast<const Vec*>(x + c), q{};
+        if constexpr (TWO) q = *reinterpret_cast<const Vec*>(x + apart + c);
+        turn(p, q, table + t * half + k * PAIRS);
+        *reinterpret_cast<Vec*>(y + c) = p;
+        if constexpr (TWO) *reinterpret_cast<Vec*>(y + apart + c) = q;
       }
-      *reinterpret_cast<Vec*>(y + c) = p;
-      *reinterpret_cast<Vec*>(y + half + c) = q;
-    } else if constexpr (V == 1) {
-      const float2 cs = table[t * half + k];
-      const float u = E::get(x[2 * k]), w = E::get(x[2 * k + 1]);
-      y[2 * k] = E::put(u * cs.x - w * cs.y);
-      y[2 * k + 1] = E::put(w * cs.x + u * cs.y);
+      advance();
     } else {
-      Vec p = *reinterpret_cast<const Vec*>(x + k * V);
+      Vec p[U], q[U];
+      T* y[U];
+      const float2* cs[U];
+      bool turned[U];
+      int there = 0;
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float2 cs = table[t * half + k * PAIRS + j];
-        const float u = E::get(p.v[2 * j]), w = E::get(p.v[2 * j + 1]);
-        p.v[2 * j] = E::put(u * cs.x - w * cs.y);
-        p.v[2 * j + 1] = E::put(w * cs.x + u * cs.y);
+      for (int i = 0; i < U; ++i) {
+        if (t >= tokens) continue;
+        there = i + 1;
+        turned[i] = k < s.turn;
+        const int c = !turned[i] ? a.rot + (k - s.turn) * V : LAYOUT == QW_ROPE_HALF ? k * V : 2 * k * PAIRS;
+        const T* x = static_cast<const T*>(a.X) + (t0 + t) * a.ldx + (int64_t)head * a.head_dim + c;
+        y[i] = static_cast<T*>(a.Y) + (t0 + t) * a.ldy + (int64_t)head * a.head_dim + c;
+        cs[i] = table + t * half + k * PAIRS;
+        p[i] = *reinterpret_cast<const Vec*>(x);
+        if (TWO && turned[i]) q[i] = *reinterpret_cast<const Vec*>(x + apart);
+        advance();
       }
-      *reinterpret_cast<Vec*>(y + k * V) = p;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (i >= there) continue;
+        if (turned[i]) {
+          turn(p[i], q[i], cs[i]);
+          if (TWO) *reinterpret_cast<Vec*>(y[i] + apart) = q[i];
+        }
+        *reinterpret_cast<Vec*>(y[i]) = p[i];
+      }
     }
   }
 }
 
-template <int TYPE, int LAYOUT>
+template <int TYPE, int LAYOUT, int V>
 qw_status launch(const RopeArgs& a, cudaStream_t st) {
-  constexpr int SIZE = TYPE == QW_T_F32 ? 4 : 2, V = 16 / SIZE;
-  const int part = LAYOUT == QW_ROPE_HALF ? a.rot / 2 : a.rot;
-  const bool wide = ((uintptr_t)a.X | (uintptr_t)a.Y) % 16 == 0 && a.ldx % V == 0 &&
-                    a.ldy % V == 0 && a.head_dim % V == 0 && part % V == 0;
-  const int64_t blocks = (a.T + ROPE_TOKENS - 1) / ROPE_TOKENS;
-  const int64_t items = (int64_t)a.heads * a.head_dim * ROPE_TOKENS / (wide ? V : 1);
-  int64_t split = (items + 2 * ROPE_THREADS - 1) / (2 * ROPE_THREADS);
-  const int64_t most = std::max<int64_t>(1, 2 * device_sm_count() / blocks);
-  split = std::max<int64_t>(1, std::min(split, most));
+  Shape s{a};
+  const int half = a.rot / 2, pairs = LAYOUT == QW_ROPE_HALF ? V : std::max(1, V / 2);
+  s.turn = half / pairs;
+  s.per_head = s.turn + (a.X == a.Y ? 0 : (a.head_dim - a.rot) / V);
+  const int64_t per_token = (int64_t)s.per_head * a.heads;
+  const int64_t sms = device_sm_count();
+  int64_t tokens = std::min<int64_t>(ROPE_ITEMS / per_token, ROPE_TABLE / half);
+  tokens = std::max<int64_t>(1, std::min(tokens, (a.T + 4 * sms - 1) / (4 * sms)));
+  s.tokens = (int32_t)tokens;
+  const int64_t blocks = (a.T + tokens - 1) / tokens;
+  // few tokens: a token's heads are shared out among CTAs
+  const int64_t need = (per_token * tokens + ROPE_THREADS - 1) / ROPE_THREADS;
+  const int64_t split = std::max<int64_t>(1, std::min(need, 2 * sms / blocks));
+  const int64_t step = split * ROPE_THREADS;
+  s.step_heads = (int32_t)(step / s.per_head);
+  s.step_items = (int32_t)(step % s.per_head);
+  s.groups = std::max(1, ROPE_THREADS / half);
+  s.by_half = divisor(half);
+  s.by_head = divisor(s.per_head);
+  s.by_heads = divisor(a.heads);
   const dim3 grid((unsigned)blocks, (unsigned)split);
-  const size_t smem = (size_t)ROPE_TOKENS * (a.rot / 2) * sizeof(float2);
-  return wide ? launch_pdl(rope_kernel<TYPE, LAYOUT, V>, grid, dim3(ROPE_THREADS), smem, st, a)
-              : launch_pdl(rope_kernel<TYPE, LAYOUT, 1>, grid, dim3(ROPE_THREADS), smem, st, a);
+  return launch_pdl(rope_kernel<TYPE, LAYOUT, V>, grid, dim3(ROPE_THREADS),
+                    (size_t)tokens * half * sizeof(float2), st, s);
+}
+
+// the widest access that everything is a multiple of
+template <int TYPE, int LAYOUT, int V>
+qw_status launch_wide(const RopeArgs& a, cudaStream_t st) {
+  constexpr int SIZE = TYPE == QW_T_F32 ? 4 : 2;
+  const int part = LAYOUT == QW_ROPE_HALF ? a.rot / 2 : a.rot;
+  const bool fits = ((uintptr_t)a.X | (uintptr_t)a.Y) % (V * SIZE) == 0 && a.ldx % V == 0 &&
+                    a.ldy % V == 0 && a.head_dim % V == 0 && part % V == 0;
+  if constexpr (V > 1) {
+    if (!fits) return launch_wide<TYPE, LAYOUT, V / 2>(a, st);
+  }
+  return launch<TYPE, LAYOUT, V>(a, st);
 }
 
 template <int TYPE>
 qw_status launch_layout(const RopeArgs& a, int32_t layout, cudaStream_t st) {
-  return layout == QW_ROPE_HALF ? launch<TYPE, QW_ROPE_HALF>(a, st)
-                                : launch<TYPE, QW_ROPE_INTERLEAVED>(a, st);
+  constexpr int V = TYPE == QW_T_F32 ? 4 : 8;
+  return layout == QW_ROPE_HALF ? launch_wide<TYPE, QW_ROPE_HALF, V>(a, st)
+                                : launch_wide<TYPE, QW_ROPE_INTERLEAVED, V>(a, st);
 }
 
 }  // namespace
