@@ -36,7 +36,9 @@ constexpr int WINDOW = 512;  // tokens that an item is taken from
 constexpr int BN = 128;      // columns of a tile
 constexpr int BK = 64;       // k (and r) of a stage: 128 bytes, a swizzle row
 constexpr int SLOT = TT * BK * 2;
-constexpr int EPI_WARP0 = 4, EPI_WARPS = 8, WARPS = EPI_WARP0 + EPI_WARPS, THREADS = 32 * WARPS;
+// warp 0: TMA; warp 1: MMAs and tensor memory; warps 2-9: X's rows, t and the epilogue (warp w may read tensor
+// memory's lanes 32 (w % 4) on).  No warp more: two CTAs an SM then have 96 registers a thread.
+constexpr int EPI_WARP0 = 2, EPI_WARPS = 8, WARPS = EPI_WARP0 + EPI_WARPS, THREADS = 32 * WARPS;
 constexpr int EPI_THREADS = 32 * EPI_WARPS;
 constexpr uint32_t TMEM_COLS = 256;  // D1, and in its place the two buffers of D2
 constexpr int MAX_STAGES = 8;
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     abort_shared = 0;
     fence_barrier_init();
   }
-  if (warp == 2) {
+  if (warp == 1) {
     tmem_alloc(&tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       cp_async_wait<0>();
       if (nk > 0 && ok) ok = warp_wait(&d1_full, ud & 1u, abort_flag, a.err);
       tc_fence_after();
-    } else if (warp == 1) {
+    } else if (warp == 0) {
       if (lane == 0) {
         for (int kb = 0, slot = 0; kb < nk; ++kb) {
           if (!stage1_free(kb)) {
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         load_b(min(uses2, p.s2));
       }
       __syncwarp();
-    } else if (warp == 2) {
+    } else if (warp == 1) {
       const bool leader = elect_one();
       const uint32_t id1 = idesc(p.r16);
       for (int kb = 0, slot = 0; ok && kb < nk; ++kb) {
@@ -592,10 +594,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (warp >= EPI_WARP0) fence_proxy_async_smem();
     __syncthreads();
     // -------------------------------------------------------------- 3: base + B t^T
-    if (warp == 1) {
+    if (warp == 0) {
       if (lane == 0) load_b(uses2);
       __syncwarp();
-    } else if (warp == 2) {
+    } else if (warp == 1) {
       const bool leader = elect_one();
       tc_fence_after();
       const uint32_t id2 = idesc(BN);
@@ -882,7 +884,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
   }
   __syncwarp();
-  if (warp == 2) {  // (after a wait that gave up, MMAs may still run)
+  if (warp == 1) {  // (after a wait that gave up, MMAs may still run)
     if (elect_one()) {
       tc_commit(&final_bar);
       wait_landed(&final_bar, 0);
@@ -891,7 +893,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) {
+  if (warp == 1) {
     tc_fence_after();
     __syncwarp();
     tmem_dealloc(tbase, TMEM_COLS);
