@@ -6,9 +6,11 @@
 //
 // One launch.  An item is up to 128 tokens of one adapter out of a window of 512 (wherever they stand
 // in it); a cluster of CTAs works on an item:
-//   1  D1[token][r] = X A^T over a CTA's slice of K, in stages of 64 k.  A comes by TMA, the listed
-//      tokens' rows by cp.async of the epilogue's warps, which have nothing else to do yet.  (TMA
-//      gather4 copies, four rows each, took 75 cycles apiece, 2400 a stage.)
+//   1  D1[token][r] = X A^T over a CTA's slice of K, in stages of 64 k.  A comes by TMA, and so do tokens
+//      that stand together; other rows by cp.async of the epilogue's warps, which have nothing else to do
+//      yet.  (TMA gather4 copies, four rows each, took 75 cycles apiece, 2400 a stage.)  A warp that copies
+//      nothing puts the fence between those rows and the MMAs: a fence waits for all of its thread's
+//      copies, also those of later stages (0.65 us a stage).
 //   2  t = s_a (sum of the CTAs' D1, in rank order): each CTA fetches its tokens' shares, adds them up
 //      and leaves its tokens' t, which the others fetch; all reads of 256 bytes in a row.  t is held as
 //      BF16 numbers that add up to it, two where results are BF16 (2^-17 t is lost of what the result
@@ -21,8 +23,12 @@
 //      Items of up to 64 or 32 tokens have t's rows twice or four times, so that all warps share the
 //      columns.  (With a column a lane every element costs accesses of its own: 20 instructions an
 //      element, 106 us for 4096 x 14336 x 4096.)
-// B's stages are on their way while t is made.  Every wait on a barrier is bounded; on expiry the kernel
-// reports QW_ERR_TIMEOUT and shuts down.
+// B's stages are on their way while t is made.  Several clusters may share an item's columns, each with a t
+// of its own, where that fills the SMs.  Every wait on a barrier is bounded; on expiry the kernel reports
+// QW_ERR_TIMEOUT and shuts down.
+// Bound by: an item's chain (find 3, X A^T and t 10 to 15, 1.5 us a tile and group) in small calls; in large
+// ones by base and C through shared memory and by what the last clusters leave idle: 4096 x 14336 x 4096, rank
+// 64, 77 us, 288 MB at 3.7 TB/s.
 #include <algorithm>
 
 #include "int8_map.cuh"
@@ -36,30 +42,39 @@ constexpr int WINDOW = 512;  // tokens that an item is taken from
 constexpr int BN = 128;      // columns of a tile
 constexpr int BK = 64;       // k (and r) of a stage: 128 bytes, a swizzle row
 constexpr int SLOT = TT * BK * 2;
-// warp 0: TMA; warp 1: MMAs and tensor memory; warps 2-9: X's rows, t and the epilogue (warp w may read tensor
-// memory's lanes 32 (w % 4) on).  No warp more: two CTAs an SM then have 96 registers a thread.
-constexpr int EPI_WARP0 = 2, EPI_WARPS = 8, WARPS = EPI_WARP0 + EPI_WARPS, THREADS = 32 * WARPS;
-constexpr int EPI_THREADS = 32 * EPI_WARPS;
-constexpr uint32_t TMEM_COLS = 256;  // D1, and in its place the two buffers of D2
+// warp 0: TMA; warp 1: MMAs and tensor memory; warps 2-17: the epilogue, in two groups of eight that take tiles by
+// turns (warp w may read tensor memory's lanes 32 (w % 4) on).  The first group also brings X's rows and
+// makes t.
+constexpr int EPI_WARP0 = 2, GROUP_WARPS = 8, EPI_WARPS = 2 * GROUP_WARPS, WARPS = EPI_WARP0 + EPI_WARPS;
+constexpr int THREADS = 32 * WARPS, GROUP_THREADS = 32 * GROUP_WARPS;
+constexpr uint32_t TMEM_COLS = 512;  // D1 (up to 256), and in its place the buffers of D2
+constexpr int ACCS = 4;
 constexpr int MAX_STAGES = 8;
-// bytes of a row of a TMA box of base and C: 64 columns of BF16, 16 of FP32
-template <bool C32>
-constexpr int kBoxRow = C32 ? 64 : 128;
+constexpr int BOX_ROW = 128;              // bytes of a row of a TMA box of base and C: 64 columns of BF16, 32 of FP32
+constexpr int UNIT_BYTES = 32 * BOX_ROW;  // a box, a warp's unit of base in shared memory
+constexpr int MAX_UNITS = 2;              // of a warp
 constexpr int HASH = 2 * WINDOW;
 constexpr int SEGS = WINDOW / 32;
 
 struct Params {
   LoraArgs a;
   int32_t csize_log;
-  int32_t k_stages;  // of a CTA's slice of K
-  int32_t n_tiles;   // of a CTA's slice of N
-  int32_t r16;       // R, rounded up to 16
-  int32_t r_slots;   // ... to 64, in stages
-  int32_t s2;        // stages of B
+  int32_t parts_log;  // clusters that share an item's columns (each makes t for itself)
+  int32_t k_stages;   // of a CTA's slice of K
+  int32_t n_tiles;    // of a CTA's slice of N
+  int32_t r16;        // R, rounded up to 16
+  int32_t r_slots;    // ... to 64, in stages
+  int32_t s2;         // stages of B
   int32_t t_bytes;
   int32_t ring_bytes;
   int32_t all_bytes;  // t, the ring and the units
+  int32_t units;      // of a warp
   bool wide;           // base and C take 16-byte accesses
+};
+
+// X in boxes of 64 k and 8, 32 or 128 rows
+struct Rows {
+  CUtensorMap map[3];
 };
 
 // kind::f16: FP32 accumulator (bit 4), A = B = BF16 (bits 7, 10), N >> 3 at bit 17, M >> 4 at bit 24
@@ -112,11 +127,6 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
                : "memory");
 }
-// a box on its way to L2
-__device__ __forceinline__ void tma_prefetch_2d(const void* map, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y)
-               : "memory");
-}
 // shared memory to global memory, a box
 __device__ __forceinline__ void tma_store_2d(const void* map, const void* smem_src, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
@@ -127,11 +137,16 @@ __device__ __forceinline__ void tma_store_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 // ... until the stores' sources have been read / until they are done
+template <int N>  // ... but the last N
 __device__ __forceinline__ void tma_store_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void tma_store_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// an arrival of this thread on `bar` when its copies so far are there (counted in the barrier's number)
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -218,12 +233,13 @@ struct Plan {
 };
 
 template <bool C32>
-__global__ void __launch_bounds__(THREADS, 2)
-    lora_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+__global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they are shared out by four)
+    lora_tc_kernel(const __grid_constant__ Rows tmX, const __grid_constant__ CUtensorMap tmA,
+                   const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmBase, const __grid_constant__ CUtensorMap tmC,
                    const __grid_constant__ CUtensorMap tmC8,
                    const __grid_constant__ Params p) {
-  constexpr int NS = C32 ? 3 : 2, SIZE = C32 ? 4 : 2, UNIT_BYTES = 32 * kBoxRow<C32>;
+  constexpr int NS = C32 ? 3 : 2, SIZE = C32 ? 4 : 2;
   using T = std::conditional_t<C32, float, uint16_t>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (0u - smem_u32(smem_raw) & 1023u);  // (stays a shared address)
@@ -232,8 +248,8 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint8_t* const ring1 = smem;  // the first product's stages reach over t's place
   uint8_t* const s_unit = ring2 + p.ring_bytes;
   __shared__ Plan plan;
-  __shared__ uint64_t full1[MAX_STAGES], empty1[MAX_STAGES], full2[MAX_STAGES], empty2[MAX_STAGES];
-  __shared__ uint64_t d1_full, acc_full[2], acc_empty[2], base_full[EPI_WARPS], final_bar;
+  __shared__ uint64_t full1[MAX_STAGES], empty1[MAX_STAGES], landed[MAX_STAGES], full2[MAX_STAGES], empty2[MAX_STAGES];
+  __shared__ uint64_t d1_full, acc_full[ACCS], acc_empty[ACCS], base_full[EPI_WARPS][MAX_UNITS], final_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_shared;
   volatile int* abort_flag = &abort_shared;
@@ -241,22 +257,25 @@ __global__ void __launch_bounds__(THREADS, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int csize_log = p.csize_log, csize = 1 << csize_log;
   const int crank = (int)(blockIdx.x & (unsigned)(csize - 1));
-  const int64_t m0 = (int64_t)(blockIdx.x >> csize_log) * WINDOW;
+  const unsigned cluster = blockIdx.x >> csize_log;
+  const int64_t m0 = (int64_t)(cluster >> p.parts_log) * WINDOW;
+  const int share = (int)(cluster & ((1u << p.parts_log) - 1u)) * csize + crank;  // of the columns
   const int win = (int)min64(WINDOW, a.M - m0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
-      mbar_init(&full1[s], 1 + EPI_WARPS);  // A's copy and the warps that bring X
+      mbar_init(&full1[s], 2);  // A and X
+      mbar_init(&landed[s], GROUP_THREADS);
       mbar_init(&empty1[s], 1);
       mbar_init(&full2[s], 1);
       mbar_init(&empty2[s], 1);
     }
     mbar_init(&d1_full, 1);
-    for (int w = 0; w < EPI_WARPS; ++w) mbar_init(&base_full[w], 1);
+    for (int w = 0; w < EPI_WARPS * MAX_UNITS; ++w) mbar_init(&base_full[0][0] + w, 1);
     mbar_init(&final_bar, 1);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < ACCS; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], EPI_WARPS);
+      mbar_init(&acc_empty[b], GROUP_WARPS);
     }
     abort_shared = 0;
     fence_barrier_init();
@@ -335,16 +354,18 @@ __global__ void __launch_bounds__(THREADS, 2)
   __syncthreads();
 
   const int64_t all_tiles = ((int64_t)a.N + BN - 1) / BN;
-  const int tile0 = (int)min64(all_tiles, (int64_t)crank * p.n_tiles);
+  const int tile0 = (int)min64(all_tiles, (int64_t)share * p.n_tiles);
   const int tiles = (int)min64(p.n_tiles, all_tiles - tile0);
   const int all_k = (a.K + BK - 1) / BK;
   const int kb0 = min(all_k, crank * p.k_stages), nk = min(p.k_stages, all_k - kb0);
-  const int e = (int)threadIdx.x - 32 * EPI_WARP0, ew = warp - EPI_WARP0;  // of the epilogue
-  const int quad = warp & 3, half = ew >> 2;
+  const int ew = warp - EPI_WARP0, group = ew >> 3;                      // of the epilogue (its first group: `worker`)
+  const int e = ((int)threadIdx.x - 32 * EPI_WARP0) & (GROUP_THREADS - 1);  // of its group
+  const bool worker = warp >= EPI_WARP0 && group == 0;
+  const int quad = warp & 3, half = (ew & 7) >> 2;
   // uses so far of the first product's barriers, of D1 and of the D2 buffers (all roles count alike), and
   // the next slot of B's ring and its phase (its two roles count alike)
-  uint32_t u1 = 0, ud = 0, ua = 0, slot2 = 0, phase2 = 0;
-  uint32_t base_phase = 0;  // of this warp's boxes of base
+  uint32_t u1 = 0, ux = 0, ud = 0, ua = 0, slot2 = 0, phase2 = 0;  // (ux: of `landed`)
+  uint32_t base_phase = 0;  // of this warp's units of base, a bit each
 
   for (int item = (int)blockIdx.y; item < plan.total; item += (int)gridDim.y) {
     // -------------------------------------------------------------- the item's tokens
@@ -387,7 +408,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     // The first product's stages, over all of the shared memory, hold the item's tokens and A; the MMA's other
     // rows are whatever lies behind.
     // Their barriers are used in turn, eight of them, whatever the number of stages.
-    const int x_bytes = (now + 7) / 8 * 1024, stage1 = x_bytes + p.r16 * BK * 2;
+    const bool together = plan.row[now - 1] - plan.row[0] == now - 1;
+    const int x_map = now <= 8 ? 0 : now <= 32 ? 1 : 2;
+    const int x_bytes = together ? 1024 << (2 * x_map) : (now + 7) / 8 * 1024, stage1 = x_bytes + p.r16 * BK * 2;
     const int s1 = min(MAX_STAGES, (p.all_bytes - max(SLOT, stage1)) / stage1 + 1);  // (an MMA reads SLOT)
     // t has the tokens' rows 128 / span times
     const int span_log = now <= 32 ? 5 : now <= 64 ? 6 : 7, span = 1 << span_log;
@@ -415,31 +438,37 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (++b_slot == slots) b_slot = 0, ++b_tile;
       }
     };
-    auto prefetch_base = [&](int tile, int who) {  // a line of the tile's base per thread
-      const int token = who >> 1;
+    auto prefetch_base = [&](int tile) {  // a line of the tile's base per thread of a group
+      const int token = e >> 1;
       if (tile >= tiles || token >= now || !a.base) return;
-      const int32_t n = (tile0 + tile) * BN + (who & 1) * (BN / 2);
+      const int32_t n = (tile0 + tile) * BN + (e & 1) * (BN / 2);
       const uint8_t* b = static_cast<const uint8_t*>(a.base) + plan.off_b[token];
       if (n < a.N) prefetch_l2(b + (int64_t)n * SIZE);
       if (C32 && n + 32 < a.N) prefetch_l2(b + (int64_t)(n + 32) * SIZE);
     };
 
     // -------------------------------------------------------------- 1: X A^T
-    if (warp >= EPI_WARP0) {
-      prefetch_base(0, e);
-      prefetch_base(1, e);
-      // The listed rows, eight threads a row of a stage.  A stage is handed over when the next ones' copies
-      // have been started.
-      const int ahead = s1 == 8 ? 7 : min(s1 - 1, 3);
-      const uint16_t* x[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = (e >> 3) + 32 * q;
-        x[q] = a.X + (m0 + (row < now ? plan.row[row] : 0)) * a.ldx + (e & 7) * 8;
+    if (warp >= EPI_WARP0 && !worker) {
+      for (int i = 0; i < 4; ++i) prefetch_base(i);
+      for (int kb = 0; ew == GROUP_WARPS && !together && kb < nk; ++kb) {
+        const uint32_t u = ux + (uint32_t)kb;
+        if (!warp_wait(&landed[u % MAX_STAGES], u / MAX_STAGES & 1u, abort_flag, a.err)) {
+          ok = false;
+          break;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full1[(u1 + (uint32_t)kb) % MAX_STAGES]);
       }
-      int slot = 0;
-      for (int kb = 0; kb < nk + ahead; ++kb) {
-        if (kb < nk) {
+    } else if (worker) {
+      if (!together) {  // the listed rows, eight threads a row of a stage
+        const uint16_t* x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = (e >> 3) + 32 * q;
+          x[q] = a.X + (m0 + (row < now ? plan.row[row] : 0)) * a.ldx + (e & 7) * 8;
+        }
+        for (int kb = 0, slot = 0; kb < nk; ++kb) {
           if (!__all_sync(0xFFFFFFFFu, stage1_free(kb))) {
             ok = false;
             break;
@@ -451,16 +480,9 @@ __global__ void __launch_bounds__(THREADS, 2)
           for (int q = 0; q < 4; ++q)
             if ((e >> 3) + 32 * q < now) cp_async16(to + q * 32 * 128, in ? x[q] + k : a.X, in ? 16 : 0);
           if (++slot == s1) slot = 0;
-        }
-        cp_async_commit();
-        if (kb >= ahead) {
-          cp_async_wait_upto(ahead);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full1[(u1 + (uint32_t)(kb - ahead)) % MAX_STAGES]);
+          cp_async_arrive(&landed[(ux + (uint32_t)kb) % MAX_STAGES]);
         }
       }
-      cp_async_wait<0>();
       if (nk > 0 && ok) ok = warp_wait(&d1_full, ud & 1u, abort_flag, a.err);
       tc_fence_after();
     } else if (warp == 0) {
@@ -474,6 +496,10 @@ __global__ void __launch_bounds__(THREADS, 2)
           mbar_arrive_expect_tx(bar, (uint32_t)(p.r16 * BK * 2));
           tma_load_2d(ring1 + slot * stage1 + x_bytes, &tmA, bar, (kb0 + kb) * BK,
                       (int32_t)((int64_t)id * a.R));
+          if (together) {
+            mbar_arrive_expect_tx(bar, (uint32_t)x_bytes);
+            tma_load_2d(ring1 + slot * stage1, &tmX.map[x_map], bar, (kb0 + kb) * BK, (int32_t)m0 + plan.row[0]);
+          }
           if (++slot == s1) slot = 0;
         }
         // the first of B's stages take the place of the first product's as soon as that has read them
@@ -508,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     // -------------------------------------------------------------- 2: t
     const float scale = a.scales ? a.scales[id] : 1.f;
     const int token = 32 * quad + lane;
-    if (warp >= EPI_WARP0) {
+    if (worker) {
       for (int r = half * (p.r16 / 2); r < (half + 1) * (p.r16 / 2); r += 8) {
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (nk > 0) {
@@ -540,10 +566,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         float v[MOST][4];
 #pragma unroll
         for (int q = 0; q < MOST; ++q) {
-          const int i = e + q * EPI_THREADS, r = (i >> each_log) * 4, mine = crank * each + (i & (each - 1));
+          const int i = e + q * GROUP_THREADS, r = (i >> each_log) * 4, mine = crank * each + (i & (each - 1));
           const uint32_t at = smem_u32(s_t) + (uint32_t)((i >> each_log) * TT + mine) * 16;
           float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (warp >= EPI_WARP0 && i < n4 && mine < now) {
+          if (worker && i < n4 && mine < now) {
             uint4 x[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) x[c] = c < csize ? ld_cluster_u32x4(mapa_shared(at, c)) : zero4();
@@ -561,16 +587,16 @@ __global__ void __launch_bounds__(THREADS, 2)
         cluster_sync();  // all sums have been read
 #pragma unroll
         for (int q = 0; q < MOST; ++q) {
-          const int i = e + q * EPI_THREADS, mine = crank * each + (i & (each - 1));
-          if (warp >= EPI_WARP0 && i < n4 && mine < now) put_t<NS>(s_t, p.r_slots, mine, (i >> each_log) * 4, v[q]);
+          const int i = e + q * GROUP_THREADS, mine = crank * each + (i & (each - 1));
+          if (worker && i < n4 && mine < now) put_t<NS>(s_t, p.r_slots, mine, (i >> each_log) * 4, v[q]);
         }
       };
-      if (n4 <= EPI_THREADS)
+      if (n4 <= GROUP_THREADS)
         join(std::integral_constant<int, 1>{});
       else
-        join(std::integral_constant<int, TT * 256 / 4 / 4 / EPI_THREADS>{});  // (two CTAs with 128 r, or four)
+        join(std::integral_constant<int, TT * 256 / 4 / 4 / GROUP_THREADS>{});  // (two CTAs with 128 r, or four)
       cluster_sync();
-      if (warp >= EPI_WARP0) {  // the tokens' rows to all their places, eight threads a row
+      if (worker) {  // the tokens' rows to all their places, eight threads a row
         const int chunk = (e & 7) ^ (e >> 3 & 7);  // (rows 32 apart are swizzled alike)
         for (int s = 0, in_r = 0; s < NS * p.r_slots; ++s, in_r = in_r + 1 == p.r_slots ? 0 : in_r + 1) {
           if (in_r * BK + chunk * 8 >= p.r16) continue;
@@ -591,7 +617,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
       }
     }
-    if (warp >= EPI_WARP0) fence_proxy_async_smem();
+    if (worker) fence_proxy_async_smem();
     __syncthreads();
     // -------------------------------------------------------------- 3: base + B t^T
     if (warp == 0) {
@@ -604,8 +630,8 @@ __global__ void __launch_bounds__(THREADS, 2)
       const uint64_t dt = smem_desc(smem_u32(s_t), 16, 1024, 2);
       const int odd = rank % 16;
       for (int i = 0; ok && i < tiles; ++i) {
-        const uint32_t v = ua + (uint32_t)i, buf = v & 1u;
-        if (!warp_wait(&acc_empty[buf], (v >> 1 & 1u) ^ 1u, abort_flag, a.err)) {
+        const uint32_t v = ua + (uint32_t)i, buf = v % ACCS;
+        if (!warp_wait(&acc_empty[buf], (v / ACCS & 1u) ^ 1u, abort_flag, a.err)) {
           ok = false;
           break;
         }
@@ -632,11 +658,13 @@ __global__ void __launch_bounds__(THREADS, 2)
           const uint64_t db = smem_desc(smem_u32(at), 16, 1024, 2);
           const int steps = min(BK / 16, (rank - q * BK + 15) / 16);
           if (leader) {
+#pragma unroll
             for (int w = 0; w < NS; ++w) {
               const uint64_t d = dt + (uint32_t)((w * p.r_slots + q) * (SLOT >> 4));
-              for (int j = 0; j < steps; ++j)
-                tc_mma_f16(tbase + buf * BN, d + 2 * j, db + 2 * j, id2,
-                           q != 0 || w != 0 || j != 0 ? 1u : 0u);
+#pragma unroll
+              for (int j = 0; j < BK / 16; ++j)
+                if (j < steps)
+                  tc_mma_f16(tbase + buf * BN, d + 2 * j, db + 2 * j, id2, q != 0 || w != 0 || j != 0 ? 1u : 0u);
             }
             tc_commit(&empty2[slot2]);
           }
@@ -654,21 +682,23 @@ __global__ void __launch_bounds__(THREADS, 2)
       const int width = 64 >> (7 - span_log), col0 = ((32 * quad >> span_log) * 2 + half) * width;
       const int cols = min(width, C32 ? 16 : 32), cols_log = cols == 32 ? 5 : 4;
       const int per_log = (span_log - 1) - cols_log;  // units of a tile
-      const int units = count > 0 ? tiles << per_log : 0, last = (1 << per_log) - 1;
+      const int my_tiles = (tiles + 1 - group) >> 1;  // tiles group, group + 2, ...
+      const int units = count > 0 ? my_tiles << per_log : 0, last = (1 << per_log) - 1;
       int rows_log = 3;
       while (rows_log < 5 && 1 << rows_log < count) ++rows_log;
       const int row_log = cols_log + (C32 ? 2 : 1);        // bytes of a unit's row: 64 or 32
       const int pieces_log = row_log - 4;                   // in pieces of 16 bytes
-      const int depth = min(8, UNIT_BYTES >> (rows_log + row_log));
+      int depth = 1;  // (a power of two)
+      while (depth < 8 && 2 * depth << (rows_log + row_log) <= p.units * UNIT_BYTES) depth *= 2;
       constexpr int EACH = 16 / SIZE;                       // elements of a piece
-      uint8_t* const mine = s_unit + ew * UNIT_BYTES;
+      uint8_t* const mine = s_unit + ew * p.units * UNIT_BYTES;
       // where piece j of row r lies: eight neighbouring rows' pieces j are in different banks
       auto piece = [&](int r, int j) {
         return (r << row_log) + ((j ^ (pieces_log == 2 ? r >> 1 : r >> 2)) & ((1 << pieces_log) - 1)) * 16;
       };
       auto place = [&](int unit) { return mine + ((unit & (depth - 1)) << (rows_log + row_log)); };
       auto column = [&](int unit) {
-        return (tile0 + (unit >> per_log)) * BN + col0 + ((unit & last) << cols_log);
+        return (tile0 + 2 * (unit >> per_log) + group) * BN + col0 + ((unit & last) << cols_log);
       };
       const int row1 = lane >> pieces_log, piece1 = lane & ((1 << pieces_log) - 1), rows1 = 32 >> pieces_log;
       auto load = [&](int unit) {
@@ -744,42 +774,44 @@ __global__ void __launch_bounds__(THREADS, 2)
       // box of 32 rows, or boxes of 8 and what is left in pieces.
       const bool boxes = p.wide && span == TT && count > 0 && plan.row[t0 + count - 1] - plan.row[t0] == count - 1;
       if (boxes) {
-        constexpr int COLS = kBoxRow<C32> / SIZE, PER = 64 / COLS;  // columns of a box, boxes of a tile
+        constexpr int COLS = BOX_ROW / SIZE, PER = 64 / COLS;  // columns of a box, boxes of a tile
         const int32_t y = (int32_t)m0 + plan.row[t0];
-        uint64_t* const bar = &base_full[ew];
-        auto fetch = [&](int unit) {  // (one lane)
-          const int32_t n = (tile0 + unit / PER) * BN + col0 + unit % PER * COLS;
-          if (unit >= tiles * PER || n >= a.N || !a.base) return;
-          mbar_arrive_expect_tx(bar, UNIT_BYTES);
-          tma_load_2d(mine, &tmBase, bar, n, y);
+        const bool leader = elect_one();
+        auto fetch = [&](int unit, int slot) {  // (the warp; its leader asks)
+          const int32_t n = (tile0 + 2 * (unit / PER) + group) * BN + col0 + unit % PER * COLS;
+          if (unit >= my_tiles * PER || n >= a.N || !a.base) return;
+          if (leader) {
+            mbar_arrive_expect_tx(&base_full[ew][slot], UNIT_BYTES);
+            tma_load_2d(mine + slot * UNIT_BYTES, &tmBase, &base_full[ew][slot], n, y);
+          }
+          __syncwarp();
         };
         fence_proxy_async_smem();  // (an item before may have written the place in pieces)
         __syncwarp();
-        auto ahead = [&](int tile) {  // (one lane) a tile's boxes on their way to L2
-          for (int u = 0; u < PER; ++u) {
-            const int32_t n = (tile0 + tile) * BN + col0 + u * COLS;
-            if (tile < tiles && n < a.N && a.base) tma_prefetch_2d(&tmBase, n, y);
-          }
-        };
-        if (lane == 0) {
-          fetch(0);
-          ahead(1), ahead(2);
-        }
-        for (int i = 0; i < tiles; ++i) {
-          const uint32_t v = ua + (uint32_t)i, buf = v & 1u;
-          if (lane == 0) ahead(i + 3);
-          if (ok) ok = warp_wait(&acc_full[buf], v >> 1 & 1u, abort_flag, a.err);
+        for (int d = 0; d < p.units; ++d) fetch(d, d);
+        int slot = 0;
+        for (int k = 0; k < my_tiles; ++k) {
+          const uint32_t v = ua + (uint32_t)(2 * k + group), buf = v % ACCS;
+          if (ok) ok = warp_wait(&acc_full[buf], v / ACCS & 1u, abort_flag, a.err);
           tc_fence_after();
 #pragma unroll 1
           for (int u = 0; u < PER; ++u) {
-            const int32_t n = (tile0 + i) * BN + col0 + u * COLS;
-            if (n >= a.N) break;
-            if (a.base) {
-              if (ok) ok = warp_wait(bar, base_phase, abort_flag, a.err);
-              base_phase ^= 1u;
+            const int32_t n = (tile0 + 2 * k + group) * BN + col0 + u * COLS;
+            if (n >= a.N) {
+              if (u == PER - 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (leader) mbar_arrive(&acc_empty[buf]);
+              }
+              continue;
             }
-            uint8_t* const at = mine + lane * kBoxRow<C32>;
-            const int sw = C32 ? lane >> 1 & 3 : lane & 7;  // the box's swizzle
+            if (a.base) {
+              if (ok) ok = warp_wait(&base_full[ew][slot], base_phase >> slot & 1u, abort_flag, a.err);
+              base_phase ^= 1u << slot;
+            }
+            uint8_t* const box = mine + slot * UNIT_BYTES;
+            uint8_t* const at = box + lane * BOX_ROW;
+            const int sw = lane & 7;  // the box's swizzle
             constexpr int STEP = COLS < 32 ? COLS : 32;
 #pragma unroll 1
             for (int c = 0; c < COLS; c += STEP) {
@@ -790,18 +822,23 @@ __global__ void __launch_bounds__(THREADS, 2)
               for (int j = 0; j < STEP / EACH; ++j)
                 was[j] = a.base ? *reinterpret_cast<const uint4*>(at + (((c / EACH + j) ^ sw) << 4)) : zero4();
               tc_landed(d);
+              if (u == PER - 1 && c + STEP == COLS) {  // D2 has been read
+                tc_fence_before();
+                __syncwarp();
+                if (leader) mbar_arrive(&acc_empty[buf]);
+              }
 #pragma unroll
               for (int j = 0; j < STEP / EACH; ++j)
                 *reinterpret_cast<uint4*>(at + (((c / EACH + j) ^ sw) << 4)) = add_piece<C32>(was[j], d + j * EACH);
             }
             const int eights = count / 8;
             if (count < 32) {
-              constexpr int PIECES = kBoxRow<C32> / 16;
+              constexpr int PIECES = BOX_ROW / 16;
               __syncwarp();
               for (int q = 8 * eights * PIECES + lane; q < count * PIECES; q += 32) {
                 const int r = q / PIECES, j = q % PIECES, left = a.N - n - j * EACH;
                 const uint4 x = *reinterpret_cast<const uint4*>(
-                    mine + r * kBoxRow<C32> + ((j ^ (C32 ? r >> 1 & 3 : r & 7)) << 4));
+                    box + r * BOX_ROW + ((j ^ (r & 7)) << 4));
                 put_piece<C32>(static_cast<uint8_t*>(a.C) + plan.off_c[t0 + r] + (int64_t)(n + j * EACH) * SIZE, x,
                                left);
               }
@@ -809,29 +846,35 @@ __global__ void __launch_bounds__(THREADS, 2)
             fence_proxy_async_smem();
             __syncwarp();
             if (count == 32) {
-              if (lane == 0 && ok) tma_store_2d(&tmC, mine, n, y);
+              if (leader && ok) tma_store_2d(&tmC, box, n, y);
             } else if (lane < eights && ok) {
-              tma_store_2d(&tmC8, mine + lane * 8 * kBoxRow<C32>, n, y + 8 * lane);
+              tma_store_2d(&tmC8, box + lane * 8 * BOX_ROW, n, y + 8 * lane);
             }
             tma_store_commit();
-            tma_store_read();
-            __syncwarp();
-            if (lane == 0) fetch(i * PER + u + 1);
+            // The place is asked for again when the store has read it: with more than one, a unit later.
+            const int unit = k * PER + u;
+            if (p.units == 1) {
+              tma_store_read<0>();
+              __syncwarp();
+              fetch(unit + 1, 0);
+            } else {
+              tma_store_read<1>();
+              __syncwarp();
+              if (unit > 0) fetch(unit - 1 + p.units, slot == 0 ? p.units - 1 : slot - 1);
+              if (++slot == p.units) slot = 0;
+            }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
         tma_store_done();
         __syncwarp();
       } else {
         for (int d = 0; d < depth; ++d) load(d);
-        for (int i = 0; i < tiles; ++i) {
-          const uint32_t v = ua + (uint32_t)i, buf = v & 1u;
-          prefetch_base(i + 2, e);
-          if (ok) ok = warp_wait(&acc_full[buf], v >> 1 & 1u, abort_flag, a.err);
+        for (int k = 0; k < my_tiles; ++k) {
+          const uint32_t v = ua + (uint32_t)(2 * k + group), buf = v % ACCS;
+          prefetch_base(2 * k + group + 4);
+          if (ok) ok = warp_wait(&acc_full[buf], v / ACCS & 1u, abort_flag, a.err);
           tc_fence_after();
-          for (int unit = i << per_log; unit < min(units, (i + 1) << per_log); ++unit) {
+          for (int unit = k << per_log; unit < min(units, (k + 1) << per_log); ++unit) {
             cp_async_wait_upto(depth - 1);
             __syncwarp();  // the unit's base is there
             uint8_t* at = place(unit);
@@ -863,6 +906,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
     }
     u1 += (uint32_t)nk;
+    if (!together) ux += (uint32_t)nk;
     ud += nk > 0 ? 1u : 0u;
     ua += (uint32_t)tiles;
     if (warp >= EPI_WARP0) fence_proxy_async_smem();  // (the units' place is the next item's first stages')
@@ -874,15 +918,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int i = (int)(blockIdx.y + gridDim.y * warp); i < win; i += (int)gridDim.y * WARPS)
       if (plan.ids[i] == -1) copy_row<C32>(a, p.wide, m0 + i, n0, n1);
   }
-  // After a wait that gave up, copies may still be under way to the rings (both roles' in the first, which
-  // may lack the other's: bounded).
-  if (*abort_flag && threadIdx.x == 0) {
-    const uint64_t t0 = globaltimer_ns();
-    for (int s = 0; s < MAX_STAGES; ++s)
-      for (uint64_t* bar : {&full1[s], &full2[s], &base_full[s]})
-        while ((!mbar_try_wait(bar, 0) || !mbar_try_wait(bar, 1)) && globaltimer_ns() - t0 < kWaitLimitNs) {
-        }
-  }
+  // After a wait that gave up, copies may still be under way to the rings: they have this long.
+  if (*abort_flag && threadIdx.x == 0)
+    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < kWaitLimitNs / 100;) {
+    }
   __syncwarp();
   if (warp == 1) {  // (after a wait that gave up, MMAs may still run)
     if (elect_one()) {
@@ -900,8 +939,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 }
 
-constexpr int kSmemCta = 232448;         // of one CTA
-constexpr int kSmemHalf = 233472 / 2 - 1024;  // of each of two on an SM
+constexpr int kSmemCta = 232448;  // of one CTA
 
 template <bool C32>
 qw_status launch(const LoraArgs& a, cudaStream_t st) {
@@ -923,52 +961,56 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   p.r_slots = (a.R + BK - 1) / BK;
   p.t_bytes = NS * p.r_slots * SLOT;
   const int stage1 = SLOT + p.r16 * BK * 2;
-  // two CTAs an SM where two of B's stages fit
-  constexpr int UNITS = EPI_WARPS * 32 * kBoxRow<C32>;
-  int room = kSmemHalf - fixed - 1024 - p.t_bytes - UNITS;
-  const bool two = room >= 2 * SLOT;
-  if (!two) room = kSmemCta - fixed - 1024 - p.t_bytes - UNITS;
+  constexpr int UNITS = EPI_WARPS * UNIT_BYTES;
+  const int all = kSmemCta - fixed - 1024 - p.t_bytes;
+  p.units = std::max(1, std::min(MAX_UNITS, (all - 2 * SLOT) / UNITS));
+  const int room = all - p.units * UNITS;
   p.ring_bytes = std::min(room, MAX_STAGES * SLOT) / 1024 * 1024;
   p.s2 = std::min(MAX_STAGES, p.ring_bytes / SLOT);
-  p.all_bytes = p.t_bytes + p.ring_bytes + UNITS;
-  if (p.all_bytes / stage1 < 2 || p.s2 < 2) return QW_ERR_UNSUPPORTED;
-  // The cheapest cluster, in rounds of what runs at once (about 90 % of it: a cluster lies within one GPC) of
-  // what an item takes: to find and, shared, to join (cycles 8000 and 15000), and each CTA's share of the
-  // stages (1000 each) and tiles (4400).  About a fifth of the items are parts of 128 tokens; in small calls
-  // each adapter has one of its own.  (us with clusters of 2, 4 and 8: 4096 x 14336 x 4096 rank 64 185, 103,
-  // [87]; 8192 x 4096 x 4096 rank 128 [84], 92, 135; 256 tokens of 64 adapters, 4096 x 4096 rank 32 50, [34], 43.)
-  const double items = (double)((a.M + TT - 1) / TT) * 1.25 + 1 + (a.M <= WINDOW ? std::min<int64_t>(a.L, a.M) : 0);
-  const double at_once = sms * (two ? 2 : 1) * 0.9;
+  p.all_bytes = p.t_bytes + p.ring_bytes + p.units * UNITS;
+  if (p.all_bytes / stage1 < 2 || p.s2 < 1) return QW_ERR_UNSUPPORTED;
+  // The cheapest cluster and number of clusters on an item's columns, in rounds of what runs at once (a cluster
+  // lies within one GPC) of what an item takes, in us: to find, to join, each CTA's stages and tiles.  What is past
+  // one round starts late.  The items: 128 tokens each, and a part of that for each adapter.  (us measured,
+  // cluster x clusters: 4096 x 14336 x 4096 rank 64 in runs of 8 adapters 2x1 98, 4x1 83, [2x2] 77, 8x1 100;
+  // 2048 mixed tokens of 8, 4096 x 4096 rank 16 2x1 46, [4x1] 31, 2x2 34, 8x1 54; 256 tokens of 64, rank 32 1x1 48,
+  // [2x1] 33, 4x1 42; 128 of one, rank 64 4x1 30, 8x1 21, 8x2 17.)
+  const double items = (double)((a.M + TT - 1) / TT) + 1 + std::min<int64_t>(a.L, a.M);
   double least = 1e30;
-  for (int log = 0; log <= 3; ++log) {
-    const int64_t c = (int64_t)1 << log;
-    if ((c > 1 && c > all_k && c > all_tiles) || (c == 2 && a.R > 128)) continue;
-    const double cost = std::max(1.0, items * c / at_once) *
-                        (8000.0 + (c > 1 ? 15000 : 0) + (all_k + c - 1) / c * 1000.0 + (all_tiles + c - 1) / c * 4400.0);
-    if (cost < least) least = cost, p.csize_log = log;
-  }
+  for (int log = 0; log <= 3; ++log)
+    for (int parts = 0; parts <= 3; ++parts) {
+      const int64_t c = (int64_t)1 << log, shares = c << parts;
+      if ((c > 1 && c > all_k && c > all_tiles) || (c == 2 && a.R > 128) || (parts > 0 && shares > all_tiles)) continue;
+      const double rounds = items * shares / (sms * (c == 8 ? 0.79 : c == 4 ? 0.9 : 1.0));
+      const double cost = (rounds <= 1 ? 1 : rounds + 0.25) * (6 + (c > 1 ? 5 : 0) + (all_k + c - 1) / c * 0.3 +
+                                                               (all_tiles + shares - 1) / shares * 1.7);
+      if (cost < least) least = cost, p.csize_log = log, p.parts_log = parts;
+    }
   const int csize = 1 << p.csize_log;
   p.k_stages = (int32_t)((all_k + csize - 1) / csize);
-  p.n_tiles = (int32_t)((all_tiles + csize - 1) / csize);
+  const int shares = csize << p.parts_log;
+  p.n_tiles = (int32_t)((all_tiles + shares - 1) / shares);
   const int vec = C32 ? 4 : 8;
   p.wide = ((uintptr_t)a.C | (uintptr_t)a.base) % 16 == 0 && a.ldc % vec == 0 &&
            (!a.base || a.ld_base % vec == 0);
   CUtensorMap tmA, tmB;
+  Rows tmX;
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   if (!encode_int8_2d(&tmA, bf16, a.A, a.K, (uint64_t)a.L * a.R, (uint64_t)a.K * 2, BK, p.r16) ||
       !encode_int8_2d(&tmB, bf16, a.B, a.R, (uint64_t)a.L * a.N, (uint64_t)a.R * 2, BK, BN))
     return QW_ERR_CUDA;
+  for (int i = 0; i < 3; ++i)
+    if (!encode_int8_2d(&tmX.map[i], bf16, a.X, a.K, a.M, (uint64_t)a.ldx * 2, BK, 8u << (2 * i))) return QW_ERR_CUDA;
   CUtensorMap tmBase{}, tmC[2]{};
   if (p.wide) {
     const auto type = C32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf16;
-    const auto swizzle = C32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     constexpr int SIZE = C32 ? 4 : 2;
-    constexpr uint32_t cols = kBoxRow<C32> / SIZE, rows[2] = {32, 8};
+    constexpr uint32_t cols = BOX_ROW / SIZE, rows[2] = {32, 8};
     for (int i = 0; i < 2; ++i)
-      if (!encode_int8_2d(&tmC[i], type, a.C, a.N, a.M, (uint64_t)a.ldc * SIZE, cols, rows[i], swizzle))
+      if (!encode_int8_2d(&tmC[i], type, a.C, a.N, a.M, (uint64_t)a.ldc * SIZE, cols, rows[i]))
         return QW_ERR_CUDA;
     if (a.base &&
-        !encode_int8_2d(&tmBase, type, a.base, a.N, a.M, (uint64_t)a.ld_base * SIZE, cols, 32, swizzle))
+        !encode_int8_2d(&tmBase, type, a.base, a.N, a.M, (uint64_t)a.ld_base * SIZE, cols, 32))
       return QW_ERR_CUDA;
   }
   static std::atomic<int> ready[64];
@@ -977,13 +1019,13 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
                                     kSmemCta - fixed) == cudaSuccess;
       }) <= 0)
     return QW_ERR_CUDA;
-  const int64_t x = windows * csize;
+  const int64_t x = windows * shares;
   const int64_t y = std::max<int64_t>(1, std::min<int64_t>(most, (4 * sms + x - 1) / x));
   if (x > 0x7FFFFFFF) return QW_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)x, (unsigned)y);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = (size_t)(1024 + p.t_bytes + p.ring_bytes + UNITS);
+  cfg.dynamicSmemBytes = (size_t)(1024 + p.all_bytes);
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -993,7 +1035,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = csize > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, lora_tc_kernel<C32>, tmA, tmB, tmBase, tmC[0], tmC[1], p) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, lora_tc_kernel<C32>, tmX, tmA, tmB, tmBase, tmC[0], tmC[1], p) == cudaSuccess
              ? QW_OK
              : QW_ERR_CUDA;
 }
@@ -1004,7 +1046,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
 // 128 ranks leaves the rings no room.
 bool lora_tc_takes(const LoraArgs& a, bool c_f32) {
   return (int64_t)a.L * a.R <= kInt8MaxN && (int64_t)a.L * a.N <= kInt8MaxN &&
-         a.ldc < ((int64_t)1 << 37) && a.ld_base < ((int64_t)1 << 37) && !(c_f32 && a.R > 128);
+         a.ldx < ((int64_t)1 << 38) && a.ldc < ((int64_t)1 << 37) && a.ld_base < ((int64_t)1 << 37) && !(c_f32 && a.R > 128);
 }
 
 qw_status launch_lora_tc(const LoraArgs& a, bool c_f32, cudaStream_t st) {
