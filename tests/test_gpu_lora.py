@@ -127,6 +127,39 @@ def test_shapes(M, N, K, L, R, c, runs):
     run_and_check(M, N, K, L, R, c, M + N, runs, in_place=runs)
 
 
+# more adapters than tokens of a window, ranks past 128, windows of 512 tokens and their last few, few columns
+# and many, K of one stage and of many
+MORE = [(1100, 600, 640, 700, 16), (513, 264, 264, 2, 200), (40, 136, 64, 1, 256), (1023, 8, 136, 2, 40),
+        (515, 1000, 1032, 1, 64), (2048, 520, 264, 40, 40), (130, 9000, 64, 1, 16), (700, 4096, 4096, 1, 64),
+        (520, 130, 8, 5, 136), (257, 2000, 2048, 6, 8)]
+
+
+@pytest.mark.parametrize("M,N,K,L,R", MORE)
+@pytest.mark.parametrize("c", ["bf16", "f32"])
+@pytest.mark.parametrize("runs", [False, True])
+def test_many_tokens(M, N, K, L, R, c, runs):
+    run_and_check(M, N, K, L, R, c, M + N, runs, in_place=not runs)
+
+
+@pytest.mark.parametrize("c", ["bf16", "f32"])
+@pytest.mark.parametrize("most", [1, 7, 8, 9, 31, 32, 33, 64, 65, 127, 128, 129])
+def test_runs_of_every_length(c, most):
+    """Adapters whose tokens stand together, from odd places on, and one whose tokens stand between."""
+    M, N, K = 600, 392, 328
+    x, a, b, scales, ranks, ids, y = problem(M, N, K, 5, 24, c, 20)
+    ids[:] = -1
+    at, i = 3, 0
+    while at + most <= M:
+        ids[at:at + most] = i % 4
+        at, i = at + most + 1, i + 1
+    ids[ids == -1] = 4
+    ids[0] = -1
+    for in_place in (False, True):
+        got = call(x, a, b, scales, ranks, ids, y, c, in_place=in_place)
+        none = (ids == -1) | (ranks[ids.clamp(min=0).long()] == 0)
+        check(got, reference(x, a, b, scales, ranks, ids, y), c, none, y)
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 200, 600])
 @pytest.mark.parametrize("c", ["bf16", "f32"])
 def test_strides_and_alignment(M, c):

@@ -1,7 +1,8 @@
 """qw_rmsnorm on the GPU against 64 bits.
 
 Bound.  The sum of squares is one of positive terms in chains of at most c = 8 ceil(K / 8 / lanes) + 10
-additions, lanes being 32 up to K = 1024 and at least min(K / 16, 1024) beyond; each adds 2^-24, and
+additions, lanes being 32 up to K = 1024 and at least min(K / 32, 512) beyond (a thread has four vectors
+of eight values where a call has many rows: 32 additions, ten for the joins); each adds 2^-24, and
 1 / rms has half of that, the division and the addition of eps 2^-24 each, 1 / rms itself no more than
 2^-23.  h w, w_offset + w and y add 2^-24 each.  So y is within e |y|, e = 2^-24 (c / 2 + 7), before it is
 rounded: to BF16 (2^-8 |y|), to E4M3 (2^-4 |y|, below 2^-6 of its scale 2^-10 of it) or to a step of the
@@ -21,7 +22,7 @@ EPS = 1e-5
 
 
 def bound(K):
-    lanes = 32 if K <= 1024 else min(K // 16, 1024)
+    lanes = 32 if K <= 1024 else min(K // 32, 512)
     return 2.0 ** -24 * ((8 * math.ceil(K / 8 / lanes) + 10) / 2 + 7)
 
 
@@ -125,6 +126,16 @@ def test_shapes(rows, K, q):
     xv, rv, w = problem(rows, K, x, r, i)
     h, y = reference(xv, rv, w)
     check(call(xv, rv, w, q, y=q is None or i % 2 == 0, pad=[0, 8, 40][i % 3]), h, y, q, bound(K))
+
+
+@pytest.mark.parametrize("rows,K", [(1300, 1056), (320, 4096), (200, 7200), (160, 16384), (155, 16352)])
+@pytest.mark.parametrize("x,r", [("bf16", "bf16"), ("bf16", None), ("f32", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("q", ["mxfp8", "int8", None])
+def test_more_rows_than_run_at_once(rows, K, x, r, q):
+    xv, rv, w = problem(rows, K, x, r, rows)
+    xv[rows - 1] *= 1e30  # (its squares pass FP32; the row before it is the same CTA's or another's)
+    h, y = reference(xv, rv, w, 1.0)
+    check(call(xv, rv, w, q, y=True, pad=8, offset=1.0), h, y, q, bound(K))
 
 
 @pytest.mark.parametrize("x", ["bf16", "f32"])

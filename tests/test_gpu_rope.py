@@ -83,6 +83,15 @@ def test_shapes(layout, kind, T, heads, D, rot, pad, shift):
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,heads,D,rot,pad", [
+    (3001, 5, 256, 126, 0), (2500, 6, 72, 36, 0), (5003, 1, 64, 64, 0), (2049, 3, 80, 80, 3),
+    (400, 33, 256, 256, 64), (1777, 4, 10, 10, 1)])
+def test_many_tokens(layout, kind, T, heads, D, rot, pad):
+    run(T, heads, D, rot, layout, kind, pad, seed=T, in_place=T % 2 == 0)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_far_and_negative_positions(layout):
     positions = [0, 1, -1, 1 << 20, (1 << 24) + 1, (1 << 31) - 1, -(1 << 31), -12345678, 1000003]
     run(len(positions), 3, 128, 128, layout, "f32", positions=positions, scale=1.25)
