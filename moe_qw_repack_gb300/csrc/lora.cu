@@ -461,10 +461,13 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
 }  // namespace
 
 qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st) {
-  // Many tokens of an adapter go through the tensor cores together (us here and there, 4096 x 4096: 64 tokens of
-  // 64 adapters rank 64 26, 35; 64 of 8 rank 16 11, 17; 128 of 64 rank 16 23, 31; 192 of 64 rank 64 46, 36;
-  // 4096 x 14336 x 4096 rank 64 216, 87).
-  if (a.M > 16 && (a.M > 128 || a.M > T * (int64_t)a.L) && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
+  // Many tokens of an adapter go through the tensor cores together, and so do large calls, whose tokens may all
+  // be one adapter's (us here and there, K = 4096: 32 tokens of one adapter, N = 4096, rank 64 22, 14; of two,
+  // N = 14336, rank 16 17, 17; 96 of 8, N = 14336, rank 64 26, 26; 128 of 32, N = 4096, rank 32 18, 21 and 192 27,
+  // 26; 192 of 64, rank 64 46, 35; 256 of 300, rank 16 52, 90 and 512 98, 93; 4096 of 8 in runs, N = 14336,
+  // rank 64 277, 77).
+  const bool many = a.M > 512 || (a.M > 128 && a.M > 2 * (int64_t)a.L) || (a.M > 16 && a.M > 12 * (int64_t)a.L);
+  if (many && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
   return c_f32 ? launch<true>(a, st) : launch<false>(a, st);
 }
 
