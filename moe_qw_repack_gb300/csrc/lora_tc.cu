@@ -8,7 +8,7 @@
 // in it); a cluster of CTAs works on an item:
 //   1  D1[token][r] = X A^T over a CTA's slice of K, in stages of 64 k.  A comes by TMA, and so do tokens
 //      that stand together; other rows by cp.async of the epilogue's warps, which have nothing else to do
-//      yet.  (TMA gather4 copies, four rows each, took 75 cycles apiece, 2400 a stage.)  A warp that copies
+//      yet.  Four threads ask for the copies by turns.  (TMA gather4 copies, four rows each, took 75 cycles apiece, 2400 a stage.)  A warp that copies
 //      nothing puts the fence between those rows and the MMAs: a fence waits for all of its thread's
 //      copies, also those of later stages (0.65 us a stage).
 //   2  t = s_a (sum of the CTAs' D1, in rank order): each CTA fetches its tokens' shares, adds them up
@@ -23,12 +23,12 @@
 //      Items of up to 64 or 32 tokens have t's rows twice or four times, so that all warps share the
 //      columns.  (With a column a lane every element costs accesses of its own: 20 instructions an
 //      element, 106 us for 4096 x 14336 x 4096.)
-// B's stages are on their way while t is made.  Several clusters may share an item's columns, each with a t
+// B's first stages have a place of their own and are on their way from the start.  Several clusters may share an item's columns, each with a t
 // of its own, where that fills the SMs.  Every wait on a barrier is bounded; on expiry the kernel reports
 // QW_ERR_TIMEOUT and shuts down.
-// Bound by: an item's chain (find 3, X A^T and t 10 to 15, 1.5 us a tile and group) in small calls; in large
-// ones by base and C through shared memory and by what the last clusters leave idle: 4096 x 14336 x 4096, rank
-// 64, 77 us, 288 MB at 3.7 TB/s.
+// Bound by: an item's chain (list 2, X A^T and t 6 to 10, 2 us a tile and group) in small calls; in large ones
+// by L2 while all SMs read X and A (17 of 70 us for 4096 x 14336 x 4096, rank 64, where DRAM has little to do),
+// then by base and C through shared memory (5 TB/s), on 123 of 152 SMs there; 288 MB at 4.1 TB/s in all.
 #include <algorithm>
 
 #include "int8_map.cuh"
@@ -59,15 +59,14 @@ constexpr int SEGS = WINDOW / 32;
 struct Params {
   LoraArgs a;
   int32_t csize_log;
-  int32_t parts_log;  // clusters that share an item's columns (each makes t for itself)
+  int32_t parts;      // clusters that share an item's columns (each makes t for itself)
   int32_t k_stages;   // of a CTA's slice of K
   int32_t n_tiles;    // of a CTA's slice of N
   int32_t r16;        // R, rounded up to 16
   int32_t r_slots;    // ... to 64, in stages
   int32_t s2;         // stages of B
   int32_t t_bytes;
-  int32_t ring_bytes;
-  int32_t all_bytes;  // t, the ring and the units
+  int32_t first_bytes;  // t and the units; before them the first product's stages
   int32_t units;      // of a warp
   bool wide;           // base and C take 16-byte accesses
 };
@@ -137,9 +136,8 @@ __device__ __forceinline__ void tma_store_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 // ... until the stores' sources have been read / until they are done
-template <int N>  // ... but the last N
 __device__ __forceinline__ void tma_store_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void tma_store_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -220,15 +218,24 @@ __device__ __forceinline__ void put_piece(uint8_t* to, const uint4& x, int left)
   }
 }
 
+// the sum of v over the lanes up to this one
+__device__ __forceinline__ int scan(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int before = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += before;
+  }
+  return v;
+}
+
 // What the CTA knows of its window and of the item at hand.
 struct Plan {
   int32_t ids[WINDOW];       // adapters: -1 none, -2 behind the last token
-  uint16_t start[WINDOW];    // an adapter's first token: its first item, from its segment's first
+  uint16_t start[WINDOW];    // an adapter's first token: its first item, counted from its 32 tokens' first
   uint8_t items[WINDOW];     // ... and how many it has (0: not a first token)
-  int32_t seg[SEGS];         // items (then members) of 32 tokens, then of those before them
-  int32_t total;             // items
-  int32_t id, chunk, count;  // the item: adapter, its which 128 tokens, how many of them there are
-  int16_t row[TT];           // ... and where in the window
+  int32_t seg[SEGS];         // items of 32 tokens
+  int16_t row[TT];           // the item's tokens: where in the window
   int64_t off_c[TT], off_b[TT];  // bytes to the tokens' rows of C and base
 };
 
@@ -244,9 +251,9 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (0u - smem_u32(smem_raw) & 1023u);  // (stays a shared address)
   uint8_t* const s_t = smem;
-  uint8_t* const ring2 = smem + p.t_bytes;
-  uint8_t* const ring1 = smem;  // the first product's stages reach over t's place
-  uint8_t* const s_unit = ring2 + p.ring_bytes;
+  uint8_t* const ring1 = smem;  // the first product's stages reach over t's place and the units'
+  uint8_t* const s_unit = smem + p.t_bytes;
+  uint8_t* const ring2 = smem + p.first_bytes;
   __shared__ Plan plan;
   __shared__ uint64_t full1[MAX_STAGES], empty1[MAX_STAGES], landed[MAX_STAGES], full2[MAX_STAGES], empty2[MAX_STAGES];
   __shared__ uint64_t d1_full, acc_full[ACCS], acc_empty[ACCS], base_full[EPI_WARPS][MAX_UNITS], final_bar;
@@ -258,8 +265,9 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
   const int csize_log = p.csize_log, csize = 1 << csize_log;
   const int crank = (int)(blockIdx.x & (unsigned)(csize - 1));
   const unsigned cluster = blockIdx.x >> csize_log;
-  const int64_t m0 = (int64_t)(cluster >> p.parts_log) * WINDOW;
-  const int share = (int)(cluster & ((1u << p.parts_log) - 1u)) * csize + crank;  // of the columns
+  const unsigned window = cluster / (unsigned)p.parts;
+  const int64_t m0 = (int64_t)window * WINDOW;
+  const int share = (int)(cluster - window * (unsigned)p.parts) * csize + crank;  // of the columns
   const int win = (int)min64(WINDOW, a.M - m0);
 
   if (threadIdx.x == 0) {
@@ -325,33 +333,17 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
         while (key[h] != id) h = (h + 1) & (HASH - 1);
         if (at[h] == i) n = (count[h] + TT - 1) / TT;
       }
-      int sum = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += v;
-      }
+      const int sum = scan(n);
       plan.items[i] = (uint8_t)n;
       plan.start[i] = (uint16_t)(sum - n);
       if (lane == 31) plan.seg[s] = sum;
     }
+    fence_proxy_async_smem();  // (the hash's place is written by copies from here on)
     __syncthreads();
-    if (warp == 0) {
-      const int n = lane < SEGS ? plan.seg[lane] : 0;
-      int sum = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (lane == 31) plan.total = sum;
-      if (lane < SEGS) plan.seg[lane] = sum - n;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < win; i += THREADS) plan.start[i] += (uint16_t)plan.seg[i >> 5];
   }
-  fence_proxy_async_smem();  // (the hash's place is written by copies from here on)
-  __syncthreads();
+  // every warp: items of segment `lane`, of those before it and of the window
+  const int seg_items = lane < SEGS ? plan.seg[lane] : 0, seg_sum = scan(seg_items), seg_before = seg_sum - seg_items;
+  const int total = __shfl_sync(0xFFFFFFFFu, seg_sum, 31);
 
   const int64_t all_tiles = ((int64_t)a.N + BN - 1) / BN;
   const int tile0 = (int)min64(all_tiles, (int64_t)share * p.n_tiles);
@@ -367,51 +359,44 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
   uint32_t u1 = 0, ux = 0, ud = 0, ua = 0, slot2 = 0, phase2 = 0;  // (ux: of `landed`)
   uint32_t base_phase = 0;  // of this warp's units of base, a bit each
 
-  for (int item = (int)blockIdx.y; item < plan.total; item += (int)gridDim.y) {
-    // -------------------------------------------------------------- the item's tokens
-    for (int i = threadIdx.x; i < win; i += THREADS) {
-      const int c = item - plan.start[i];
-      if (c >= 0 && c < plan.items[i]) plan.id = plan.ids[i], plan.chunk = c;
-    }
-    __syncthreads();
-    const int id = plan.id;
-    for (int s = warp; s < SEGS; s += WARPS) {
-      const uint32_t b = __ballot_sync(0xFFFFFFFFu, plan.ids[32 * s + lane] == id);
-      if (lane == 0) plan.seg[s] = __popc(b);
-    }
-    __syncthreads();
-    {
-      int n = lane < SEGS ? plan.seg[lane] : 0, sum = n;
+  for (int item = (int)blockIdx.y; item < total; item += (int)gridDim.y) {
+    // -------------------------------------------------------------- the item's tokens (every warp: one barrier)
+    const int in_seg = item - seg_before;
+    const int seg = __ffs((int)__ballot_sync(0xFFFFFFFFu, in_seg >= 0 && in_seg < seg_items)) - 1;
+    const int in_adapter = __shfl_sync(0xFFFFFFFFu, in_seg, seg) - plan.start[32 * seg + lane];
+    const int first = __ffs((int)__ballot_sync(0xFFFFFFFFu, in_adapter >= 0 &&
+                                                            in_adapter < plan.items[32 * seg + lane])) - 1;
+    const int id = plan.ids[32 * seg + first], chunk = __shfl_sync(0xFFFFFFFFu, in_adapter, first);
+    int members = 0;  // of segment `lane`
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (threadIdx.x == 31) plan.count = min(TT, sum - plan.chunk * TT);
-      for (int s = warp; s < SEGS; s += WARPS) {
-        const int before = __shfl_sync(0xFFFFFFFFu, sum - n, s);
-        const bool mine = plan.ids[32 * s + lane] == id;
-        const uint32_t b = __ballot_sync(0xFFFFFFFFu, mine);
-        const int at = before + __popc(b & ((1u << lane) - 1u)) - plan.chunk * TT;
-        if (mine && at >= 0 && at < TT) {
-          plan.row[at] = (int16_t)(32 * s + lane);
-          plan.off_c[at] = (m0 + 32 * s + lane) * a.ldc * SIZE;
-          plan.off_b[at] = (m0 + 32 * s + lane) * a.ld_base * SIZE;
-        }
+    for (int s = 0; s < SEGS; ++s) {
+      const uint32_t b = __ballot_sync(0xFFFFFFFFu, plan.ids[32 * s + lane] == id);
+      if (lane == s) members = __popc(b);
+    }
+    const int member_sum = scan(members);
+    const int now = min(TT, __shfl_sync(0xFFFFFFFFu, member_sum, 31) - chunk * TT);
+    for (int s = warp; s < SEGS; s += WARPS) {
+      const int before = __shfl_sync(0xFFFFFFFFu, member_sum - members, s);
+      const bool mine = plan.ids[32 * s + lane] == id;
+      const uint32_t b = __ballot_sync(0xFFFFFFFFu, mine);
+      const int at = before + __popc(b & ((1u << lane) - 1u)) - chunk * TT;
+      if (mine && at >= 0 && at < TT) {
+        plan.row[at] = (int16_t)(32 * s + lane);
+        plan.off_c[at] = (m0 + 32 * s + lane) * a.ldc * SIZE;
+        plan.off_b[at] = (m0 + 32 * s + lane) * a.ld_base * SIZE;
       }
     }
     __syncthreads();
-    const int now = plan.count;
     const int rank = a.ranks ? a.ranks[id] : a.R;
     const int slots = (rank + BK - 1) / BK;
     const int uses2 = tiles * slots;
-    // The first product's stages, over all of the shared memory, hold the item's tokens and A; the MMA's other
-    // rows are whatever lies behind.
-    // Their barriers are used in turn, eight of them, whatever the number of stages.
+    // The first product's stages hold the item's tokens and A; the MMA's other rows are whatever lies behind
+    // (at the end some of B's ring, or what is on its way there).  Their barriers are used in turn, eight of
+    // them, whatever the number of stages.
     const bool together = plan.row[now - 1] - plan.row[0] == now - 1;
     const int x_map = now <= 8 ? 0 : now <= 32 ? 1 : 2;
     const int x_bytes = together ? 1024 << (2 * x_map) : (now + 7) / 8 * 1024, stage1 = x_bytes + p.r16 * BK * 2;
-    const int s1 = min(MAX_STAGES, (p.all_bytes - max(SLOT, stage1)) / stage1 + 1);  // (an MMA reads SLOT)
+    const int s1 = min(MAX_STAGES, p.first_bytes / stage1);
     // t has the tokens' rows 128 / span times
     const int span_log = now <= 32 ? 5 : now <= 64 ? 6 : 7, span = 1 << span_log;
     int issued2 = 0;
@@ -448,9 +433,31 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
     };
 
     // -------------------------------------------------------------- 1: X A^T
+    auto bring_a = [&](int first) {  // every other stage (one lane; false: a wait gave up)
+      for (int kb = first; kb < nk; kb += 2) {
+        if (!stage1_free(kb)) return false;
+        uint64_t* bar = &full1[(u1 + (uint32_t)kb) % MAX_STAGES];
+        mbar_arrive_expect_tx(bar, (uint32_t)(p.r16 * BK * 2));
+        tma_load_2d(ring1 + kb % s1 * stage1 + x_bytes, &tmA, bar, (kb0 + kb) * BK, (int32_t)((int64_t)id * a.R));
+      }
+      return true;
+    };
+    auto bring_x = [&](int first) {
+      const int32_t y = (int32_t)m0 + plan.row[0];
+      for (int kb = first; kb < nk && stage1_free(kb); kb += 2) {
+        uint64_t* bar = &full1[(u1 + (uint32_t)kb) % MAX_STAGES];
+        mbar_arrive_expect_tx(bar, (uint32_t)x_bytes);
+        tma_load_2d(ring1 + kb % s1 * stage1, &tmX.map[x_map], bar, (kb0 + kb) * BK, y);
+      }
+    };
     if (warp >= EPI_WARP0 && !worker) {
-      for (int i = 0; i < 4; ++i) prefetch_base(i);
-      for (int kb = 0; ew == GROUP_WARPS && !together && kb < nk; ++kb) {
+      const int job = ew - GROUP_WARPS;
+      if (lane == 0) {
+        if (together && job < 2) bring_x(job);
+        if (job == 2) bring_a(1);
+      }
+      __syncwarp();
+      for (int kb = 0; job == 0 && !together && kb < nk; ++kb) {
         const uint32_t u = ux + (uint32_t)kb;
         if (!warp_wait(&landed[u % MAX_STAGES], u / MAX_STAGES & 1u, abort_flag, a.err)) {
           ok = false;
@@ -460,6 +467,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
         __syncwarp();
         if (lane == 0) mbar_arrive(&full1[(u1 + (uint32_t)kb) % MAX_STAGES]);
       }
+      for (int i = 0; i < min(tiles, 2); ++i) prefetch_base(i);
     } else if (worker) {
       if (!together) {  // the listed rows, eight threads a row of a stage
         const uint16_t* x[4];
@@ -487,23 +495,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
       tc_fence_after();
     } else if (warp == 0) {
       if (lane == 0) {
-        for (int kb = 0, slot = 0; kb < nk; ++kb) {
-          if (!stage1_free(kb)) {
-            ok = false;
-            break;
-          }
-          uint64_t* bar = &full1[(u1 + (uint32_t)kb) % MAX_STAGES];
-          mbar_arrive_expect_tx(bar, (uint32_t)(p.r16 * BK * 2));
-          tma_load_2d(ring1 + slot * stage1 + x_bytes, &tmA, bar, (kb0 + kb) * BK,
-                      (int32_t)((int64_t)id * a.R));
-          if (together) {
-            mbar_arrive_expect_tx(bar, (uint32_t)x_bytes);
-            tma_load_2d(ring1 + slot * stage1, &tmX.map[x_map], bar, (kb0 + kb) * BK, (int32_t)m0 + plan.row[0]);
-          }
-          if (++slot == s1) slot = 0;
-        }
-        // the first of B's stages take the place of the first product's as soon as that has read them
-        if (ok && nk > 0) ok = mbar_wait(&d1_full, ud & 1u, abort_flag, a.err);
+        ok = bring_a(0);
         load_b(min(uses2, p.s2));
       }
       __syncwarp();
@@ -790,13 +782,24 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
         __syncwarp();
         for (int d = 0; d < p.units; ++d) fetch(d, d);
         int slot = 0;
+        // With two places the next unit is asked for before this one is waited for, as soon as the store of the one
+        // before has read its place.  (After this one: 77 us instead of 73 for 4096 x 14336 x 4096.)
+        auto ahead = [&](int unit, int slot) {
+          if (p.units == MAX_UNITS && unit > 0) {
+            tma_store_read();
+            __syncwarp();
+            fetch(unit + 1, slot ^ 1);
+          }
+        };
         for (int k = 0; k < my_tiles; ++k) {
           const uint32_t v = ua + (uint32_t)(2 * k + group), buf = v % ACCS;
+          ahead(k * PER, slot);
           if (ok) ok = warp_wait(&acc_full[buf], v / ACCS & 1u, abort_flag, a.err);
           tc_fence_after();
 #pragma unroll 1
           for (int u = 0; u < PER; ++u) {
             const int32_t n = (tile0 + 2 * k + group) * BN + col0 + u * COLS;
+            if (u > 0) ahead(k * PER + u, slot);
             if (n >= a.N) {
               if (u == PER - 1) {
                 tc_fence_before();
@@ -851,17 +854,12 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
               tma_store_2d(&tmC8, box + lane * 8 * BOX_ROW, n, y + 8 * lane);
             }
             tma_store_commit();
-            // The place is asked for again when the store has read it: with more than one, a unit later.
-            const int unit = k * PER + u;
             if (p.units == 1) {
-              tma_store_read<0>();
+              tma_store_read();
               __syncwarp();
-              fetch(unit + 1, 0);
+              fetch(k * PER + u + 1, 0);
             } else {
-              tma_store_read<1>();
-              __syncwarp();
-              if (unit > 0) fetch(unit - 1 + p.units, slot == 0 ? p.units - 1 : slot - 1);
-              if (++slot == p.units) slot = 0;
+              slot ^= 1;
             }
           }
         }
@@ -964,31 +962,29 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   constexpr int UNITS = EPI_WARPS * UNIT_BYTES;
   const int all = kSmemCta - fixed - 1024 - p.t_bytes;
   p.units = std::max(1, std::min(MAX_UNITS, (all - 2 * SLOT) / UNITS));
-  const int room = all - p.units * UNITS;
-  p.ring_bytes = std::min(room, MAX_STAGES * SLOT) / 1024 * 1024;
-  p.s2 = std::min(MAX_STAGES, p.ring_bytes / SLOT);
-  p.all_bytes = p.t_bytes + p.ring_bytes + p.units * UNITS;
-  if (p.all_bytes / stage1 < 2 || p.s2 < 1) return QW_ERR_UNSUPPORTED;
+  p.s2 = std::min(MAX_STAGES, (all - p.units * UNITS) / SLOT);
+  p.first_bytes = p.t_bytes + p.units * UNITS;
+  if (p.first_bytes / stage1 < 2 || p.s2 < 1) return QW_ERR_UNSUPPORTED;
   // The cheapest cluster and number of clusters on an item's columns, in rounds of what runs at once (a cluster
   // lies within one GPC) of what an item takes, in us: to find, to join, each CTA's stages and tiles.  What is past
   // one round starts late.  The items: 128 tokens each, and a part of that for each adapter.  (us measured,
-  // cluster x clusters: 4096 x 14336 x 4096 rank 64 in runs of 8 adapters 2x1 98, 4x1 83, [2x2] 77, 8x1 100;
-  // 2048 mixed tokens of 8, 4096 x 4096 rank 16 2x1 46, [4x1] 31, 2x2 34, 8x1 54; 256 tokens of 64, rank 32 1x1 48,
-  // [2x1] 33, 4x1 42; 128 of one, rank 64 4x1 30, 8x1 21, 8x2 17.)
+  // cluster x clusters: 4096 x 14336 x 4096 rank 64 in runs of 8 adapters 2x1 86, 4x1 76, 2x2 72, [1x3] 70, 1x4
+  // 77, 8x1 86; 2048 mixed tokens of 8, 4096 x 4096 rank 16 2x1 42, [4x1] 28, 2x2 31, 8x1 48; 256 tokens of 64,
+  // rank 32 1x1 48, [2x1] 32, 4x1 40; 128 of one, rank 64 4x1 27, 8x1 18, 8x2 16, [8x4] 15.)
   const double items = (double)((a.M + TT - 1) / TT) + 1 + std::min<int64_t>(a.L, a.M);
   double least = 1e30;
   for (int log = 0; log <= 3; ++log)
-    for (int parts = 0; parts <= 3; ++parts) {
-      const int64_t c = (int64_t)1 << log, shares = c << parts;
-      if ((c > 1 && c > all_k && c > all_tiles) || (c == 2 && a.R > 128) || (parts > 0 && shares > all_tiles)) continue;
+    for (int parts = 1; parts <= 8; ++parts) {
+      const int64_t c = (int64_t)1 << log, shares = c * parts;
+      if ((c > 1 && c > all_k && c > all_tiles) || (c == 2 && a.R > 128) || (parts > 1 && shares > all_tiles)) continue;
       const double rounds = items * shares / (sms * (c == 8 ? 0.79 : c == 4 ? 0.9 : 1.0));
       const double cost = (rounds <= 1 ? 1 : rounds + 0.25) * (6 + (c > 1 ? 5 : 0) + (all_k + c - 1) / c * 0.3 +
                                                                (all_tiles + shares - 1) / shares * 1.7);
-      if (cost < least) least = cost, p.csize_log = log, p.parts_log = parts;
+      if (cost < least) least = cost, p.csize_log = log, p.parts = parts;
     }
   const int csize = 1 << p.csize_log;
   p.k_stages = (int32_t)((all_k + csize - 1) / csize);
-  const int shares = csize << p.parts_log;
+  const int shares = csize * p.parts;
   p.n_tiles = (int32_t)((all_tiles + shares - 1) / shares);
   const int vec = C32 ? 4 : 8;
   p.wide = ((uintptr_t)a.C | (uintptr_t)a.base) % 16 == 0 && a.ldc % vec == 0 &&
@@ -1025,7 +1021,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)x, (unsigned)y);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = (size_t)(1024 + p.all_bytes);
+  cfg.dynamicSmemBytes = (size_t)(1024 + p.first_bytes + p.s2 * SLOT);
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
