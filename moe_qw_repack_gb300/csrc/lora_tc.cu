@@ -8,9 +8,9 @@
 // in it); a cluster of CTAs works on an item:
 //   1  D1[token][r] = X A^T over a CTA's slice of K, in stages of 64 k.  A comes by TMA, and so do tokens
 //      that stand together; other rows by cp.async of the epilogue's warps, which have nothing else to do
-//      yet.  Four threads ask for the copies by turns.  (TMA gather4 copies, four rows each, took 75 cycles apiece, 2400 a stage.)  A warp that copies
-//      nothing puts the fence between those rows and the MMAs: a fence waits for all of its thread's
-//      copies, also those of later stages (0.65 us a stage).
+//      yet.  Four threads ask for the copies by turns.  (TMA gather4 copies, four rows each, took 75 cycles
+//      apiece, 2400 a stage.)  A warp that copies nothing puts the fence between those rows and the MMAs: a
+//      fence waits for all of its thread's copies, also those of later stages (0.65 us a stage).
 //   2  t = s_a (sum of the CTAs' D1, in rank order): each CTA fetches its tokens' shares, adds them up
 //      and leaves its tokens' t, which the others fetch; all reads of 256 bytes in a row.  t is held as
 //      BF16 numbers that add up to it, two where results are BF16 (2^-17 t is lost of what the result
@@ -23,9 +23,9 @@
 //      Items of up to 64 or 32 tokens have t's rows twice or four times, so that all warps share the
 //      columns.  (With a column a lane every element costs accesses of its own: 20 instructions an
 //      element, 106 us for 4096 x 14336 x 4096.)
-// B's first stages have a place of their own and are on their way from the start.  Several clusters may share an item's columns, each with a t
-// of its own, where that fills the SMs.  Every wait on a barrier is bounded; on expiry the kernel reports
-// QW_ERR_TIMEOUT and shuts down.
+// B's stages have a place of their own and the first are on their way from the start.  Several clusters may
+// share an item's columns, each with a t of its own, where that fills the SMs.  Every wait on a barrier is
+// bounded; on expiry the kernel reports QW_ERR_TIMEOUT and shuts down.
 // Bound by: an item's chain (list 2, X A^T and t 6 to 10, 2 us a tile and group) in small calls; in large ones
 // by L2 while all SMs read X and A (17 of 70 us for 4096 x 14336 x 4096, rank 64, where DRAM has little to do),
 // then by base and C through shared memory (5 TB/s), on 123 of 152 SMs there; 288 MB at 4.1 TB/s in all.
@@ -674,6 +674,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
       const int width = 64 >> (7 - span_log), col0 = ((32 * quad >> span_log) * 2 + half) * width;
       const int cols = min(width, C32 ? 16 : 32), cols_log = cols == 32 ? 5 : 4;
       const int per_log = (span_log - 1) - cols_log;  // units of a tile
+      // (Both groups on every tile, half its columns each: 4096 x 14336 x 4096 73 us instead of 70.)
       const int my_tiles = (tiles + 1 - group) >> 1;  // tiles group, group + 2, ...
       const int units = count > 0 ? my_tiles << per_log : 0, last = (1 << per_log) - 1;
       int rows_log = 3;
