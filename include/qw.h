@@ -521,7 +521,8 @@ qw_status qw_rmsnorm(int32_t x_type, const void* X, int64_t ldx, int32_t r_type,
  *   with a = ids[m], the token's adapter (device int32 [M], any order; tokens of the same adapter
  *   that stand together share its weights).  ids[m] = -1: C's row is base's, bit for bit.
  *   X: BF16 [M][K], row pitch ldx.  A: BF16 [L][R][K], B: BF16 [L][N][R], contiguous: adapters of up
- *   to R rows and columns, of which ranks[a] (device int32 [L], 0 .. R; NULL: R) are read.  scales:
+ *   to R rows and columns, of which ranks[a] (device int32 [L], 0 .. R; NULL: R) are used (what lies
+ *   behind may be anything).  A token whose A x or result is not finite leaves the others alone.  scales:
  *   FP32 [L] or NULL (1).  base: c_type, row pitch ld_base, or NULL (0); may be C with the same
  *   pitch, which adds to a projection's output in place (rows without adapter are then not
  *   touched).  C: c_type QW_T_BF16 or QW_T_F32, row pitch ldc >= N, rounded once.  Products and sums

@@ -125,9 +125,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float x0, float x1) {
 //   ROWS_ONE    a CTA takes one row: few rows, or long ones
 //   ROWS_MANY   CTAs take rows in turn, the next row's values on their way while one is worked on, and keep
 //               the weights
-// Bound: the bytes, and under them the instructions (about 25 an element with two vectors a thread, fewer
-// with four, as reductions and addresses are per row).  8192 x 4096, residual, to BF16 and MXFP8: 55.2 us with a
-// CTA a row, 54.0 in turn with two vectors a thread, 50.6 with four (6.0 TB/s).
+// Bound: the bytes, and close under them the instructions (29 an element to BF16 and MXFP8), whose reductions
+// and addresses are per row: more vectors a thread are fewer of them.  8192 x 4096, residual, to BF16 and MXFP8:
+// 55.2 us with a CTA a row, 54.0 in turn with two vectors a thread, 50.9 with four (5.95 TB/s).
 enum { ROWS_WARP = 0, ROWS_ONE = 1, ROWS_MANY = 2 };
 constexpr int threads_of(int form) { return form == ROWS_WARP ? NORM_WARPS * 32 : form == ROWS_ONE ? 1024 : 512; }
 

@@ -571,6 +571,11 @@ qw_status qw_rmsnorm(int32_t x_type, const void* X, int64_t ldx, int32_t r_type,
       (Y && (!aligned(Y, 16) || ldy % 8)) || !aligned(Q, 16) ||
       (q_fmt == QW_A_INT8_TOKEN && !aligned(Q_sf, 4)))
     return QW_ERR_ALIGNMENT;
+  // buffers in each other's place: rows would be overwritten before they are read, or twice
+  if ((R_out && R_out == R && ldro != ldr) || (R_out && R_out == X && (r_type != x_type || ldro != ldx)) ||
+      (Y && Y == X && (x_type != QW_T_BF16 || ldy != ldx)) || (Y && (Y == R || Y == R_out)) ||
+      (Q && (Q == X || Q == R || Q == R_out || Q == Y || Q == Q_sf)))
+    return QW_ERR_INVALID_ARG;
   const NormArgs a{X, ldx, R, ldr, R_out, ldro, W, w_offset, eps, rows, K, Y, ldy, Q, Q_sf, d_err};
   return launch_rmsnorm(a, x_type, r_type, q_fmt, static_cast<cudaStream_t>(stream));
 }

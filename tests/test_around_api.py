@@ -55,6 +55,20 @@ def test_norm_refusals(Q):
         assert norm(**kw) == want, kw
 
 
+def test_norm_refuses_buffers_in_each_others_place(Q):
+    """What the declaration allows in place has one pitch and type; the rest is refused before any launch."""
+    def norm(**kw):
+        a = dict(x_type=Q.QW_T_BF16, X=G, ldx=64, r_type=Q.QW_T_BF16, R=2 * G, ldr=72, R_out=3 * G, ldro=80,
+                 W=4 * G, w_offset=0.0, eps=1e-6, rows=4, K=64, Y=5 * G, ldy=88, q_fmt=Q.QW_A_MXFP8_G32,
+                 Q=6 * G, Q_sf=7 * G, d_err=None, stream=0)
+        a.update(kw)
+        return status(Q.qw_rmsnorm, *a.values())
+    for kw in (dict(R_out=2 * G), dict(R_out=G), dict(R_out=G, ldro=64, r_type=Q.QW_T_F32), dict(Y=G),
+               dict(Y=G, ldy=64, x_type=Q.QW_T_F32), dict(Y=2 * G, ldy=72), dict(Y=3 * G, ldy=80),
+               dict(Q=G), dict(Q=2 * G), dict(Q=3 * G), dict(Q=5 * G), dict(Q=7 * G)):
+        assert norm(**kw) == Q.QW_ERR_INVALID_ARG, kw
+
+
 def test_adapter_refusals(Q):
     inv, uns, ali = Q.QW_ERR_INVALID_ARG, Q.QW_ERR_UNSUPPORTED, Q.QW_ERR_ALIGNMENT
 
