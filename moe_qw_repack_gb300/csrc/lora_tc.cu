@@ -681,52 +681,55 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
       while (rows_log < 5 && 1 << rows_log < count) ++rows_log;
       const int row_log = cols_log + (C32 ? 2 : 1);        // bytes of a unit's row: 64 or 32
       const int pieces_log = row_log - 4;                   // in pieces of 16 bytes
-      int depth = 1;  // (a power of two)
-      while (depth < 8 && 2 * depth << (rows_log + row_log) <= p.units * UNIT_BYTES) depth *= 2;
+      // Rows that 16-byte accesses do not fit: base comes in the 16-byte pieces that it lies in (one more than
+      // its length, an odd number: lanes that hold a row each meet different banks), C goes in words.
+      const int words_log = row_log - 2, pitch = (1 << row_log) + 16;
+      const int place_bytes = p.wide ? 1 << (rows_log + row_log) : pitch << rows_log;
+      int depth = 1;
+      while (depth < 8 && 2 * depth * place_bytes <= p.units * UNIT_BYTES) depth *= 2;
+      if (depth == 2 && 3 * place_bytes <= p.units * UNIT_BYTES) depth = 3;
       constexpr int EACH = 16 / SIZE;                       // elements of a piece
       uint8_t* const mine = s_unit + ew * p.units * UNIT_BYTES;
       // where piece j of row r lies: eight neighbouring rows' pieces j are in different banks
       auto piece = [&](int r, int j) {
         return (r << row_log) + ((j ^ (pieces_log == 2 ? r >> 1 : r >> 2)) & ((1 << pieces_log) - 1)) * 16;
       };
-      auto place = [&](int unit) { return mine + ((unit & (depth - 1)) << (rows_log + row_log)); };
       auto column = [&](int unit) {
         return (tile0 + 2 * (unit >> per_log) + group) * BN + col0 + ((unit & last) << cols_log);
       };
       const int row1 = lane >> pieces_log, piece1 = lane & ((1 << pieces_log) - 1), rows1 = 32 >> pieces_log;
-      auto load = [&](int unit) {
+      const int word1 = lane & ((1 << words_log) - 1), rows2 = 32 >> words_log;
+      auto load = [&](int unit, int slot) {
         if (unit < units && a.base) {
-          uint8_t* to = place(unit);
+          uint8_t* to = mine + slot * place_bytes;
           const int32_t n0 = column(unit);
           const uint8_t* from = static_cast<const uint8_t*>(a.base) + (int64_t)n0 * SIZE;
+          const int left = min(cols, a.N - n0) * SIZE;  // bytes of a row
           if (p.wide) {
-            const int left = (a.N - n0 - piece1 * EACH) * SIZE;  // bytes of the row from here
             int64_t off[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) off[i] = plan.off_b[t0 + min(row1 + i * rows1, count - 1)];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (row1 + i * rows1 < count && left > 0)
-                cp_async16(to + piece(row1 + i * rows1, piece1), from + off[i] + piece1 * 16, min(16, left));
-          } else {
-            const int c = lane & (cols - 1), step = 32 >> cols_log;
-            for (int r0 = lane >> cols_log; n0 + c < a.N && r0 < count; r0 += 8 * step) {
-              T x[8];
+              if (row1 + i * rows1 < count && left > piece1 * 16)
+                cp_async16(to + piece(row1 + i * rows1, piece1), from + off[i] + piece1 * 16,
+                           min(16, left - piece1 * 16));
+          } else if (left > 0) {  // (whole pieces, whosever the ends of the first and the last are)
+            auto get = [&](int r, int j) {
+              const uint8_t* x = from + plan.off_b[t0 + r];
+              const int shift = (int)((uintptr_t)x & 15);
+              if (16 * j < left + shift) cp_async16(to + r * pitch + 16 * j, x - shift + 16 * j);
+            };
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                x[i] = *reinterpret_cast<const T*>(from + plan.off_b[t0 + min(r0 + i * step, count - 1)] +
-                                                   c * SIZE);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (r0 + i * step < count)
-                  *reinterpret_cast<T*>(to + piece(r0 + i * step, c / EACH) + c % EACH * SIZE) = x[i];
-            }
+            for (int i = 0; i < 4; ++i)
+              if (row1 + i * rows1 < count) get(row1 + i * rows1, piece1);
+            if (lane < count) get(lane, 1 << pieces_log);
           }
         }
         cp_async_commit();
       };
-      auto store = [&](int unit) {
-        const uint8_t* from = place(unit);
+      auto store = [&](int unit, int slot) {
+        const uint8_t* from = mine + slot * place_bytes;
         const int32_t n0 = column(unit);
         uint8_t* to = static_cast<uint8_t*>(a.C) + (int64_t)n0 * SIZE;
         if (p.wide) {
@@ -745,19 +748,23 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
             put_piece<C32>(to + off[i] + piece1 * 16, x[i], left);
           }
         } else {
-          const int c = lane & (cols - 1), step = 32 >> cols_log;
-          for (int r0 = lane >> cols_log; n0 + c < a.N && r0 < count; r0 += 8 * step) {
-            int64_t off[8];
-            T x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = min(r0 + i * step, count - 1);
-              off[i] = plan.off_c[t0 + r];
-              x[i] = *reinterpret_cast<const T*>(from + piece(r, c / EACH) + c % EACH * SIZE);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (r0 + i * step < count) *reinterpret_cast<T*>(to + off[i] + c * SIZE) = x[i];
+          const int left = min(cols, a.N - n0) * SIZE;
+#pragma unroll 8
+          for (int i = 0; i < 16; ++i) {  // (16 words a row: two rows at a time; eight: four)
+            const int r = (lane >> words_log) + i * rows2;
+            if (r >= count) break;
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(from + r * pitch + 4 * word1);
+            uint8_t* row = to + plan.off_c[t0 + r];
+            const int at = 4 * word1 - (int)((uintptr_t)row & 3);  // in the unit's row
+            if (at >= 0 && at + 4 <= left) *reinterpret_cast<uint32_t*>(row + at) = x;
+          }
+          if (!C32 && lane < count && left > 0) {  // halves of words at the ends
+            uint8_t* row = to + plan.off_c[t0 + lane];
+            const int shift = (int)((uintptr_t)row & 3), end = left + shift;
+            const uint8_t* x = from + lane * pitch;
+            if (shift) *reinterpret_cast<uint16_t*>(row) = *reinterpret_cast<const uint16_t*>(x + 2);
+            if (end & 2)
+              *reinterpret_cast<uint16_t*>(row + left - 2) = *reinterpret_cast<const uint16_t*>(x + end - 2);
           }
         }
       };
@@ -867,7 +874,8 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
         tma_store_done();
         __syncwarp();
       } else {
-        for (int d = 0; d < depth; ++d) load(d);
+        for (int d = 0; d < depth; ++d) load(d, d);
+        int slot = 0;
         for (int k = 0; k < my_tiles; ++k) {
           const uint32_t v = ua + (uint32_t)(2 * k + group), buf = v % ACCS;
           prefetch_base(2 * k + group + 4);
@@ -876,26 +884,69 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
           for (int unit = k << per_log; unit < min(units, (k + 1) << per_log); ++unit) {
             cp_async_wait_upto(depth - 1);
             __syncwarp();  // the unit's base is there
-            uint8_t* at = place(unit);
+            uint8_t* at = mine + slot * place_bytes;
             const uint32_t d2 = tbase + lanes + buf * BN + col0 + ((unit & last) << cols_log);
-            for (int c = 0; c < cols; c += 16) {
-              float d[16];
-              uint4 was[16 / EACH];
-              tc_ld<16>(d2 + c, d);
+            if (p.wide) {
+              for (int c = 0; c < cols; c += 16) {
+                float d[16];
+                uint4 was[16 / EACH];
+                tc_ld<16>(d2 + c, d);
 #pragma unroll
-              for (int j = 0; j < 16 / EACH; ++j)
-                was[j] = a.base ? *reinterpret_cast<const uint4*>(at + piece(my_row, c / EACH + j)) : zero4();
-              tc_landed(d);
+                for (int j = 0; j < 16 / EACH; ++j)
+                  was[j] = a.base ? *reinterpret_cast<const uint4*>(at + piece(my_row, c / EACH + j)) : zero4();
+                tc_landed(d);
 #pragma unroll
-              for (int j = 0; j < 16 / EACH; ++j) {
-                const uint4 o = add_piece<C32>(was[j], d + j * EACH);
-                if (lane < count) *reinterpret_cast<uint4*>(at + piece(my_row, c / EACH + j)) = o;
+                for (int j = 0; j < 16 / EACH; ++j) {
+                  const uint4 o = add_piece<C32>(was[j], d + j * EACH);
+                  if (lane < count) *reinterpret_cast<uint4*>(at + piece(my_row, c / EACH + j)) = o;
+                }
               }
+            } else {
+              // this lane's row: from where it lies in base to where its words lie in C
+              uint4* w = reinterpret_cast<uint4*>(at + my_row * pitch);
+              const int64_t n0 = column(unit);
+              const int mine_row = t0 + min(lane, count - 1);
+              const uint32_t from = (uint32_t)((uintptr_t)a.base + plan.off_b[mine_row] + n0 * SIZE) & 15u;
+              const uint32_t to = (uint32_t)((uintptr_t)a.C + plan.off_c[mine_row] + n0 * SIZE) & 3u;
+              constexpr int WORDS = 16 * SIZE / 4;  // of 16 columns
+              uint32_t carry = 0;
+              for (int c = 0; c < cols / 16; ++c) {
+                float d[16];
+                uint32_t x[WORDS + 4];
+                tc_ld<16>(d2 + 16 * c, d);
+#pragma unroll
+                for (int j = 0; j <= WORDS / 4; ++j)
+                  *reinterpret_cast<uint4*>(&x[4 * j]) = a.base ? w[c * WORDS / 4 + j] : zero4();
+#pragma unroll
+                for (int j = 0; j < WORDS + 2; ++j) x[j] = from & 8 ? x[j + 2] : x[j];
+#pragma unroll
+                for (int j = 0; j < WORDS + 1; ++j) x[j] = from & 4 ? x[j + 1] : x[j];
+                tc_landed(d);
+#pragma unroll
+                for (int j = 0; j < WORDS; ++j) {
+                  if constexpr (C32) {
+                    x[j] = __float_as_uint(__uint_as_float(x[j]) + d[j]);
+                  } else {
+                    const uint32_t b = __funnelshift_r(x[j], x[j + 1], 8 * (from & 2));
+                    const uint32_t sum = pack_bf16x2(__uint_as_float(b << 16) + d[2 * j],
+                                                     __uint_as_float(b & 0xFFFF0000u) + d[2 * j + 1]);
+                    x[j] = __funnelshift_l(carry, sum, 8 * to);
+                    carry = sum;
+                  }
+                }
+                if (lane < count) {
+#pragma unroll
+                  for (int j = 0; j < WORDS / 4; ++j)
+                    w[c * WORDS / 4 + j] = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                }
+              }
+              if (!C32 && lane < count) w[cols * SIZE / 16].x = carry >> 16;
             }
             __syncwarp();  // its results are
-            store(unit);
+            store(unit, slot);
             __syncwarp();
-            load(unit + depth);
+            load(unit + depth, slot);
+            if (++slot == depth) slot = 0;
           }
           tc_fence_before();
           __syncwarp();
