@@ -36,7 +36,6 @@ constexpr int SLOT = BN * BR * 2, SLOTS = 3;
 // part (nsplit of them), slices of n_len.
 struct Cut {
   int32_t csize, csize_log, nsplit, k_len, n_len;
-  bool wide;  // base and C take 16-byte accesses
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -76,30 +75,57 @@ __device__ __forceinline__ void shrink_block(const uint16_t* a_lo, const uint16_
   }
 }
 
-// base of a lane's four columns of a token, as it lies in memory; `left`: columns from there to the end
+// Four columns of a token.
 template <bool C32>
 using Piece = std::conditional_t<C32, uint4, uint2>;
-template <bool C32>
-__device__ __forceinline__ Piece<C32> get4(const uint8_t* b, bool wide, int32_t left) {
-  if (wide && left >= 4) return *reinterpret_cast<const Piece<C32>*>(b);
-  uint32_t w[4] = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= left) continue;
-    if constexpr (C32)
-      w[i] = reinterpret_cast<const uint32_t*>(b)[i];
-    else
-      w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(b)[i] << (16 * (i % 2));
+// base of them as it lies in memory: BF16 rows that begin anywhere in the words that they touch
+template <bool C32, bool WIDE>
+struct Raw {
+  uint32_t w[C32 ? 4 : WIDE ? 2 : 3];
+};
+// (`left`: columns from there to the end)
+template <bool C32, bool WIDE>
+__device__ __forceinline__ Raw<C32, WIDE> get4(const uint8_t* b, int32_t left) {
+  Raw<C32, WIDE> x{};
+  if constexpr (WIDE) {
+    if (left >= 4) {
+      const Piece<C32> v = *reinterpret_cast<const Piece<C32>*>(b);
+      x.w[0] = v.x, x.w[1] = v.y;
+      if constexpr (C32) x.w[2] = v.z, x.w[3] = v.w;
+      return x;
+    }
   }
+  if constexpr (C32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) x.w[i] = reinterpret_cast<const uint32_t*>(b)[i];
+  } else if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) x.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(b)[i] << (16 * (i % 2));
+  } else {  // (whole words, whosever the other half of the first and the last is; put together when they are used)
+    const int shift = (int)((uintptr_t)b & 2);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (4 * i < 2 * min(left, 4) + shift) x.w[i] = *reinterpret_cast<const uint32_t*>(b - shift + 4 * i);
+  }
+  return x;
+}
+template <bool C32, bool WIDE>
+__device__ __forceinline__ Piece<C32> four(const Raw<C32, WIDE>& x, const uint8_t* b) {
   if constexpr (C32)
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  else
-    return make_uint2(w[0], w[1]);
+    return make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+  else if constexpr (WIDE)
+    return make_uint2(x.w[0], x.w[1]);
+  else {
+    const uint32_t shift = 8 * (uint32_t)((uintptr_t)b & 2);
+    return make_uint2(__funnelshift_r(x.w[0], x.w[1], shift), __funnelshift_r(x.w[1], x.w[2], shift));
+  }
 }
 // ... plus sums, to C
-template <bool C32>
-__device__ __forceinline__ void put4(uint8_t* c, bool wide, int32_t left, const Piece<C32>& x, float s0, float s1,
-                                     float s2, float s3) {
+template <bool C32, bool WIDE>
+__device__ __forceinline__ void put4(uint8_t* c, int32_t left, const Piece<C32>& x, float s0, float s1, float s2,
+                                     float s3) {
   Piece<C32> o;
   uint32_t w[4];
   if constexpr (C32) {
@@ -111,7 +137,7 @@ __device__ __forceinline__ void put4(uint8_t* c, bool wide, int32_t left, const 
     w[1] = pack_bf16x2(__uint_as_float(x.y << 16) + s2, __uint_as_float(x.y & 0xFFFF0000u) + s3);
     o = make_uint2(w[0], w[1]);
   }
-  if (wide && left >= 4) {
+  if (WIDE && left >= 4) {
     *reinterpret_cast<Piece<C32>*>(c) = o;
   } else {
 #pragma unroll
@@ -231,7 +257,7 @@ struct Ring {
   }
 };
 
-template <bool C32>
+template <bool C32, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 2)
     lora_mma_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB32,
                     const __grid_constant__ LoraArgs p, const __grid_constant__ Cut cut) {
@@ -306,10 +332,12 @@ __global__ void __launch_bounds__(THREADS, 2)
       ring.start();
       if (lane == 0 && ok)
         for (int i = 0; i < SLOTS; ++i) ring.request(tmB, tmB32);
-      if (lane == 0 && warp < now && p.base && cut.wide && n1 - n0 >= 8) {  // base on its way to L2
+      if (lane == 0 && warp < now && p.base) {  // base on its way to L2, as far as it is whole 16 bytes
         constexpr int SIZE = C32 ? 4 : 2;
-        bulk_prefetch_l2(static_cast<const uint8_t*>(p.base) + ((m0 + list[warp]) * p.ld_base + n0) * SIZE,
-                         (uint32_t)(n1 - n0) / 8u * 8u * SIZE);
+        const uint8_t* x = static_cast<const uint8_t*>(p.base) + ((m0 + list[warp]) * p.ld_base + n0) * SIZE;
+        const int skip = (int)(0u - (uint32_t)(uintptr_t)x & 15u);
+        const int64_t bytes = (int64_t)(n1 - n0) * SIZE - skip;
+        if (bytes >= 16) bulk_prefetch_l2(x + skip, (uint32_t)(bytes & ~15ll));
       }
       __syncwarp();
       const Pass<C32> pass{p, cut, m0, id, rank, now, list, lane, warp, g, t};
@@ -340,17 +368,17 @@ __global__ void __launch_bounds__(THREADS, 2)
         c[e] = static_cast<uint8_t*>(p.C) + (m * p.ldc + n) * SIZE;
       }
       const bool mine0 = 2 * t < now, mine1 = 2 * t + 1 < now;
-      Piece<C32> one[2] = {}, two[2] = {};  // base of the next two blocks
-      auto ahead = [&](int32_t to, Piece<C32>(&x)[2]) {
+      Raw<C32, WIDE> one[2] = {}, two[2] = {};  // base of the next two blocks
+      auto ahead = [&](int32_t to, Raw<C32, WIDE>(&x)[2]) {
         const int32_t left = n1 - n - to;
         if (left <= 0 || !p.base) return;
-        if (mine0) x[0] = get4<C32>(b[0] + (int64_t)to * SIZE, cut.wide, left);
-        if (mine1) x[1] = get4<C32>(b[1] + (int64_t)to * SIZE, cut.wide, left);
+        if (mine0) x[0] = get4<C32, WIDE>(b[0] + (int64_t)to * SIZE, left);
+        if (mine1) x[1] = get4<C32, WIDE>(b[1] + (int64_t)to * SIZE, left);
       };
       ahead(0, one);
       ahead(WARPS * BN, two);
       for (int32_t nb = ring.n0; nb < n1; nb += WARPS * BN) {
-        const Piece<C32> was[2] = {one[0], one[1]};
+        const Raw<C32, WIDE> was[2] = {one[0], one[1]};
         one[0] = two[0], one[1] = two[1];
         ahead(2 * WARPS * BN, two);
         float acc[2][4] = {};
@@ -387,8 +415,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         const int32_t left = n1 - n;
         if (left > 0) {
-          if (mine0) put4<C32>(c[0], cut.wide, left, was[0], acc[0][0], acc[0][2], acc[1][0], acc[1][2]);
-          if (mine1) put4<C32>(c[1], cut.wide, left, was[1], acc[0][1], acc[0][3], acc[1][1], acc[1][3]);
+          if (mine0) put4<C32, WIDE>(c[0], left, four<C32, WIDE>(was[0], b[0]), acc[0][0], acc[0][2], acc[1][0], acc[1][2]);
+          if (mine1) put4<C32, WIDE>(c[1], left, four<C32, WIDE>(was[1], b[1]), acc[0][1], acc[0][3], acc[1][1], acc[1][3]);
         }
         n += WARPS * BN;
 #pragma unroll
@@ -402,12 +430,12 @@ __global__ void __launch_bounds__(THREADS, 2)
   if (p.C != p.base)
     for (int i = warp + WARPS * (int)blockIdx.y; i < TM; i += WARPS * (int)gridDim.y) {
       const int id = __shfl_sync(0xFFFFFFFFu, i < 32 ? id_lo : id_hi, i & 31);
-      if (id == -1) copy_row<C32>(p, cut.wide, m0 + i, n0, n1);
+      if (id == -1) copy_row<C32>(p, WIDE, m0 + i, n0, n1);
     }
   if (reading) cluster_wait();
 }
 
-template <bool C32>
+template <bool C32, bool WIDE>
 qw_status launch(const LoraArgs& a, cudaStream_t st) {
   const int sms = device_sm_count();
   const int64_t tiles = (a.M + TM - 1) / TM;
@@ -422,9 +450,6 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   const int parts = cut.csize * cut.nsplit;
   cut.k_len = ((a.K + cut.csize - 1) / cut.csize + 63) / 64 * 64;
   cut.n_len = (int32_t)((((int64_t)a.N + parts - 1) / parts + 63) / 64 * 64);
-  const int vec = C32 ? 4 : 8;
-  cut.wide = ((uintptr_t)a.C | (uintptr_t)a.base) % 16 == 0 && a.ldc % vec == 0 &&
-             (!a.base || a.ld_base % vec == 0);
   const int64_t x = tiles * parts;
   const int64_t y = std::max<int64_t>(1, std::min<int64_t>(groups, (4 * sms + x - 1) / x));
   if (x > 0x7FFFFFFF) return QW_ERR_UNSUPPORTED;
@@ -437,7 +462,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
     return QW_ERR_CUDA;
   static std::atomic<int> ready[64];
   if (once_per_device(ready, [&] {
-        return cudaFuncSetAttribute(lora_mma_kernel<C32>,
+        return cudaFuncSetAttribute(lora_mma_kernel<C32, WIDE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     RING + most.bytes()) == cudaSuccess;
       }) <= 0)
@@ -455,7 +480,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cut.csize > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, lora_mma_kernel<C32>, tmB, tmB32, a, cut) == cudaSuccess ? QW_OK : QW_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, lora_mma_kernel<C32, WIDE>, tmB, tmB32, a, cut) == cudaSuccess ? QW_OK : QW_ERR_CUDA;
 }
 
 }  // namespace
@@ -468,7 +493,11 @@ qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st) {
   // rank 64 277, 77).
   const bool many = a.M > 512 || (a.M > 128 && a.M > 2 * (int64_t)a.L) || (a.M > 16 && a.M > 12 * (int64_t)a.L);
   if (many && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
-  return c_f32 ? launch<true>(a, st) : launch<false>(a, st);
+  const int vec = c_f32 ? 4 : 8;
+  const bool wide = ((uintptr_t)a.C | (uintptr_t)a.base) % 16 == 0 && a.ldc % vec == 0 &&
+                    (!a.base || a.ld_base % vec == 0);  // base and C take 16-byte accesses
+  if (wide) return c_f32 ? launch<true, true>(a, st) : launch<false, true>(a, st);
+  return c_f32 ? launch<true, false>(a, st) : launch<false, false>(a, st);
 }
 
 }  // namespace qw

@@ -63,7 +63,14 @@ __device__ __forceinline__ void copy_row(const LoraArgs& p, bool wide, int64_t m
     }
     n = end;
   }
-  for (n += lane; n < n1; n += 32) c[n] = b ? b[n] : (T)0;
+  for (n += lane; n < n1; n += 8 * 32) {
+    T x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = b && n + i * 32 < n1 ? b[n + i * 32] : (T)0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (n + i * 32 < n1) c[n + i * 32] = x[i];
+  }
 }
 
 }  // namespace qw
