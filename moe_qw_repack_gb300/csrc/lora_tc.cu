@@ -27,8 +27,9 @@
 // share an item's columns, each with a t of its own, where that fills the SMs.  Every wait on a barrier is
 // bounded; on expiry the kernel reports QW_ERR_TIMEOUT and shuts down.
 // Bound by: an item's chain (list 2, X A^T and t 6 to 10, 2 us a tile and group) in small calls; in large ones
-// by L2 while all SMs read X and A (17 of 70 us for 4096 x 14336 x 4096, rank 64, where DRAM has little to do),
-// then by base and C through shared memory (5 TB/s), on 123 of 152 SMs there; 288 MB at 4.1 TB/s in all.
+// by L2 while all SMs read X and A, where DRAM has little to do (17 us of 4096 x 14336 x 4096, rank 64, with a CTA
+// on all of K, 6 with three and 5 to join), then by base and C through shared memory, on 123 of 152 SMs there:
+// 62 us, 288 MB at 4.6 TB/s in all.
 #include <algorithm>
 
 #include "int8_map.cuh"
@@ -58,7 +59,7 @@ constexpr int SEGS = WINDOW / 32;
 
 struct Params {
   LoraArgs a;
-  int32_t csize_log;
+  int32_t csize;
   int32_t parts;      // clusters that share an item's columns (each makes t for itself)
   int32_t k_stages;   // of a CTA's slice of K
   int32_t n_tiles;    // of a CTA's slice of N
@@ -262,9 +263,9 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
   volatile int* abort_flag = &abort_shared;
   const LoraArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int csize_log = p.csize_log, csize = 1 << csize_log;
-  const int crank = (int)(blockIdx.x & (unsigned)(csize - 1));
-  const unsigned cluster = blockIdx.x >> csize_log;
+  const int csize = p.csize;
+  const unsigned cluster = blockIdx.x / (unsigned)csize;
+  const int crank = (int)(blockIdx.x - cluster * (unsigned)csize);
   const unsigned window = cluster / (unsigned)p.parts;
   const int64_t m0 = (int64_t)window * WINDOW;
   const int share = (int)(cluster - window * (unsigned)p.parts) * csize + crank;  // of the columns
@@ -550,18 +551,21 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
       tc_fence_before();
     }
     if (csize > 1) {
-      const int each_log = 7 - csize_log, each = 1 << each_log;  // tokens that a CTA adds up
-      const int n4 = p.r16 / 4 * each;
+      // tokens that a CTA adds up, and the power of two they fit
+      const int each = (TT + csize - 1) / csize, each_log = 32 - __clz(each - 1);
+      const int n4 = p.r16 / 4 << each_log;
+      const int own = (65536 + each - 1) / each;  // row * own >> 16: the CTA that adds up the row
       cluster_sync();
       auto join = [&](auto most) {
         constexpr int MOST = decltype(most)::value;  // of a thread
         float v[MOST][4];
 #pragma unroll
         for (int q = 0; q < MOST; ++q) {
-          const int i = e + q * GROUP_THREADS, r = (i >> each_log) * 4, mine = crank * each + (i & (each - 1));
+          const int i = e + q * GROUP_THREADS, r = (i >> each_log) * 4, of = i & ((1 << each_log) - 1);
+          const int mine = crank * each + of;
           const uint32_t at = smem_u32(s_t) + (uint32_t)((i >> each_log) * TT + mine) * 16;
           float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (worker && i < n4 && mine < now) {
+          if (worker && i < n4 && of < each && mine < now) {
             uint4 x[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) x[c] = c < csize ? ld_cluster_u32x4(mapa_shared(at, c)) : zero4();
@@ -579,14 +583,14 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
         cluster_sync();  // all sums have been read
 #pragma unroll
         for (int q = 0; q < MOST; ++q) {
-          const int i = e + q * GROUP_THREADS, mine = crank * each + (i & (each - 1));
-          if (worker && i < n4 && mine < now) put_t<NS>(s_t, p.r_slots, mine, (i >> each_log) * 4, v[q]);
+          const int i = e + q * GROUP_THREADS, of = i & ((1 << each_log) - 1), mine = crank * each + of;
+          if (worker && i < n4 && of < each && mine < now) put_t<NS>(s_t, p.r_slots, mine, (i >> each_log) * 4, v[q]);
         }
       };
       if (n4 <= GROUP_THREADS)
         join(std::integral_constant<int, 1>{});
       else
-        join(std::integral_constant<int, TT * 256 / 4 / 4 / GROUP_THREADS>{});  // (two CTAs with 128 r, or four)
+        join(std::integral_constant<int, TT * 256 / 4 / 4 / GROUP_THREADS>{});  // (two or three CTAs with 128 r, or more)
       cluster_sync();
       if (worker) {  // the tokens' rows to all their places, eight threads a row
         const int chunk = (e & 7) ^ (e >> 3 & 7);  // (rows 32 apart are swizzled alike)
@@ -597,13 +601,13 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int row = (e >> 3) + 32 * q;
-            if (row < now) x[q] = ld_cluster_u32x4(mapa_shared(smem_u32(to + q * 32 * 128), row >> each_log));
+            if (row < now) x[q] = ld_cluster_u32x4(mapa_shared(smem_u32(to + q * 32 * 128), row * own >> 16));
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int row = (e >> 3) + 32 * q;
             if (row < now)
-              for (int r = row >> each_log == crank ? row + span : row; r < TT; r += span)
+              for (int r = row * own >> 16 == crank ? row + span : row; r < TT; r += span)
                 *reinterpret_cast<uint4*>(to + (r - (e >> 3)) * 128) = x[q];
           }
         }
@@ -773,8 +777,8 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
       if (p.wide && span == TT && count > 0) {
         // A whole share of rows that 16-byte accesses fit, 128 bytes of each at a time.  Where the tokens stand
         // together by TMA: a box of base may reach past them; C takes a box of 32 rows, or boxes of 8 and what
-        // is left in pieces.  Others in pieces (in units of 64 bytes, four under way: 84 us instead of 67 where
-        // 128 tokens of 4096 x 14336 x 4096 do not stand together).
+        // is left in pieces.  Others in pieces (in units of 64 bytes, four under way: 84 us instead of 74 where
+        // some 128 tokens of 4096 x 14336 x 4096 do not stand together).
         const bool tma = plan.row[t0 + count - 1] - plan.row[t0] == count - 1;
         constexpr int COLS = BOX_ROW / SIZE, PER = 64 / COLS;  // columns of a box, boxes of a tile
         const int32_t y = (int32_t)m0 + plan.row[t0];
@@ -1045,23 +1049,31 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   p.first_bytes = p.t_bytes + p.units * UNITS;
   if (p.first_bytes / stage1 < 2 || p.s2 < 1) return QW_ERR_UNSUPPORTED;
   // The cheapest cluster and number of clusters on an item's columns, in rounds of what runs at once (a cluster
-  // lies within one GPC) of what an item takes, in us: to find, to join, each CTA's stages and tiles.  What is past
-  // one round starts late.  The items: 128 tokens each, and a part of that for each adapter.  (us measured,
-  // cluster x clusters: 4096 x 14336 x 4096 rank 64 in runs of 8 adapters 2x1 86, 4x1 76, 2x2 72, [1x3] 70, 1x4
-  // 77, 8x1 86; 2048 mixed tokens of 8, 4096 x 4096 rank 16 2x1 42, [4x1] 28, 2x2 31, 8x1 48; 256 tokens of 64,
-  // rank 32 1x1 48, [2x1] 32, 4x1 40; 128 of one, rank 64 4x1 27, 8x1 18, 8x2 16, [8x4] 15.)
+  // lies within one GPC: 152, 76, 46, 36 and 15 of them) of what an item takes, in us: to find, to join, each
+  // CTA's stages and tiles.  What is past one round starts late.  The items: 128 tokens each, and a part of that
+  // for each adapter.  (us measured, cluster x clusters: 4096 x 14336 x 4096 rank 64 in runs of 8 adapters 1x3
+  // 69, 2x2 72, [3x1] 64, 4x1 76, 8x1 87; 2048 mixed tokens of 8, 4096 x 4096 rank 16 2x1 39, 3x1 31, [4x1] 26,
+  // 8x1 49; 256 tokens of 64, rank 32 1x1 48, [2x1] 31, 3x1 48; 128 of one, rank 64 4x1 25, 8x1 18, 8x2 16, [8x4]
+  // 15.)
   const double items = (double)((a.M + TT - 1) / TT) + 1 + std::min<int64_t>(a.L, a.M);
+  constexpr struct {
+    int csize;
+    double sms;  // of all
+  } sizes[] = {{1, 1.0}, {2, 1.0}, {3, 0.9}, {4, 0.94}, {8, 0.79}};
   double least = 1e30;
-  for (int log = 0; log <= 3; ++log)
+  for (const auto& size : sizes)
     for (int parts = 1; parts <= 8; ++parts) {
-      const int64_t c = (int64_t)1 << log, shares = c * parts;
-      if ((c > 1 && c > all_k && c > all_tiles) || (c == 2 && a.R > 128) || (parts > 1 && shares > all_tiles)) continue;
-      const double rounds = items * shares / (sms * (c == 8 ? 0.79 : c == 4 ? 0.9 : 1.0));
+      const int c = size.csize;
+      const int64_t shares = (int64_t)c * parts;
+      if ((c > 1 && c > all_k && c > all_tiles) || ((c == 2 || c == 3) && a.R > 128) ||
+          (parts > 1 && shares > all_tiles))
+        continue;
+      const double rounds = items * shares / (sms * size.sms);
       const double cost = (rounds <= 1 ? 1 : rounds + 0.25) * (6 + (c > 1 ? 5 : 0) + (all_k + c - 1) / c * 0.3 +
                                                                (all_tiles + shares - 1) / shares * 1.7);
-      if (cost < least) least = cost, p.csize_log = log, p.parts = parts;
+      if (cost < least) least = cost, p.csize = c, p.parts = parts;
     }
-  const int csize = 1 << p.csize_log;
+  const int csize = p.csize;
   p.k_stages = (int32_t)((all_k + csize - 1) / csize);
   const int shares = csize * p.parts;
   p.n_tiles = (int32_t)((all_tiles + shares - 1) / shares);
