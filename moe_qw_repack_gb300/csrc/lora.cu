@@ -493,10 +493,7 @@ qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st) {
   // runs, N = 14336, rank 64 277, 62).
   const bool many = a.M > 512 || (a.M > 128 && a.M > 2 * (int64_t)a.L) || (a.M > 16 && a.M > 12 * (int64_t)a.L);
   if (many && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
-  const int vec = c_f32 ? 4 : 8;
-  const bool wide = ((uintptr_t)a.C | (uintptr_t)a.base) % 16 == 0 && a.ldc % vec == 0 &&
-                    (!a.base || a.ld_base % vec == 0);  // base and C take 16-byte accesses
-  if (wide) return c_f32 ? launch<true, true>(a, st) : launch<false, true>(a, st);
+  if (lora_wide(a, c_f32)) return c_f32 ? launch<true, true>(a, st) : launch<false, true>(a, st);
   return c_f32 ? launch<true, false>(a, st) : launch<false, false>(a, st);
 }
 

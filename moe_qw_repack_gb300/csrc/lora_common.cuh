@@ -73,4 +73,10 @@ __device__ __forceinline__ void copy_row(const LoraArgs& p, bool wide, int64_t m
   }
 }
 
+// Whether base and C take 16-byte accesses.
+inline bool lora_wide(const LoraArgs& a, bool c_f32) {
+  const int vec = c_f32 ? 4 : 8;
+  return ((uintptr_t)a.C | (uintptr_t)a.base) % 16 == 0 && a.ldc % vec == 0 && (!a.base || a.ld_base % vec == 0);
+}
+
 }  // namespace qw

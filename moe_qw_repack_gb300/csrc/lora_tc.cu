@@ -69,7 +69,6 @@ struct Params {
   int32_t t_bytes;
   int32_t first_bytes;  // t and the units; before them the first product's stages
   int32_t units;      // of a warp
-  bool wide;           // base and C take 16-byte accesses
 };
 
 // X in boxes of 64 k and 8, 32 or 128 rows
@@ -240,7 +239,7 @@ struct Plan {
   int64_t off_c[TT], off_b[TT];  // bytes to the tokens' rows of C and base
 };
 
-template <bool C32>
+template <bool C32, bool WIDE>  // (WIDE: base and C take 16-byte accesses)
 __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they are shared out by four)
     lora_tc_kernel(const __grid_constant__ Rows tmX, const __grid_constant__ CUtensorMap tmA,
                    const __grid_constant__ CUtensorMap tmB,
@@ -271,22 +270,22 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
   const int share = (int)(cluster - window * (unsigned)p.parts) * csize + crank;  // of the columns
   const int win = (int)min64(WINDOW, a.M - m0);
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < MAX_STAGES; ++s) {
-      mbar_init(&full1[s], 2);  // A and X
-      mbar_init(&landed[s], GROUP_THREADS);
-      mbar_init(&empty1[s], 1);
-      mbar_init(&full2[s], 1);
-      mbar_init(&empty2[s], 1);
+  if (warp == 0) {  // (a lane a few barriers each: one after the other they take 0.4 us)
+    if (lane < MAX_STAGES) {
+      mbar_init(&full1[lane], 2);  // A and X
+      mbar_init(&landed[lane], GROUP_THREADS);
+      mbar_init(&empty1[lane], 1);
+      mbar_init(&full2[lane], 1);
+      mbar_init(&empty2[lane], 1);
+    } else if (lane < MAX_STAGES + ACCS) {
+      mbar_init(&acc_full[lane - MAX_STAGES], 1);
+      mbar_init(&acc_empty[lane - MAX_STAGES], GROUP_WARPS);
+    } else if (lane == 31) {
+      mbar_init(&d1_full, 1);
+      mbar_init(&final_bar, 1);
+      abort_shared = 0;
     }
-    mbar_init(&d1_full, 1);
-    for (int w = 0; w < EPI_WARPS * MAX_UNITS; ++w) mbar_init(&base_full[0][0] + w, 1);
-    mbar_init(&final_bar, 1);
-    for (int b = 0; b < ACCS; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], GROUP_WARPS);
-    }
-    abort_shared = 0;
+    for (int w = lane; w < EPI_WARPS * MAX_UNITS; w += 32) mbar_init(&base_full[0][0] + w, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -688,7 +687,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
       // Rows that 16-byte accesses do not fit: base comes in the 16-byte pieces that it lies in (one more than
       // its length, an odd number: lanes that hold a row each meet different banks), C goes in words.
       const int words_log = row_log - 2, pitch = (1 << row_log) + 16;
-      const int place_bytes = p.wide ? 1 << (rows_log + row_log) : pitch << rows_log;
+      const int place_bytes = WIDE ? 1 << (rows_log + row_log) : pitch << rows_log;
       int depth = 1;
       while (depth < 8 && 2 * depth * place_bytes <= p.units * UNIT_BYTES) depth *= 2;
       if (depth == 2 && 3 * place_bytes <= p.units * UNIT_BYTES) depth = 3;
@@ -709,7 +708,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
           const int32_t n0 = column(unit);
           const uint8_t* from = static_cast<const uint8_t*>(a.base) + (int64_t)n0 * SIZE;
           const int left = min(cols, a.N - n0) * SIZE;  // bytes of a row
-          if (p.wide) {
+          if constexpr (WIDE) {
             int64_t off[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) off[i] = plan.off_b[t0 + min(row1 + i * rows1, count - 1)];
@@ -719,15 +718,19 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
                 cp_async16(to + piece(row1 + i * rows1, piece1), from + off[i] + piece1 * 16,
                            min(16, left - piece1 * 16));
           } else if (left > 0) {  // (whole pieces, whosever the ends of the first and the last are)
-            auto get = [&](int r, int j) {
-              const uint8_t* x = from + plan.off_b[t0 + r];
-              const int shift = (int)((uintptr_t)x & 15);
-              if (16 * j < left + shift) cp_async16(to + r * pitch + 16 * j, x - shift + 16 * j);
-            };
+            // (all offsets before the first copy: nothing is read across one)
+            const uint8_t* x[5];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (row1 + i * rows1 < count) get(row1 + i * rows1, piece1);
-            if (lane < count) get(lane, 1 << pieces_log);
+            for (int i = 0; i < 5; ++i) {
+              const int r = i < 4 ? row1 + i * rows1 : lane;
+              x[i] = from + plan.off_b[t0 + min(r, count - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+              const int r = i < 4 ? row1 + i * rows1 : lane, at = 16 * (i < 4 ? piece1 : 1 << pieces_log);
+              const int shift = (int)((uintptr_t)x[i] & 15);
+              if (r < count && at < left + shift) cp_async16(to + r * pitch + at, x[i] - shift + at);
+            }
           }
         }
         cp_async_commit();
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
         const uint8_t* from = mine + slot * place_bytes;
         const int32_t n0 = column(unit);
         uint8_t* to = static_cast<uint8_t*>(a.C) + (int64_t)n0 * SIZE;
-        if (p.wide) {
+        if constexpr (WIDE) {
           const int left = a.N - n0 - piece1 * EACH;
           int64_t off[4];
           uint4 x[4];
@@ -753,14 +756,20 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
           }
         } else {
           const int left = min(cols, a.N - n0) * SIZE;
-#pragma unroll 8
-          for (int i = 0; i < 16; ++i) {  // (16 words a row: two rows at a time; eight: four)
-            const int r = (lane >> words_log) + i * rows2;
-            if (r >= count) break;
-            const uint32_t x = *reinterpret_cast<const uint32_t*>(from + r * pitch + 4 * word1);
-            uint8_t* row = to + plan.off_c[t0 + r];
-            const int at = 4 * word1 - (int)((uintptr_t)row & 3);  // in the unit's row
-            if (at >= 0 && at + 4 <= left) *reinterpret_cast<uint32_t*>(row + at) = x;
+          for (int r0 = lane >> words_log; r0 < count; r0 += 8 * rows2) {
+            uint8_t* row[8];
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = min(r0 + i * rows2, count - 1);
+              row[i] = to + plan.off_c[t0 + r];
+              x[i] = *reinterpret_cast<const uint32_t*>(from + r * pitch + 4 * word1);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int at = 4 * word1 - (int)((uintptr_t)row[i] & 3);  // in the unit's row
+              if (r0 + i * rows2 < count && at >= 0 && at + 4 <= left) *reinterpret_cast<uint32_t*>(row[i] + at) = x[i];
+            }
           }
           if (!C32 && lane < count && left > 0) {  // halves of words at the ends
             uint8_t* row = to + plan.off_c[t0 + lane];
@@ -774,7 +783,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
       };
       const uint32_t lanes = (uint32_t)(32 * quad) << 16;
       const int my_row = lane & ((1 << rows_log) - 1);
-      if (p.wide && span == TT && count > 0) {
+      if (WIDE && span == TT && count > 0) {
         // A whole share of rows that 16-byte accesses fit, 128 bytes of each at a time.  Where the tokens stand
         // together by TMA: a box of base may reach past them; C takes a box of 32 rows, or boxes of 8 and what
         // is left in pieces.  Others in pieces (in units of 64 bytes, four under way: 84 us instead of 74 where
@@ -798,11 +807,17 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
             const uint8_t* from = static_cast<const uint8_t*>(a.base) + (int64_t)n * SIZE + 16 * j;
             if (in && left > 0) {
 #pragma unroll
-              for (int i = 0; i < PIECES; ++i) {
-                const int r = lane / PIECES + 32 / PIECES * i;
-                if (r < count)
-                  cp_async16(mine + slot * UNIT_BYTES + r * BOX_ROW + ((j ^ (r & 7)) << 4), from + plan.off_b[t0 + r],
-                             min(16, left));
+              for (int h = 0; h < PIECES; h += 4) {
+                int64_t off[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) off[i] = plan.off_b[t0 + min(lane / PIECES + 32 / PIECES * (h + i), count - 1)];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int r = lane / PIECES + 32 / PIECES * (h + i);
+                  if (r < count)
+                    cp_async16(mine + slot * UNIT_BYTES + r * BOX_ROW + ((j ^ (r & 7)) << 4), from + off[i],
+                               min(16, left));
+                }
               }
             }
             cp_async_commit();
@@ -917,7 +932,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
             __syncwarp();  // the unit's base is there
             uint8_t* at = mine + slot * place_bytes;
             const uint32_t d2 = tbase + lanes + buf * BN + col0 + ((unit & last) << cols_log);
-            if (p.wide) {
+            if constexpr (WIDE) {
               for (int c = 0; c < cols; c += 16) {
                 float d[16];
                 uint4 was[16 / EACH];
@@ -997,7 +1012,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
   if (a.C != a.base) {  // the rows without adapter
     const int32_t n0 = tile0 * BN, n1 = min(a.N, (tile0 + tiles) * BN);
     for (int i = (int)(blockIdx.y + gridDim.y * warp); i < win; i += (int)gridDim.y * WARPS)
-      if (plan.ids[i] == -1) copy_row<C32>(a, p.wide, m0 + i, n0, n1);
+      if (plan.ids[i] == -1) copy_row<C32>(a, WIDE, m0 + i, n0, n1);
   }
   // After a wait that gave up, copies may still be under way to the rings: they have this long.
   if (*abort_flag && threadIdx.x == 0)
@@ -1022,13 +1037,13 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
 
 constexpr int kSmemCta = 232448;  // of one CTA
 
-template <bool C32>
+template <bool C32, bool WIDE>
 qw_status launch(const LoraArgs& a, cudaStream_t st) {
   constexpr int NS = C32 ? 3 : 2;
   static std::atomic<int> fixed_smem[64];
   const int fixed = once_per_device(fixed_smem, [] {
     cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, lora_tc_kernel<C32>) == cudaSuccess ? (int)fa.sharedSizeBytes + 1 : 0;
+    return cudaFuncGetAttributes(&fa, lora_tc_kernel<C32, WIDE>) == cudaSuccess ? (int)fa.sharedSizeBytes + 1 : 0;
   }) - 1;
   if (fixed < 0) return QW_ERR_CUDA;
   const int sms = device_sm_count();
@@ -1077,9 +1092,6 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   p.k_stages = (int32_t)((all_k + csize - 1) / csize);
   const int shares = csize * p.parts;
   p.n_tiles = (int32_t)((all_tiles + shares - 1) / shares);
-  const int vec = C32 ? 4 : 8;
-  p.wide = ((uintptr_t)a.C | (uintptr_t)a.base) % 16 == 0 && a.ldc % vec == 0 &&
-           (!a.base || a.ld_base % vec == 0);
   CUtensorMap tmA, tmB;
   Rows tmX;
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1089,7 +1101,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   for (int i = 0; i < 3; ++i)
     if (!encode_int8_2d(&tmX.map[i], bf16, a.X, a.K, a.M, (uint64_t)a.ldx * 2, BK, 8u << (2 * i))) return QW_ERR_CUDA;
   CUtensorMap tmBase{}, tmC[2]{};
-  if (p.wide) {
+  if constexpr (WIDE) {
     const auto type = C32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf16;
     constexpr int SIZE = C32 ? 4 : 2;
     constexpr uint32_t cols = BOX_ROW / SIZE, rows[2] = {32, 8};
@@ -1102,7 +1114,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   }
   static std::atomic<int> ready[64];
   if (once_per_device(ready, [=] {
-        return cudaFuncSetAttribute(lora_tc_kernel<C32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(lora_tc_kernel<C32, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kSmemCta - fixed) == cudaSuccess;
       }) <= 0)
     return QW_ERR_CUDA;
@@ -1122,7 +1134,7 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = csize > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, lora_tc_kernel<C32>, tmX, tmA, tmB, tmBase, tmC[0], tmC[1], p) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, lora_tc_kernel<C32, WIDE>, tmX, tmA, tmB, tmBase, tmC[0], tmC[1], p) == cudaSuccess
              ? QW_OK
              : QW_ERR_CUDA;
 }
@@ -1137,7 +1149,8 @@ bool lora_tc_takes(const LoraArgs& a, bool c_f32) {
 }
 
 qw_status launch_lora_tc(const LoraArgs& a, bool c_f32, cudaStream_t st) {
-  return c_f32 ? launch<true>(a, st) : launch<false>(a, st);
+  if (lora_wide(a, c_f32)) return c_f32 ? launch<true, true>(a, st) : launch<false, true>(a, st);
+  return c_f32 ? launch<true, false>(a, st) : launch<false, false>(a, st);
 }
 
 }  // namespace qw
