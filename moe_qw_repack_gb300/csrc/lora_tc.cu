@@ -803,21 +803,15 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
             }
             __syncwarp();
           } else {
-            const int j = lane % PIECES, left = (a.N - n) * SIZE - 16 * j;  // bytes of the row from here
+            const int j = lane % PIECES, left = min(COLS, a.N - n) * SIZE - 16 * j;  // bytes of the row from here
             const uint8_t* from = static_cast<const uint8_t*>(a.base) + (int64_t)n * SIZE + 16 * j;
             if (in && left > 0) {
 #pragma unroll
-              for (int h = 0; h < PIECES; h += 4) {
-                int64_t off[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) off[i] = plan.off_b[t0 + min(lane / PIECES + 32 / PIECES * (h + i), count - 1)];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int r = lane / PIECES + 32 / PIECES * (h + i);
-                  if (r < count)
-                    cp_async16(mine + slot * UNIT_BYTES + r * BOX_ROW + ((j ^ (r & 7)) << 4), from + off[i],
-                               min(16, left));
-                }
+              for (int i = 0; i < PIECES; ++i) {
+                const int r = lane / PIECES + 32 / PIECES * i;
+                if (r < count)
+                  cp_async16(mine + slot * UNIT_BYTES + r * BOX_ROW + ((j ^ (r & 7)) << 4), from + plan.off_b[t0 + r],
+                             min(16, left));
               }
             }
             cp_async_commit();
@@ -825,96 +819,85 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
         };
         fence_proxy_async_smem();  // (an item before may have written the place in pieces)
         __syncwarp();
-        for (int d = 0; d < p.units; ++d) fetch(d, d);
         int slot = 0;
-        // With two places the next unit is asked for before this one is waited for, as soon as the store of the one
-        // before has read its place.  (After this one: 77 us instead of 73 for 4096 x 14336 x 4096.)
-        auto ahead = [&](int unit, int slot) {
-          if (p.units == MAX_UNITS && unit > 0) {
+        for (int unit = 0; unit < my_tiles * PER; ++unit) {
+          const int k = unit / PER, u = unit % PER;
+          const uint32_t v = ua + (uint32_t)(2 * k + group), buf = v % ACCS;
+          // With two places the next unit is asked for before this one is waited for, as soon as the store of the
+          // one before has read its place.  (After this one: 77 us instead of 73 for 4096 x 14336 x 4096.)
+          if (unit > 0) {
             tma_store_read();
             __syncwarp();
-            fetch(unit + 1, slot ^ 1);
           }
-        };
-        for (int k = 0; k < my_tiles; ++k) {
-          const uint32_t v = ua + (uint32_t)(2 * k + group), buf = v % ACCS;
-          ahead(k * PER, slot);
-          if (ok) ok = warp_wait(&acc_full[buf], v / ACCS & 1u, abort_flag, a.err);
-          tc_fence_after();
-#pragma unroll 1
-          for (int u = 0; u < PER; ++u) {
-            const int32_t n = (tile0 + 2 * k + group) * BN + col0 + u * COLS;
-            if (u > 0) ahead(k * PER + u, slot);
-            if (n >= a.N) {
-              if (u == PER - 1) {
-                tc_fence_before();
-                __syncwarp();
-                if (leader) mbar_arrive(&acc_empty[buf]);
-              }
-              continue;
-            }
-            if (a.base) {
-              if (tma) {
-                if (ok) ok = warp_wait(&base_full[ew][slot], base_phase >> slot & 1u, abort_flag, a.err);
-                base_phase ^= 1u << slot;
-              } else {
-                if (p.units == MAX_UNITS)
-                  cp_async_wait<MAX_UNITS - 1>();
-                else
-                  cp_async_wait<0>();
-                __syncwarp();
-              }
-            }
-            uint8_t* const box = mine + slot * UNIT_BYTES;
-            uint8_t* const at = box + lane * BOX_ROW;
-            const int sw = lane & 7;  // the box's swizzle
-            constexpr int STEP = COLS < 32 ? COLS : 32;
-#pragma unroll 1
-            for (int c = 0; c < COLS; c += STEP) {
-              float d[STEP];
-              uint4 was[STEP / EACH];
-              tc_ld<STEP>(tbase + ((uint32_t)(32 * quad) << 16) + buf * BN + col0 + u * COLS + c, d);
-#pragma unroll
-              for (int j = 0; j < STEP / EACH; ++j)
-                was[j] = a.base ? *reinterpret_cast<const uint4*>(at + (((c / EACH + j) ^ sw) << 4)) : zero4();
-              tc_landed(d);
-              if (u == PER - 1 && c + STEP == COLS) {  // D2 has been read
-                tc_fence_before();
-                __syncwarp();
-                if (leader) mbar_arrive(&acc_empty[buf]);
-              }
-#pragma unroll
-              for (int j = 0; j < STEP / EACH; ++j)
-                *reinterpret_cast<uint4*>(at + (((c / EACH + j) ^ sw) << 4)) = add_piece<C32>(was[j], d + j * EACH);
-            }
-            const int eights = tma ? count / 8 : 0;
-            if (8 * eights < count) {
+          for (int d = unit == 0 ? 0 : p.units - 1; d < p.units; ++d)  // (one copy of the code: it is long as it is)
+            fetch(unit + d, slot + d < p.units ? slot + d : slot + d - p.units);
+          if (u == 0) {
+            if (ok) ok = warp_wait(&acc_full[buf], v / ACCS & 1u, abort_flag, a.err);
+            tc_fence_after();
+          }
+          const int32_t n = (tile0 + 2 * k + group) * BN + col0 + u * COLS;
+          if (n >= a.N) {
+            if (u == PER - 1) {
+              tc_fence_before();
               __syncwarp();
-#pragma unroll 4
-              for (int q = 8 * eights * PIECES + lane; q < count * PIECES; q += 32) {
-                const int r = q / PIECES, j = q % PIECES, left = a.N - n - j * EACH;
-                const uint4 x = *reinterpret_cast<const uint4*>(
-                    box + r * BOX_ROW + ((j ^ (r & 7)) << 4));
-                put_piece<C32>(static_cast<uint8_t*>(a.C) + plan.off_c[t0 + r] + (int64_t)(n + j * EACH) * SIZE, x,
-                               left);
-              }
+              if (leader) mbar_arrive(&acc_empty[buf]);
             }
-            if (tma) fence_proxy_async_smem();
-            __syncwarp();
-            if (tma && count == 32) {
-              if (leader && ok) tma_store_2d(&tmC, box, n, y);
-            } else if (lane < eights && ok) {
-              tma_store_2d(&tmC8, box + lane * 8 * BOX_ROW, n, y + 8 * lane);
-            }
-            tma_store_commit();
-            if (p.units == 1) {
-              tma_store_read();
-              __syncwarp();
-              fetch(k * PER + u + 1, 0);
+            continue;
+          }
+          if (a.base) {
+            if (tma) {
+              if (ok) ok = warp_wait(&base_full[ew][slot], base_phase >> slot & 1u, abort_flag, a.err);
+              base_phase ^= 1u << slot;
             } else {
-              slot ^= 1;
+              if (p.units == MAX_UNITS)
+                cp_async_wait<MAX_UNITS - 1>();
+              else
+                cp_async_wait<0>();
+              __syncwarp();
             }
           }
+          uint8_t* const box = mine + slot * UNIT_BYTES;
+          uint8_t* const at = box + lane * BOX_ROW;
+          const int sw = lane & 7;  // the box's swizzle
+          constexpr int STEP = COLS < 32 ? COLS : 32;
+#pragma unroll 1
+          for (int c = 0; c < COLS; c += STEP) {
+            float d[STEP];
+            uint4 was[STEP / EACH];
+            tc_ld<STEP>(tbase + ((uint32_t)(32 * quad) << 16) + buf * BN + col0 + u * COLS + c, d);
+#pragma unroll
+            for (int j = 0; j < STEP / EACH; ++j)
+              was[j] = a.base ? *reinterpret_cast<const uint4*>(at + (((c / EACH + j) ^ sw) << 4)) : zero4();
+            tc_landed(d);
+            if (u == PER - 1 && c + STEP == COLS) {  // D2 has been read
+              tc_fence_before();
+              __syncwarp();
+              if (leader) mbar_arrive(&acc_empty[buf]);
+            }
+#pragma unroll
+            for (int j = 0; j < STEP / EACH; ++j)
+              *reinterpret_cast<uint4*>(at + (((c / EACH + j) ^ sw) << 4)) = add_piece<C32>(was[j], d + j * EACH);
+          }
+          const int eights = tma ? count / 8 : 0;
+          if (8 * eights < count) {
+            __syncwarp();
+            for (int q = 8 * eights * PIECES + lane; q < count * PIECES; q += 32) {
+              const int r = q / PIECES, j = q % PIECES, left = a.N - n - j * EACH;
+              const uint4 x = *reinterpret_cast<const uint4*>(
+                  box + r * BOX_ROW + ((j ^ (r & 7)) << 4));
+              put_piece<C32>(static_cast<uint8_t*>(a.C) + plan.off_c[t0 + r] + (int64_t)(n + j * EACH) * SIZE, x,
+                             left);
+            }
+          }
+          if (tma) fence_proxy_async_smem();
+          __syncwarp();
+          if (tma && count == 32) {
+            if (leader && ok) tma_store_2d(&tmC, box, n, y);
+          } else if (lane < eights && ok) {
+            tma_store_2d(&tmC8, box + lane * 8 * BOX_ROW, n, y + 8 * lane);
+          }
+          tma_store_commit();
+          if (++slot == p.units) slot = 0;
         }
         tma_store_done();
         cp_async_wait<0>();
