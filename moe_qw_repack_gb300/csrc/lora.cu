@@ -415,8 +415,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         const int32_t left = n1 - n;
         if (left > 0) {
-          if (mine0) put4<C32, WIDE>(c[0], left, four<C32, WIDE>(was[0], b[0]), acc[0][0], acc[0][2], acc[1][0], acc[1][2]);
-          if (mine1) put4<C32, WIDE>(c[1], left, four<C32, WIDE>(was[1], b[1]), acc[0][1], acc[0][3], acc[1][1], acc[1][3]);
+          if (mine0)
+            put4<C32, WIDE>(c[0], left, four<C32, WIDE>(was[0], b[0]), acc[0][0], acc[0][2], acc[1][0], acc[1][2]);
+          if (mine1)
+            put4<C32, WIDE>(c[1], left, four<C32, WIDE>(was[1], b[1]), acc[0][1], acc[0][3], acc[1][1], acc[1][3]);
         }
         n += WARPS * BN;
 #pragma unroll

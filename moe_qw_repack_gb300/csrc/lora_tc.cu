@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
       if (n4 <= GROUP_THREADS)
         join(std::integral_constant<int, 1>{});
       else
-        join(std::integral_constant<int, TT * 256 / 4 / 4 / GROUP_THREADS>{});  // (two or three CTAs with 128 r, or more)
+        // (two or three CTAs with 128 r, or more)
+        join(std::integral_constant<int, TT * 256 / 4 / 4 / GROUP_THREADS>{});
       cluster_sync();
       if (worker) {  // the tokens' rows to all their places, eight threads a row
         const int chunk = (e & 7) ^ (e >> 3 & 7);  // (rows 32 apart are swizzled alike)
@@ -1128,7 +1129,8 @@ qw_status launch(const LoraArgs& a, cudaStream_t st) {
 // 128 ranks leaves the rings no room.
 bool lora_tc_takes(const LoraArgs& a, bool c_f32) {
   return (int64_t)a.L * a.R <= kInt8MaxN && (int64_t)a.L * a.N <= kInt8MaxN &&
-         a.ldx < ((int64_t)1 << 38) && a.ldc < ((int64_t)1 << 37) && a.ld_base < ((int64_t)1 << 37) && !(c_f32 && a.R > 128);
+         a.ldx < ((int64_t)1 << 38) && a.ldc < ((int64_t)1 << 37) && a.ld_base < ((int64_t)1 << 37) &&
+         !(c_f32 && a.R > 128);
 }
 
 qw_status launch_lora_tc(const LoraArgs& a, bool c_f32, cudaStream_t st) {

@@ -131,7 +131,7 @@ def test_shapes(M, N, K, L, R, c, runs):
 # and many, K of one stage and of many
 MORE = [(1100, 600, 640, 700, 16), (513, 264, 264, 2, 200), (40, 136, 64, 1, 256), (1023, 8, 136, 2, 40),
         (515, 1000, 1032, 1, 64), (2048, 520, 264, 40, 40), (130, 9000, 64, 1, 16), (700, 4096, 4096, 1, 64),
-        (520, 130, 8, 5, 136), (257, 2000, 2048, 6, 8)]
+        (520, 130, 8, 5, 136), (257, 2000, 2048, 6, 8), (4096, 2048, 2048, 8, 64), (3000, 1001, 1032, 20, 128)]
 
 
 @pytest.mark.parametrize("M,N,K,L,R", MORE)
