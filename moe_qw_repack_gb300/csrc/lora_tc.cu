@@ -879,7 +879,9 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
             for (int j = 0; j < STEP / EACH; ++j)
               *reinterpret_cast<uint4*>(at + (((c / EACH + j) ^ sw) << 4)) = add_piece<C32>(was[j], d + j * EACH);
           }
-          const int eights = tma ? count / 8 : 0;
+          // (a box's last columns are stored in whole 16 bytes: not where the row ends within them)
+          const bool boxed = tma && (n + COLS <= a.N || a.N % EACH == 0);
+          const int eights = boxed ? count / 8 : 0;
           if (8 * eights < count) {
             __syncwarp();
             for (int q = 8 * eights * PIECES + lane; q < count * PIECES; q += 32) {
@@ -892,7 +894,7 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
           }
           if (tma) fence_proxy_async_smem();
           __syncwarp();
-          if (tma && count == 32) {
+          if (boxed && count == 32) {
             if (leader && ok) tma_store_2d(&tmC, box, n, y);
           } else if (lane < eights && ok) {
             tma_store_2d(&tmC8, box + lane * 8 * BOX_ROW, n, y + 8 * lane);

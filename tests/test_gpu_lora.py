@@ -160,6 +160,16 @@ def test_runs_of_every_length(c, most):
         check(got, reference(x, a, b, scales, ranks, ids, y), c, none, y)
 
 
+@pytest.mark.parametrize("M", [5, 70, 300, 1166])
+@pytest.mark.parametrize("N,pad", [(7, 1), (132, 4), (131, 5), (66, 6), (1153, 7), (127, 1), (190, 2)])
+@pytest.mark.parametrize("c", ["bf16", "f32"])
+def test_rows_that_end_within_16_bytes(M, N, pad, c):
+    """What lies behind them, up to the pitch, stays as it was."""
+    for in_place in (False, True):
+        run_and_check(M, N, 136, 2, 16, c, M + N, True, pad_c=pad, in_place=in_place)
+    run_and_check(M, N, 136, 2, 16, c, M + N, True, pad_c=pad, base=False)
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 200, 600])
 @pytest.mark.parametrize("c", ["bf16", "f32"])
 def test_strides_and_alignment(M, c):
