@@ -492,7 +492,7 @@ qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st) {
   // be one adapter's (us here and there, K = 4096: 32 tokens of one adapter, N = 4096, rank 64 22, 13; of two,
   // N = 14336, rank 16 17, 15; 96 of 8, N = 4096, rank 16 12, 13; 128 of 8, N = 14336, rank 64 27, 24; 192 of 32,
   // N = 4096, rank 32 27, 20; 192 of 64, rank 64 46, 34; 256 of 300, rank 16 52, 90 and 512 98, 93; 4096 of 8 in
-  // runs, N = 14336, rank 64 277, 62).
+  // runs, N = 14336, rank 64 277, 59).
   const bool many = a.M > 512 || (a.M > 128 && a.M > 2 * (int64_t)a.L) || (a.M > 16 && a.M > 12 * (int64_t)a.L);
   if (many && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
   if (lora_wide(a, c_f32)) return c_f32 ? launch<true, true>(a, st) : launch<false, true>(a, st);
