@@ -531,7 +531,8 @@ qw_status qw_rmsnorm(int32_t x_type, const void* X, int64_t ldx, int32_t r_type,
  *   then taken as one without adapter.
  *   K % 8 == 0, R % 8 == 0, R <= 256, M <= 2^26, N and K <= 2^30 (else QW_ERR_UNSUPPORTED).  X, A, B
  *   and the pitch of X 16-byte aligned, base and C their element size.  L * R * K and L * N * R may
- *   pass 2^31.  No workspace.
+ *   pass 2^31.  C in the place of another input than base is refused (QW_ERR_INVALID_ARG).  No
+ *   workspace.
  */
 qw_status qgemm_lora(const void* X, int64_t ldx, const void* A, const void* B, const float* scales,
                      const int32_t* ranks, int32_t L, int32_t R, const int32_t* ids,

@@ -595,6 +595,8 @@ qw_status qgemm_lora(const void* X, int64_t ldx, const void* A, const void* B, c
   if (!aligned(X, 16) || ldx % 8 || !aligned(A, 16) || !aligned(B, 16) || !aligned(scales, 4) ||
       !aligned(ranks, 4) || !aligned(ids, 4) || !aligned(base, size) || !aligned(C, size))
     return QW_ERR_ALIGNMENT;
+  // (clusters that are done with K write columns of C while others still read)
+  if (C == X || C == A || C == B || C == scales || C == ranks || C == ids) return QW_ERR_INVALID_ARG;
   const LoraArgs a{static_cast<const uint16_t*>(X), ldx, static_cast<const uint16_t*>(A),
                    static_cast<const uint16_t*>(B), scales, ranks, L, R, ids, base, ld_base, C, ldc,
                    M, N, K, d_err};
