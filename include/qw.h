@@ -504,7 +504,8 @@ qw_status qw_logprobs(int32_t l_type, const void* logits, int64_t ld, int64_t T,
  *   q_fmt: what else is made of y, from its FP32 values:
  *     QW_A_BF16        nothing (Q and Q_sf NULL);
  *     QW_A_INT8_TOKEN  Q INT8 [rows][K], Q_sf FP32 [rows]: scale max|y| / 127, codes
- *                      rint(y * (127 / max|y|)), ties to even (max|y| below 2^-119: codes 0);
+ *                      rint(y * (127 / max|y|)), ties to even (as qw_quantize_int8: max|y| below
+ *                      2^-126: codes 0);
  *     QW_A_MXFP8_G32   Q E4M3 [rows][K], Q_sf E8M0 [rows][K/32], as qw_quantize_mxfp8.
  *   FP32 arithmetic; |w_offset + W| below 2^64.  A row with a non-finite h sets QW_ERR_VALUE in
  *   d_err; its y is NaN, its INT8 scale NaN with codes 0, its E8M0 scales 0xFF with codes 0.

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(threads_of(FORM), FORM == ROWS_WARP ? 6 : 1)
     };
     auto weight = [&](int v, int i) { return MANY ? weights[MANY ? v : 0] : w[i]; };
     uint16_t* yr = a.Y ? static_cast<uint16_t*>(a.Y) + row * a.ldy : nullptr;
-    float inv = 0.f, scale = 0.f;
+    float inv = 0.f, scale = 0.f, down = 1.f;
     bool bad = pre != pre;
     if constexpr (QF == Q_INT8) {
       float top = 0.f;
@@ -312,19 +312,35 @@ __global__ void __launch_bounds__(threads_of(FORM), FORM == ROWS_WARP ? 6 : 1)
       top = reduce.top(top);
       bad = bad || !(top < INFINITY);
       scale = bad ? __uint_as_float(0x7FC00000u) : top / 127.f;
-      inv = bad || top < FLT_MIN * 128.f ? 0.f : 127.f / top;
+      inv = bad || top < FLT_MIN ? 0.f : 127.f / top;
+      // Below 2^-121 the quotient passes FP32: such a row is taken times 2^64, which is exact.  (A factor in all
+      // rows: 8192 x 4096 38.4 us instead of 37.6.)  A row without a normal number has codes 0.
+      if (top < 0x1p-119f) {
+        down = 0x1p-64f;
+        if (top >= FLT_MIN) inv = 127.f / (top * 0x1p64f);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[v][j] *= 0x1p64f;
+      }
     }
     auto put8 = [&](int i, const float (&y)[8]) {
-      if (yr) reinterpret_cast<uint4*>(yr)[i] = pack8(y);
+      if (yr) {
+        float z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = QF == Q_INT8 ? y[j] * down : y[j];
+        reinterpret_cast<uint4*>(yr)[i] = pack8(z);
+      }
       if constexpr (QF == Q_INT8) {
         // adding 1.5 * 2^23 rounds to an integer, ties to even, in the sum's low bits
         uint32_t q[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          q[j] = bad ? 0u : __float_as_uint(__fadd_rn(__fmul_rn(y[j], inv), 12582912.f));
+          q[j] = __float_as_uint(__fadd_rn(__fmul_rn(y[j], inv), 12582912.f));
         uint2 o;
         o.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
         o.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+        if (bad) o = make_uint2(0, 0);
         reinterpret_cast<uint2*>(a.Q)[row * n8 + i] = o;
       }
     };
@@ -371,6 +387,10 @@ __global__ void __launch_bounds__(threads_of(FORM), FORM == ROWS_WARP ? 6 : 1)
       const int i = i0 + me;
       float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (i < n8) tail8(i, y);
+      if (QF == Q_INT8 && down != 1.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= 0x1p64f;
+      }
       if constexpr (QF == Q_MXFP8)
         put8_mx(i, y, i < n8);
       else if (i < n8)
