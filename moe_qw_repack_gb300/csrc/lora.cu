@@ -223,7 +223,7 @@ struct Pass {
       v *= scale;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        const __nv_bfloat16 h = next_part(v, s == NS - 1);
         ts[(s * T + c) * pitch + r] = __bfloat16_as_ushort(h);
         v -= __bfloat162float(h);
       }

@@ -21,6 +21,13 @@ __device__ __forceinline__ uint4 first_of(uint4 v, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The next of the BF16 numbers that t is held as: t rounded, but none above BF16's largest number for a finite
+// t (the numbers after it have the rest; the last one gets what is infinite or NaN).
+__device__ __forceinline__ __nv_bfloat16 next_part(float t, bool last) {
+  constexpr float TOP = 0x1.FEp127f;
+  return __float2bfloat16_rn(last ? t : fminf(fmaxf(t, -TOP), TOP));
+}
+
 // A token's adapter and rank: -1 where it has none, or none that works (which sets the error).
 __device__ __forceinline__ int adapter_of(const LoraArgs& p, int64_t m, int& rank) {
   const int id = p.ids[m];

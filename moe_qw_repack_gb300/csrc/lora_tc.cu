@@ -175,7 +175,7 @@ __device__ __forceinline__ void put_t(uint8_t* at, int r_slots, int token, int r
     __nv_bfloat16 h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      h[i] = __float2bfloat16_rn(w[i]);
+      h[i] = next_part(w[i], s == NS - 1);
       w[i] -= __bfloat162float(h[i]);
     }
     *reinterpret_cast<uint2*>(to + s * r_slots * SLOT) =
