@@ -60,3 +60,75 @@ def test_t_above_the_largest_bf16_number(M, N, K, c):
     got = call(x, a, b, c)
     assert bool((got[0] != got[0]).logical_or(got[0].isinf()).all())
     assert torch.equal(got[1:], want[1:].to(TYPES[c]))
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("scale", [None, 0.25])
+def test_three_parts_for_fp32_results(M, N, K, scale):
+    """t = 1 + 2^-9 + 2^-18, one bit in each of three BF16 numbers (two would lose the last): sums of 19 bits, which
+    neither cut nor round, so the results are exact."""
+    R = 24
+    x, a, b, ks, r_of, g = sparse(M, N, K, R, M + 1)
+    x[:, ks] = 1
+    a[0, :, ks[0]], a[0, :, ks[1]], a[0, :, ks[2]] = 1, 2.0 ** -9, 2.0 ** -18
+    power = torch.exp2(torch.randint(-3, 4, (N,), generator=g, device="cuda").double())
+    b[0, torch.arange(N, device="cuda"), r_of] = power
+    base = -power.expand(M, N)
+    t = (1 + 2.0 ** -9 + 2.0 ** -18) * (scale or 1.0)
+    assert torch.equal(call(x, a, b, "f32", None, scale).double(), (t * power).expand(M, N))
+    assert torch.equal(call(x, a, b, "f32", base, scale).double(), t * power + base)
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_all_bits_of_t_for_fp32_results(M, N, K):
+    """t of 24 random bits out of three products (of 8 bits each: 1.xxxxxxx, and the next ones 2^-8 and 2^-16 of
+    that).  A tensor core may cut each number of a sum to FP32's 24 bits of the largest, 2^-23: four numbers to make
+    t, two in each of the two sums that join its parts.  FP32 additions round, 2^-24: two for a cluster's slices, and
+    the result.  10 * 2^-23 in all; without t's third part it would be up to 2^-17."""
+    R = 24
+    x, a, b, ks, r_of, g = sparse(M, N, K, R, M + 2)
+    bits = torch.randint(0, 128, (3, R), generator=g, device="cuda").double() / 128 + 1
+    x[:, ks] = 1
+    for i in range(3):
+        a[0, :, ks[i]] = bits[i] * 2.0 ** (-8 * i)
+    b[0, torch.arange(N, device="cuda"), r_of] = 1
+    want = a[0][:, ks].sum(dim=1)[r_of].expand(M, N)
+    off = (call(x, a, b, "f32").double() - want).abs() / want
+    assert float(off.max()) <= 10 * 2.0 ** -23, float(off.max() * 2.0 ** 23)
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_two_parts_for_bf16_results(M, N, K):
+    """16 bits of t are exact (1 + 2^-9 + 2^-16, of which base leaves the last two), and of 19 bits no more than
+    2^-17 t is lost beside the result's rounding."""
+    R = 24
+    x, a, b, ks, r_of, g = sparse(M, N, K, R, M + 3)
+    x[:, ks] = 1
+    power = torch.exp2(torch.randint(-3, 4, (N,), generator=g, device="cuda").double())
+    b[0, torch.arange(N, device="cuda"), r_of] = power
+    base = -power.expand(M, N)
+    a[0, :, ks[0]], a[0, :, ks[1]], a[0, :, ks[2]] = 1, 2.0 ** -9, 2.0 ** -16
+    want = (2.0 ** -9 + 2.0 ** -16) * power.expand(M, N)
+    assert torch.equal(call(x, a, b, "bf16", base).double(), want)
+    a[0, :, ks[2]] = 2.0 ** -18
+    want = (2.0 ** -9 + 2.0 ** -18) * power.expand(M, N)
+    off = (call(x, a, b, "bf16", base).double() - want).abs()
+    assert bool((off <= 2.0 ** -17 * (1 + 2.0 ** -8) * power + 2.0 ** -8 * want).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 200, 4096), (64, 520, 2048), (200, 1032, 4096), (1100, 392, 1040)])
+@pytest.mark.parametrize("c", ["bf16", "f32"])
+def test_small_whole_numbers(M, N, K, c):
+    """x and a of -1, 0 and 1, b of one -1 or 1 in eight: |t| <= 4096 takes 13 bits, which two parts hold, sums stay
+    below 2^24, so FP32 results are exact and BF16 ones rounded once."""
+    R = 64
+    g = torch.Generator(device="cuda").manual_seed(M)
+
+    def draw(*shape):
+        return torch.randint(-1, 2, shape, generator=g, device="cuda").double()
+    x, a = draw(M, K), draw(1, R, K)
+    b = draw(1, N, R) * (torch.rand((1, N, R), generator=g, device="cuda") < 0.125)
+    base = torch.randint(-100, 101, (M, N), generator=g, device="cuda").double()
+    want = base + (x @ a[0].t()) @ b[0].t()
+    assert float(want.abs().max()) < 2 ** 24
+    assert torch.equal(call(x, a, b, c, base), want.float().to(TYPES[c]))
