@@ -117,8 +117,10 @@ typedef enum qw_rope_method {
   QW_ROPE_NONE = 0,
   QW_ROPE_LINEAR = 1,      /* every frequency / factor (position interpolation)            */
   QW_ROPE_NTK = 2,         /* base * factor^(rot_dim / (rot_dim - 2))                      */
-  QW_ROPE_YARN = 3,        /* by bands, and attention 0.1 ln(factor) + 1                   */
-  QW_ROPE_BANDS = 4        /* slow frequencies / factor, fast ones kept, between them mixed */
+  QW_ROPE_YARN = 3,        /* by bands mixed by turns, and attention 0.1 ln(factor) + 1    */
+  QW_ROPE_BANDS = 4,       /* slow frequencies / factor, fast ones kept, between them mixed */
+  QW_ROPE_YARN_INDEX = 5   /* as QW_ROPE_YARN, mixed by the pair's index: models whose     */
+                           /* configuration names YaRN were trained and are run with this  */
 } qw_rope_method;
 
 /* Description of one repacked weight set (E experts; E = 1 for a dense layer).
@@ -554,9 +556,15 @@ qw_status qgemm_lora(const void* X, int64_t ldx, const void* A, const void* B, c
  *
  * qw_rope_frequencies - the freqs of qw_rope, on the host (freqs: host double [rot_dim / 2]; attention:
  *   host float, the `scale` of qw_rope): base^(-2 j / rot_dim), for longer contexts changed by `method`
- *   with factor >= 1.  The two by bands take f * (k + (1 - k) / factor) with
- *   k = clamp((original f / 2 pi - low) / (high - low), 0, 1): frequencies of over `high` turns in
- *   the `original` length are kept, those of under `low` are stretched.
+ *   with factor >= 1.  Those by bands take f * (k + (1 - k) / factor): frequencies of over `high` turns in
+ *   the `original` length are kept, those of under `low` are stretched.  Between them
+ *     QW_ROPE_YARN, QW_ROPE_BANDS   k = clamp((original f / 2 pi - low) / (high - low), 0, 1)
+ *     QW_ROPE_YARN_INDEX            k = 1 - clamp((j - first) / (last - first), 0, 1), where
+ *       first = max(floor(i(high)), 0), last = min(ceil(i(low)), rot_dim - 1) and
+ *       i(n) = rot_dim ln(original / (2 pi n)) / (2 ln base), the index of a pair of n turns (last no more
+ *       than first: the pairs behind `first` are stretched).
+ *   The method's paper gives the first form under its name, its released code and the models that were
+ *   made with that the second; they differ by up to 3 times at 16 times a length of 4096.
  */
 qw_status qw_rope(int32_t type, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t T,
                   int32_t heads, int32_t head_dim, int32_t rot_dim, int32_t layout,

@@ -606,12 +606,12 @@ qw_status qgemm_lora(const void* X, int64_t ldx, const void* A, const void* B, c
 qw_status qw_rope_frequencies(int32_t method, double base, int32_t rot_dim, double factor,
                               double original, double low, double high, double* freqs,
                               float* attention) {
-  if (method < QW_ROPE_NONE || method > QW_ROPE_BANDS) return QW_ERR_UNSUPPORTED;
+  if (method < QW_ROPE_NONE || method > QW_ROPE_YARN_INDEX) return QW_ERR_UNSUPPORTED;
   if (!freqs || !attention || rot_dim < 2 || rot_dim % 2 || rot_dim > kRopeMaxDim)
     return QW_ERR_INVALID_ARG;
   if (!(base > 1.0 && base <= 1e30)) return QW_ERR_INVALID_ARG;
   if (method != QW_ROPE_NONE && !(factor >= 1.0 && factor <= 1e9)) return QW_ERR_INVALID_ARG;
-  if ((method == QW_ROPE_YARN || method == QW_ROPE_BANDS) &&
+  if ((method == QW_ROPE_YARN || method == QW_ROPE_BANDS || method == QW_ROPE_YARN_INDEX) &&
       !(original > 0.0 && original <= 1e18 && low >= 0.0 && high > low && high <= 1e18))
     return QW_ERR_INVALID_ARG;
   return rope_frequencies(method, base, rot_dim, factor, original, low, high, freqs, attention);

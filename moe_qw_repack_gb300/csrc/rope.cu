@@ -255,18 +255,28 @@ qw_status rope_frequencies(int32_t method, double base, int32_t rot, double fact
                            double low, double high, double* freqs, float* attention) {
   const double two_pi = 6.283185307179586;
   if (method == QW_ROPE_NTK && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+  // mixed by index: the last pair that is kept, the first that is stretched as a whole
+  auto pair_of = [&](double turns) { return rot * std::log(original / (two_pi * turns)) / (2.0 * std::log(base)); };
+  double first = 0.0, last = 0.0;
+  if (method == QW_ROPE_YARN_INDEX) {
+    first = std::fmax(std::floor(pair_of(high)), 0.0);
+    last = std::fmin(std::ceil(pair_of(low)), rot - 1.0);  // (low 0: no pair is that slow)
+  }
   for (int j = 0; j < rot / 2; ++j) {
     double f = std::pow(base, -2.0 * j / rot);
     if (method == QW_ROPE_LINEAR) f /= factor;
+    double keep = 1.0;
     if (method == QW_ROPE_YARN || method == QW_ROPE_BANDS) {
       // turns within the original length: over `high` kept, under `low` stretched, between them mixed
       const double turns = original * f / two_pi;
-      const double keep = std::fmin(1.0, std::fmax(0.0, (turns - low) / (high - low)));
-      f = f * (keep + (1.0 - keep) / factor);
+      keep = std::fmin(1.0, std::fmax(0.0, (turns - low) / (high - low)));
+    } else if (method == QW_ROPE_YARN_INDEX) {
+      keep = j <= first ? 1.0 : j >= last ? 0.0 : 1.0 - (j - first) / (last - first);
     }
+    if (keep < 1.0) f = f * (keep + (1.0 - keep) / factor);
     freqs[j] = f;
   }
-  *attention = method == QW_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  *attention = method == QW_ROPE_YARN || method == QW_ROPE_YARN_INDEX ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
   return QW_OK;
 }
 

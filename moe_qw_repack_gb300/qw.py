@@ -49,6 +49,7 @@ QW_ROPE_LINEAR = 1
 QW_ROPE_NTK = 2
 QW_ROPE_YARN = 3
 QW_ROPE_BANDS = 4
+QW_ROPE_YARN_INDEX = 5
 
 EXPORTS = (
     "qw_status_str", "qw_version", "qw_repack_query", "qw_repack", "qw_unpack",
@@ -365,7 +366,8 @@ def qw_rope(type, X, ldx, Y, ldy, T, heads, head_dim, rot_dim, layout, positions
 
 
 def qw_rope_frequencies(method, base, rot_dim, factor=1.0, original=0.0, low=1.0, high=32.0):
-    """(frequencies, attention): FP64 tensor [rot_dim / 2] on the host, and qw_rope's ``scale``."""
+    """(frequencies, attention): FP64 tensor [rot_dim / 2] on the host, and qw_rope's ``scale``.  Models whose
+    configuration names YaRN take QW_ROPE_YARN_INDEX."""
     freqs = torch.empty(max(rot_dim, 2) // 2, dtype=torch.float64)
     attention = _F32(1.0)
     _check("qw_rope_frequencies", LIB.qw_rope_frequencies(
