@@ -1004,9 +1004,10 @@ __global__ void __launch_bounds__(640, 1)  // (registers as for 20 warps: they a
     for (int i = copier + copiers * warp; i < win; i += copiers * WARPS)
       if (plan.ids[i] == -1) copy_row<C32>(a, WIDE, m0 + i, n0, n1);
   }
-  // After a wait that gave up, copies may still be under way to the rings: they have this long.
+  // After a wait that gave up, copies may still be under way to the rings, some on barriers that will never have all
+  // their arrivals: they have as long as any wait.
   if (*abort_flag && threadIdx.x == 0)
-    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < kWaitLimitNs / 100;) {
+    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < kWaitLimitNs;) {
     }
   __syncwarp();
   if (warp == 1) {  // (after a wait that gave up, MMAs may still run)
