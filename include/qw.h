@@ -528,8 +528,10 @@ qw_status qw_rmsnorm(int32_t x_type, const void* X, int64_t ldx, int32_t r_type,
  *   behind may be anything).  A token whose A x or result is not finite leaves the others alone.  scales:
  *   FP32 [L] or NULL (1).  base: c_type, row pitch ld_base, or NULL (0); may be C with the same
  *   pitch, which adds to a projection's output in place (rows without adapter are then not
- *   touched).  C: c_type QW_T_BF16 or QW_T_F32, row pitch ldc >= N, rounded once.  Products and sums
- *   in FP32.
+ *   touched).  C: c_type QW_T_BF16 or QW_T_F32, row pitch ldc >= N, rounded once.  Sums in FP32 (a tensor
+ *   core's, which may cut instead of round).  Between the products A x, times its scale, keeps 24 bits for
+ *   FP32 results and 16 for BF16 ones: these are off by up to 2^-17 |B| |s A x| beside their own rounding,
+ *   which shows where base or B's signs cancel nearly all of it.
  *   An id outside [-1, L) or a rank outside [0, R] sets QW_ERR_INVALID_ARG in d_err; the token is
  *   then taken as one without adapter.
  *   K % 8 == 0, R % 8 == 0, R <= 256, M <= 2^26, N and K <= 2^30 (else QW_ERR_UNSUPPORTED).  X, A, B

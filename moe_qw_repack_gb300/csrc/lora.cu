@@ -9,8 +9,8 @@
 // the weights' rows as the other: a lone token costs its adapter's bytes and little else.  A group is
 // worked on by a cluster: its CTAs take slices of K for t, leave them in shared memory, add them up in
 // rank order, and take slices of N for the second product.  So t never leaves the SMs.
-// t is held as a sum of BF16 numbers for the second product: two for BF16 results (2^-17 t is lost
-// of what the result rounds to 2^-9), three for FP32 ones (all 24 bits).
+// t is held as a sum of BF16 numbers for the second product: two for BF16 results (up to 2^-17 t is lost, where
+// the result is rounded by up to 2^-8 of itself), three for FP32 ones (all 24 bits).
 // The order of k and r within an MMA is free as long as both operands have the same: a lane reads 16
 // bytes of a row at once, two MMAs' share.  In the second product row 4 g + i of 32 belongs to the lanes
 // of group g, so that a lane ends with four neighbouring columns of a token.
@@ -492,7 +492,8 @@ qw_status launch_lora(const LoraArgs& a, bool c_f32, cudaStream_t st) {
   // be one adapter's (us here and there, K = 4096: 32 tokens of one adapter, N = 4096, rank 64 22, 13; of two,
   // N = 14336, rank 16 17, 15; 96 of 8, N = 4096, rank 16 12, 13; 128 of 8, N = 14336, rank 64 27, 24; 192 of 32,
   // N = 4096, rank 32 27, 20; 192 of 64, rank 64 46, 34; 256 of 300, rank 16 52, 90 and 512 98, 93; 4096 of 8 in
-  // runs, N = 14336, rank 64 277, 59).
+  // runs, N = 14336, rank 64 277, 61).  L is what is loaded, the ids are on the device: in all of these a call meets
+  // about as many.  Of one adapter out of 300, N = 4096, rank 64, 128 tokens take 47 here, out of one 14 there.
   const bool many = a.M > 512 || (a.M > 128 && a.M > 2 * (int64_t)a.L) || (a.M > 16 && a.M > 12 * (int64_t)a.L);
   if (many && lora_tc_takes(a, c_f32)) return launch_lora_tc(a, c_f32, st);
   if (lora_wide(a, c_f32)) return c_f32 ? launch<true, true>(a, st) : launch<false, true>(a, st);

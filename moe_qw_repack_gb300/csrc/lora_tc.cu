@@ -13,9 +13,9 @@
 //      fence waits for all of its thread's copies, also those of later stages (0.65 us a stage).
 //   2  t = s_a (sum of the CTAs' D1, in rank order): each CTA fetches its tokens' shares, adds them up
 //      and leaves its tokens' t, which the others fetch; all reads of 256 bytes in a row.  t is held as
-//      BF16 numbers that add up to it, two where results are BF16 (2^-17 t is lost of what the result
-//      rounds to 2^-9), three for FP32 ones (24 bits), and lands as the second product's operand: it
-//      never leaves the SMs.
+//      BF16 numbers that add up to it, two where results are BF16 (up to 2^-17 t is lost, where the result
+//      is rounded by up to 2^-8 of itself), three for FP32 ones (24 bits), and lands as the second product's
+//      operand: it never leaves the SMs.
 //   3  D2[token][n] = t B^T for 128 columns at a time of the CTA's slice of N.  An epilogue warp takes
 //      32 tokens (a lane holds a token, a register a column) and a share of the columns: base into
 //      shared memory, D2 added to it there, and out to C.  32 tokens that stand together in the call
@@ -29,7 +29,7 @@
 // Bound by: an item's chain (list 2, X A^T and t 6 to 10, 2 us a tile and group) in small calls; in large ones
 // by L2 while all SMs read X and A, where DRAM has little to do (17 us of 4096 x 14336 x 4096, rank 64, with a CTA
 // on all of K, 6 with three and 5 to join), then by base and C through shared memory, on 123 of 152 SMs there:
-// 59 us, 288 MB at 4.9 TB/s in all.
+// 61 us, 288 MB at 4.7 TB/s in all (mean of 40 inputs, 56 to 70 by where runs begin and meet).
 #include <algorithm>
 
 #include "int8_map.cuh"
